@@ -57,7 +57,7 @@
 extern "C" {
 #endif
 
-#define SSU_ABI_VERSION 4
+#define SSU_ABI_VERSION 5
 
 #ifndef SSU_API
 #define SSU_API __attribute__((visibility("default")))
@@ -449,6 +449,115 @@ SSU_API ssu_status_t ssu_ssd_plan(const ssu_ssd_plan_desc_t *desc, ssu_ssd_plan_
  * stream are ordered. Nothing in the array needs clearing between calls. */
 #define SSU_SSD_SCRATCH_BYTES (64ll << 20)
 SSU_API ssu_status_t ssu_ssd_prefill_noalloc(const ssu_ssd_args_t *args, void *stream);
+
+/* ---- The layer around the state update: norm, projections, answers.
+ * A Mamba-2 decode step runs x -> RMS norm -> input projection -> state
+ * update -> gated RMS norm -> output projection, and its last layer's logits
+ * become log probabilities of the drafted tokens. The entry points below
+ * follow the conventions above: caller-owned device memory, no allocation,
+ * asynchronous on `stream`, nothing device-resident read on the host. */
+
+/* Number formats of an operator's 8- or 4-bit operand. MXFP8 and MXFP4 as
+ * above (E4M3 / E2M1 elements, an E8M0 scale byte per 32 consecutive values
+ * of a row, e - 127 = floor(log2 max|v|) - 8 or - 2 clamped to [-126, 127]),
+ * except that values which are not finite reach the result: a block holding
+ * an infinity or a NaN takes the scale byte 0xFF (E8M0's NaN) and zero codes,
+ * and stands for 32 NaNs. */
+typedef enum { SSU_FORMAT_SAME = 0, SSU_FORMAT_MXFP4 = 4, SSU_FORMAT_MXFP8 = 8 } ssu_format_t;
+
+/* Gated, residual-adding RMS norm over `groups` equal parts of each row:
+ *   v = x * silu(gate)                  (x without a gate)
+ *   u = v + residual                    (v without a residual)
+ *   residual_out = u, rounded once to its dtype
+ *   out = u * rsqrt(mean over the part of u^2 + eps) * weight
+ * in fp32 from the unrounded u, rounded once to x's dtype or quantised.
+ *   x, gate         [rows, dim], f32 / f16 / bf16, last stride 1
+ *   weight          [dim], x dtype or f32, stride 1
+ *   residual, residual_out  [rows, dim], both x dtype or both f32, last
+ *                   stride 1; both or neither; may be the same memory
+ *   out             SSU_FORMAT_SAME: [rows, dim], x dtype, last stride 1 (may be
+ *                   x itself). MXFP8: u8 codes [rows, dim]; MXFP4: u8 code pairs
+ *                   [rows, dim / 2], both contiguous and 8-byte aligned, dim /
+ *                   groups a multiple of 32
+ *   out_scales      u8 [rows, dim / 32], contiguous (the MX formats only)
+ * Other overlap of an output with an input is undefined. One kernel. */
+typedef struct {
+    ssu_tensor_t x, weight, residual, gate;
+    ssu_tensor_t out, out_scales, residual_out;
+    int64_t groups;
+    float eps;
+    int32_t out_format; /* ssu_format_t */
+} ssu_norm_args_t;
+
+SSU_API ssu_status_t ssu_add_rms_norm(const ssu_norm_args_t *args, void *stream);
+
+/* Quantise rows to MXFP8 or MXFP4 (weights once, activations on the way to
+ * ssu_mx_linear).
+ *   src     [rows, k], f32 / f16 / bf16, last stride 1, k a multiple of 32
+ *   codes   u8 [rows, k] (MXFP8) or [rows, k / 2] (MXFP4), contiguous, 8-byte aligned
+ *   scales  u8 [rows, k / 32], contiguous
+ * One kernel. */
+SSU_API ssu_status_t ssu_mx_quantize(const ssu_tensor_t *src, const ssu_tensor_t *codes,
+                                     const ssu_tensor_t *scales, int32_t format, void *stream);
+
+/* Product with MXFP4 weights: out = a w^T + bias, accumulated in fp32 on the
+ * matrix cores' block-scaled instructions and rounded once.
+ *   x        the activations a: f32 / f16 / bf16 [m, k], last stride 1, which
+ *            the call quantises to x_format; or u8 codes of that format
+ *            ([m, k] or [m, k / 2]) with x_scale u8 [m, k / 32]
+ *   w        u8 MXFP4 code pairs [n, k / 2]; w_scale u8 [n, k / 32]
+ *   bias     [n], f32 or the out dtype, stride 1, or absent
+ *   out      [m, n], f32 / f16 / bf16, last stride 1
+ *   x_format SSU_FORMAT_MXFP8 or SSU_FORMAT_MXFP4
+ * k is a multiple of 32. Codes have last stride 1, a 16-byte aligned base and
+ * row strides that are multiples of 16; scales have last stride 1. The
+ * E4M3 products of one instruction are added with about 13 bits below the
+ * largest of them, the E2M1 products exactly; between instructions sums are
+ * fp32. A NaN (an E4M3 code 0x7F / 0xFF or a scale byte 0xFF) reaches every
+ * sum it takes part in.
+ * `workspace`: DEVICE memory of at least ssu_mx_linear_workspace_bytes, 256-
+ * byte aligned, used during the call only (NULL where that is 0); two calls
+ * that overlap must not share one. */
+typedef struct {
+    ssu_tensor_t x, x_scale, w, w_scale, bias, out;
+    int32_t x_format; /* ssu_format_t */
+} ssu_mx_linear_args_t;
+
+SSU_API int64_t ssu_mx_linear_workspace_bytes(const ssu_mx_linear_args_t *args);
+SSU_API ssu_status_t ssu_mx_linear(const ssu_mx_linear_args_t *args, void *workspace,
+                                   int64_t workspace_bytes, void *stream);
+
+/* Log probabilities of given tokens, with entropy, rank and the top
+ * alternatives. For every row, over its allowed tokens (mask bit set, logit
+ * above -inf), l = logits / temperature and p = softmax(l):
+ *   logprob      log p[token]; -inf for a token that is not allowed or outside
+ *                [0, vocab)
+ *   entropy      -sum p log p
+ *   rank         how many allowed tokens stand before the token (larger logit,
+ *                or an equal one at a lower index); -1 where logprob is -inf
+ *   top_tokens, top_logprobs  the first `top` tokens in that order and their
+ *                log p; -1 and -inf where fewer are allowed
+ * A row with no allowed token has logprob -inf and entropy 0. A NaN or +inf
+ * logit at a token that the mask allows makes the row's numbers NaN, its
+ * rank and tokens -1; what masked-out logits hold does not matter.
+ *   logits       [rows, vocab], f32 / f16 / bf16, last stride 1
+ *   tokens       [rows] i32 / i64
+ *   mask         [rows, ceil(vocab / 32)] i32, last stride 1 (row stride 0 shares
+ *                one mask): bit i of word j allows token 32 j + i; or absent
+ *   temperature  [rows] f32, above 0 (otherwise as a NaN logit), or absent
+ *   logprob, entropy  [rows] f32; rank [rows] i32; contiguous
+ *   top_tokens i32, top_logprobs f32 [rows, top], contiguous, top <=
+ *                SSU_TOP_MAX; both or neither
+ * `workspace` as for ssu_mx_linear. */
+#define SSU_TOP_MAX 32
+typedef struct {
+    ssu_tensor_t logits, tokens, mask, temperature;
+    ssu_tensor_t logprob, entropy, rank, top_tokens, top_logprobs;
+} ssu_logprob_args_t;
+
+SSU_API int64_t ssu_token_logprobs_workspace_bytes(const ssu_logprob_args_t *args);
+SSU_API ssu_status_t ssu_token_logprobs(const ssu_logprob_args_t *args, void *workspace,
+                                        int64_t workspace_bytes, void *stream);
 
 /* Message of the last failing call on this thread ("" if none). The pointer
  * stays valid until the next call on the same thread. */

@@ -10,12 +10,15 @@ LIB = os.path.join(HERE, "libssu.so")
 SOURCES = [os.path.join(CSRC, "ssu_kernels.hip"), os.path.join(CSRC, "ssu_replay.hip"),
            os.path.join(CSRC, "ssu_copy.hip"),
            os.path.join(CSRC, "ssu_ssd.hip"), os.path.join(CSRC, "ssu_noalloc.hip"),
-           os.path.join(CSRC, "ssu_api.cpp")]
+           os.path.join(CSRC, "ssu_norm.hip"), os.path.join(CSRC, "ssu_mx.hip"),
+           os.path.join(CSRC, "ssu_logprob.hip"),
+           os.path.join(CSRC, "ssu_api.cpp"), os.path.join(CSRC, "ssu_layer_api.cpp")]
 # Streaming-ceiling kernels for the benchmark (a separate library, not part
 # of libssu's interface).
 CEILING_SRC = os.path.join(CSRC, "ssu_ceiling.hip")
 CEILING_LIB = os.path.join(HERE, "libssu_ceiling.so")
 HEADERS = [os.path.join(CSRC, "ssu_internal.h"), os.path.join(CSRC, "ssu_device.h"),
+           os.path.join(CSRC, "ssu_layer.h"), os.path.join(CSRC, "ssu_layer_device.h"),
            os.path.join(os.path.dirname(HERE), "include", "ssu.h")]
 
 # Packed-fp32 instructions are switched off for all device code; hipcc -O3

@@ -1,0 +1,54 @@
+// Internal interface between the host entry points of the layer operators
+// (ssu_layer_api.cpp) and their gfx950 kernels (ssu_norm.hip, ssu_mx.hip,
+// ssu_logprob.hip).
+#pragma once
+
+#include <stdint.h>
+
+#include "../../include/ssu.h"
+
+namespace ssu {
+
+// RMS norm. Strides are in elements; a "part" is one group of one row.
+struct NormParams {
+    const void *x, *weight, *residual, *gate;  // residual, gate may be null
+    void *out, *residual_out;
+    uint8_t *scales;  // MX outputs
+    int64_t x_s, res_s, gate_s, out_s, res_out_s;
+    int64_t parts;  // rows * groups
+    int32_t groups, part;  // groups per row, elements per part
+    int32_t weight_f32, res_f32;
+    float eps;
+};
+int launch_norm(const NormParams &p, int dtype, int format, void *stream);
+
+// Rows to MXFP8 / MXFP4: `blocks` = k / 32 per row; codes and scales contiguous.
+int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t rows, int64_t k, uint8_t *codes,
+                            uint8_t *scales, int format, void *stream);
+
+// Product with MXFP4 weights. Strides: codes and scales in bytes, out in
+// elements.
+struct MxParams {
+    const uint8_t *a, *a_scale, *w, *w_scale;
+    const void *bias;  // may be null
+    void *out;
+    int64_t a_s, as_s, w_s, ws_s, out_s;
+    int32_t m, n, k;
+    int32_t bias_f32;
+};
+int launch_mx_linear(const MxParams &p, int format, int out_dtype, void *stream);
+
+// Token log probabilities. Strides in elements.
+struct LogprobParams {
+    const void *logits, *tokens;
+    const int32_t *mask;       // may be null
+    const float *temperature;  // may be null
+    float *logprob, *entropy, *top_logprobs;
+    int32_t *rank, *top_tokens;
+    int64_t logits_s, tokens_s, mask_s, temp_s;
+    int64_t rows;
+    int32_t vocab, top, tokens_i64;
+};
+int launch_logprobs(const LogprobParams &p, int dtype, void *stream);
+
+}  // namespace ssu

@@ -1,0 +1,89 @@
+// Device helpers shared by the layer operators' kernels: rows read eight
+// elements at a time, and eight fp32 values to their MX codes.
+#pragma once
+
+#include "ssu_device.h"
+#include "ssu_layer.h"
+
+namespace ssu {
+namespace {
+
+// Eight consecutive elements at any element-aligned address: gfx950's global
+// loads take unaligned addresses, so one 16-byte (f32: two) access serves
+// every row stride.
+template <typename T>
+__device__ __forceinline__ void load8(const T *src, float v[8]) {
+    typedef T Vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+    const Vec r = *reinterpret_cast<const Vec *>(src);
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        v[i] = widen(r[i]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *dst, const float v[8]) {
+    typedef T Vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+    Vec r;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        r[i] = narrow<T>(v[i]);
+    *reinterpret_cast<Vec *>(dst) = r;
+}
+
+// The first `n` (up to 8) of them, zeros after.
+template <typename T>
+__device__ __forceinline__ void load8(const T *src, int n, float v[8]) {
+    if (n >= 8)
+        return load8(src, v);
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        v[i] = i < n ? widen(src[i]) : 0.0f;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *dst, int n, const float v[8]) {
+    if (n >= 8)
+        return store8(dst, v);
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        if (i < n)
+            dst[i] = narrow<T>(v[i]);
+}
+
+// Four consecutive lanes hold a block of 32 values, eight each; every lane
+// gives the codes of its eight (MXFP8: two words, MXFP4: the first) and the
+// block's scale byte. The largest magnitude is taken over the bit patterns, where
+// infinities and NaNs are the largest: such a block takes the scale byte
+// 0xFF and zero codes. All four lanes must be active.
+template <int FORMAT>
+__device__ __forceinline__ uint32_t mx_block(const float v[8], uint32_t code[2]) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    a = max(a, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(a), 0xB1, 0xF, 0xF, false)));
+    a = max(a, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(a), 0x4E, 0xF, 0xF, false)));
+    const float amax = __uint_as_float(a);
+    const int k = FORMAT == SSU_FORMAT_MXFP8 ? mx8_exponent(amax) : mx4_exponent(amax);
+    if constexpr (FORMAT == SSU_FORMAT_MXFP8) {
+        code[0] = e4m3_codes4(v, k);
+        code[1] = e4m3_codes4(v + 4, k);
+    } else {
+        code[0] = e2m1_codes4(v, k) | (e2m1_codes4(v + 4, k) << 16);
+        code[1] = 0;
+    }
+    const bool finite = a < 0x7F800000u;
+    code[0] = finite ? code[0] : 0;
+    code[1] = finite ? code[1] : 0;
+    return finite ? static_cast<uint32_t>(k + 127) : 0xFFu;
+}
+
+// Stores a lane's eight codes; `at` is its first value's index in the row.
+template <int FORMAT>
+__device__ __forceinline__ void store_codes(uint8_t *row, int64_t at, const uint32_t code[2]) {
+    if constexpr (FORMAT == SSU_FORMAT_MXFP8)
+        *reinterpret_cast<u32x2 *>(row + at) = u32x2{code[0], code[1]};
+    else
+        *reinterpret_cast<uint32_t *>(row + at / 2) = code[0];
+}
+
+}  // namespace
+}  // namespace ssu

@@ -94,7 +94,10 @@ class SsuPlanInfo(ctypes.Structure):
 EXPORTS = ("ssu_plan", "ssu_update", "ssu_replay_update", "ssu_replay_spec_update",
            "ssu_replay_lp_update", "ssu_mx8_quantize", "ssu_replay_mx4_update", "ssu_mx4_quantize",
            "ssu_batch_memcpy", "ssu_conv_state_shift", "ssu_ssd_workspace_bytes", "ssu_ssd_prefill",
-           "ssu_ssd_prefill_noalloc", "ssu_ssd_plan", "ssu_last_error", "ssu_abi_version")
+           "ssu_ssd_prefill_noalloc", "ssu_ssd_plan", "ssu_last_error", "ssu_abi_version",
+           # bound in layer.py
+           "ssu_add_rms_norm", "ssu_mx_quantize", "ssu_mx_linear", "ssu_mx_linear_workspace_bytes",
+           "ssu_token_logprobs", "ssu_token_logprobs_workspace_bytes")
 SSD_SCRATCH_BYTES = 64 << 20  # SSU_SSD_SCRATCH_BYTES
 
 
