@@ -27,15 +27,24 @@ int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t 
                             uint8_t *scales, int format, void *stream);
 
 // Product with MXFP4 weights. Strides: codes and scales in bytes, out in
-// elements.
+// elements. Up to kMxRowsMax rows run in the streaming kernel, which reads
+// scales where they are (and quantises up to kMxFuseRows rows by itself); more rows run
+// in the tiled kernels, which take codes and scales packed in a workspace.
+constexpr int kMxRowsMax = 64;
+constexpr int kMxFuseRows = 4;
 struct MxParams {
+    const void *x;  // float activations, or null
     const uint8_t *a, *a_scale, *w, *w_scale;
     const void *bias;  // may be null
     void *out;
-    int64_t a_s, as_s, w_s, ws_s, out_s;
+    int64_t x_s, a_s, as_s, w_s, ws_s, out_s;
     int32_t m, n, k;
     int32_t bias_f32;
+    int32_t x_dtype;
+    uint8_t *workspace;
 };
+// Workspace bytes of a product whose activations come as floats or as codes.
+int64_t mx_linear_workspace(int64_t m, int64_t n, int64_t k, int format, bool floats);
 int launch_mx_linear(const MxParams &p, int format, int out_dtype, void *stream);
 
 // Token log probabilities. Strides in elements.

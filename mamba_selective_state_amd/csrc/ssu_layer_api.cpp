@@ -106,13 +106,6 @@ ssu_status_t mx_operand(const char *name, const ssu_tensor_t &codes, const ssu_t
     return SSU_OK;
 }
 
-// Bytes of the codes of a quantised [m, k], rounded up so that the scales
-// after them stay aligned.
-int64_t code_bytes(int64_t m, int64_t k, int format) {
-    const int64_t b = format == SSU_FORMAT_MXFP4 ? m * k / 2 : m * k;
-    return (b + 255) / 256 * 256;
-}
-
 }  // namespace
 
 extern "C" {
@@ -219,10 +212,9 @@ ssu_status_t ssu_mx_quantize(const ssu_tensor_t *src, const ssu_tensor_t *codes,
 }
 
 int64_t ssu_mx_linear_workspace_bytes(const ssu_mx_linear_args_t *a) {
-    if (!a || a->x.ndim != 2 || !is_float(a->x.dtype) || !mx_format(a->x_format))
+    if (!a || a->x.ndim != 2 || a->w.ndim != 2 || !mx_format(a->x_format))
         return 0;
-    const int64_t m = a->x.size[0], k = a->x.size[1];
-    return code_bytes(m, k, a->x_format) + m * (k / 32);
+    return ssu::mx_linear_workspace(a->x.size[0], a->w.size[0], a->w.size[1] * 2, a->x_format, is_float(a->x.dtype));
 }
 
 ssu_status_t ssu_mx_linear(const ssu_mx_linear_args_t *a, void *workspace, int64_t workspace_bytes, void *stream) {
@@ -240,12 +232,11 @@ ssu_status_t ssu_mx_linear(const ssu_mx_linear_args_t *a, void *workspace, int64
     ssu::MxParams p = {};
     if (ssu_status_t st = mx_operand("w", a->w, a->w_scale, n, k / 2, k, &p.w_s, &p.ws_s))
         return st;
-    int64_t x_s = 0;
-    const bool quantise = is_float(a->x.dtype);
-    if (quantise) {
+    const bool floats = is_float(a->x.dtype);
+    if (floats) {
         if (present(a->x_scale))
             return fail(SSU_ERR_VALUE, "x_scale belongs to u8 codes");
-        if (ssu_status_t st = matrix("x", a->x, m, k, false, &x_s))
+        if (ssu_status_t st = matrix("x", a->x, m, k, false, &p.x_s))
             return st;
     } else if (ssu_status_t st = mx_operand("x", a->x, a->x_scale, m, a->x_format == SSU_FORMAT_MXFP4 ? k / 2 : k, k,
                                             &p.a_s, &p.as_s)) {
@@ -263,20 +254,16 @@ ssu_status_t ssu_mx_linear(const ssu_mx_linear_args_t *a, void *workspace, int64
     }
     if (m == 0 || n == 0)
         return done(0);
-    p.a = static_cast<const uint8_t *>(a->x.data);
-    p.a_scale = static_cast<const uint8_t *>(a->x_scale.data);
-    if (quantise && k > 0) {
-        const int64_t need = ssu_mx_linear_workspace_bytes(a);
-        if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
-            return fail(SSU_ERR_VALUE, "workspace must be 256-byte aligned and hold %lld bytes", (long long)need);
-        uint8_t *codes = static_cast<uint8_t *>(workspace);
-        uint8_t *scales = codes + code_bytes(m, k, a->x_format);
-        if (int e = ssu::launch_mx_quantize_rows(a->x.data, a->x.dtype, x_s, m, k, codes, scales, a->x_format, stream))
-            return done(e);
-        p.a = codes;
-        p.a_scale = scales;
-        p.a_s = a->x_format == SSU_FORMAT_MXFP4 ? k / 2 : k;
-        p.as_s = k / 32;
+    const int64_t need = ssu_mx_linear_workspace_bytes(a);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return fail(SSU_ERR_VALUE, "workspace must be 256-byte aligned and hold %lld bytes", (long long)need);
+    p.workspace = static_cast<uint8_t *>(workspace);
+    if (floats) {
+        p.x = a->x.data;
+        p.x_dtype = a->x.dtype;
+    } else {
+        p.a = static_cast<const uint8_t *>(a->x.data);
+        p.a_scale = static_cast<const uint8_t *>(a->x_scale.data);
     }
     p.w = static_cast<const uint8_t *>(a->w.data);
     p.w_scale = static_cast<const uint8_t *>(a->w_scale.data);

@@ -1,11 +1,40 @@
 // Rows to MXFP8 / MXFP4 (ssu_mx_quantize) and the product of such rows with
 // MXFP4 weights (ssu_mx_linear) on the block-scaled matrix instructions.
+//
+// Operand layouts of those instructions (checked on the device): lane l of a
+// wave holds row r = l % R of its operand (R = 16 or 32) and k group g = l / R;
+// E2M1 codes: k = 32 g .. 32 g + 31 in four registers; E4M3 codes: k = 16 g ..
+// 16 g + 15 in the first four and as many, K / 2 further on, in the last four
+// (K: the instruction's depth); the scale byte, one of a register's four, is that
+// of k block g. The first operand's rows are the result's rows (register i of lane
+// l: row i % 4 + 8 (i / 4) + 4 (l / 32) with R = 32, i + 4 (l / 16) with R = 16), the
+// second operand's rows its columns (l % R). The weights go first: a lane then holds
+// four neighbouring outputs of one activation row.
+//
+// Which k block the instruction calls g is free as long as both operands and
+// both scales agree. The tiled kernel gives group h of step s the block STEPS h + s
+// of its K tile, so that one register holds a lane's scale bytes of all steps
+// and each step names its byte.
+#include <algorithm>
+
 #include "ssu_layer_device.h"
 
 namespace ssu {
 namespace {
 
 constexpr int kQuantThreads = 256;
+constexpr int kE4M3 = 0, kE2M1 = 4;  // the instructions' format numbers
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ i32x8 wide(i32x4 lo, i32x4 hi) {
+    return i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+}
+__device__ __forceinline__ i32x8 wide(i32x4 lo) { return i32x8{lo.x, lo.y, lo.z, lo.w, 0, 0, 0, 0}; }
+__device__ __forceinline__ i32x8 wide(i32x8 v) { return v; }
 
 // Four lanes per block of 32 values, eight each.
 template <typename T, int FORMAT>
@@ -27,73 +56,540 @@ __global__ __launch_bounds__(kQuantThreads) void mx_quantize_rows_kernel(const T
     }
 }
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-// One wave per 32 x 32 tile of the output; both operands straight from
-// memory. Operands of the 32x32x64 instruction (checked on the device): lane l
-// is row l % 32; E2M1 codes k = 32 (l / 32) + 0..31 in the first four
-// registers; E4M3 codes k = 16 (l / 32) + 0..15 in the first four and k = 32 +
-// 16 (l / 32) + 0..15 in the last; the scale byte of block l / 32.
-// Result: register i is row i % 4 + 8 (i / 4) + 4 (l / 32), column l % 32.
-template <typename OT, int FORMAT>
-__global__ __launch_bounds__(64) void mx_linear_kernel(const MxParams p) {
-    const int l = threadIdx.x, r = l % 32, h = l / 32;
-    const int m0 = static_cast<int>(blockIdx.y) * 32, n0 = static_cast<int>(blockIdx.x) * 32;
-    // rows past the end read the last row; their results are not stored
-    const int ra = min(m0 + r, p.m - 1), rb = min(n0 + r, p.n - 1);
-    const uint8_t *a = p.a + ra * p.a_s, *w = p.w + rb * p.w_s;
-    const uint8_t *as = p.a_scale + ra * p.as_s, *ws = p.w_scale + rb * p.ws_s;
-    f32x16 acc = {};
-    const int blocks = p.k / 32;
-    for (int b = 0; b < blocks; b += 2) {
-        const bool both = b + 1 < blocks;
-        const bool live = h == 0 || both;
-        i32x8 av = {}, wv = {};
-        if constexpr (FORMAT == SSU_FORMAT_MXFP8) {
-            const i32x4 lo = *reinterpret_cast<const i32x4 *>(a + b * 32 + 16 * h);
-            i32x4 hi = {};
-            if (both)
-                hi = *reinterpret_cast<const i32x4 *>(a + b * 32 + 32 + 16 * h);
-            av = i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        } else if (live) {
-            const i32x4 v = *reinterpret_cast<const i32x4 *>(a + (b + h) * 16);
-            av = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-        }
-        int sa = 127, sw = 127;
-        if (live) {
-            const i32x4 v = *reinterpret_cast<const i32x4 *>(w + (b + h) * 16);
-            wv = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-            sa = as[b + h];
-            sw = ws[b + h];
-        }
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, wv, acc, FORMAT == SSU_FORMAT_MXFP8 ? 0 : 4, 4, 0,
-                                                              sa, 0, sw);
-    }
-    const int n = n0 + r;
-    if (n >= p.n)
-        return;
-    float bias = 0.0f;
-    if (p.bias)
-        bias = p.bias_f32 ? static_cast<const float *>(p.bias)[n] : widen(static_cast<const OT *>(p.bias)[n]);
+// Adds the bias of outputs n .. n + 3.
+template <typename OT>
+__device__ __forceinline__ f32x4 add_bias(const MxParams &p, int n, f32x4 v) {
+    if (p.bias) {
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        const int m = m0 + i % 4 + 8 * (i / 4) + 4 * h;
-        if (m < p.m)
-            static_cast<OT *>(p.out)[m * p.out_s + n] = narrow<OT>(acc[i] + bias);
+        for (int i = 0; i < 4; i++) {
+            const int at = min(n + i, p.n - 1);
+            v[i] += p.bias_f32 ? static_cast<const float *>(p.bias)[at] : widen(static_cast<const OT *>(p.bias)[at]);
+        }
+    }
+    return v;
+}
+
+// Four neighbouring outputs of row m, from n on.
+template <typename OT>
+__device__ __forceinline__ void store_out4(const MxParams &p, int m, int n, f32x4 v) {
+    if (m >= p.m || n >= p.n)
+        return;
+    OT *dst = static_cast<OT *>(p.out) + m * p.out_s + n;
+    typedef OT Vec __attribute__((ext_vector_type(4), aligned(sizeof(OT))));
+    Vec r;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        r[i] = narrow<OT>(v[i]);
+    if (n + 4 <= p.n) {
+        *reinterpret_cast<Vec *>(dst) = r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 3; i++)
+            if (n + i < p.n)
+                dst[i] = r[i];
     }
 }
+
+// ---------------------------------------------------------------- few rows
+//
+// The weights' bytes bound it. A workgroup takes 16 outputs; its waves split k
+// and join their sums in LDS.
+
+constexpr int kStreamWaves = 8;
+constexpr int kStreamRows = 16;  // weight rows per workgroup
+constexpr int kStreamSteps = 4;  // 128-deep steps whose loads are in flight together
+
+// FT: the activations' float type when this kernel quantises them (one row tile of
+// at most kMxFuseRows rows), else void.
+template <typename OT, int FORMAT, int MT, typename FT>
+__global__ __launch_bounds__(kStreamWaves * 64) void mx_stream_kernel(const MxParams p) {
+    constexpr bool kFuse = !std::is_void_v<FT>;
+    constexpr int kChunk = kStreamSteps * 128;  // k values per round
+    constexpr int kRowBytes = FORMAT == SSU_FORMAT_MXFP8 ? kChunk : kChunk / 2;
+    __shared__ f32x4 sums[kStreamWaves][MT][64];
+    __shared__ alignas(16) uint8_t qcodes[kFuse ? kStreamWaves : 1][kMxFuseRows][kRowBytes];
+    __shared__ uint8_t qscales[kFuse ? kStreamWaves : 1][kMxFuseRows][kChunk / 32];
+    const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int r = l % 16, g = l / 16;
+    const int n0 = static_cast<int>(blockIdx.x) * kStreamRows;
+    // rows past the end read the last row; their results are not stored
+    const int64_t wrow = min(n0 + r, p.n - 1);
+    const uint8_t *w = p.w + wrow * p.w_s, *ws = p.w_scale + wrow * p.ws_s;
+    const int blocks = p.k / 32;
+    const int steps = (blocks + 3) / 4;
+    const int rounds = (steps + kStreamSteps - 1) / kStreamSteps;
+    f32x4 acc[MT] = {};
+    for (int round = wave; round < rounds; round += kStreamWaves) {
+        const int first = round * kStreamSteps;
+        i32x4 wv[kStreamSteps];
+        int wsv[kStreamSteps];
+#pragma unroll
+        for (int s = 0; s < kStreamSteps; s++) {
+            const int b = (first + s) * 4 + g;
+            const bool live = b < blocks;
+            wv[s] = live ? *reinterpret_cast<const i32x4 *>(w + static_cast<int64_t>(b) * 16) : i32x4{};
+            wsv[s] = live ? ws[b] : 0;
+        }
+        if constexpr (kFuse) {
+            // this wave's own slice of every activation row, quantised for itself
+            const int at = round * kChunk + l * 8;
+            for (int m = 0; m < p.m; m++) {
+                float v[8] = {};
+                if (at < p.k)
+                    load8(static_cast<const FT *>(p.x) + m * p.x_s + at, v);
+                uint32_t code[2];
+                const uint32_t sc = mx_block<FORMAT>(v, code);
+                store_codes<FORMAT>(qcodes[wave][m], l * 8, code);
+                if (l % 4 == 0)
+                    qscales[wave][m][l / 4] = static_cast<uint8_t>(sc);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
+#pragma unroll
+        for (int s = 0; s < kStreamSteps; s++) {
+#pragma unroll
+            for (int t = 0; t < MT; t++) {
+                i32x8 av;
+                int as;
+                if constexpr (kFuse) {
+                    const int m = min(r, p.m - 1);
+                    if constexpr (FORMAT == SSU_FORMAT_MXFP8)
+                        av = wide(*reinterpret_cast<const i32x4 *>(&qcodes[wave][m][s * 128 + 16 * g]),
+                                  *reinterpret_cast<const i32x4 *>(&qcodes[wave][m][s * 128 + 64 + 16 * g]));
+                    else
+                        av = wide(*reinterpret_cast<const i32x4 *>(&qcodes[wave][m][s * 64 + 16 * g]));
+                    as = qscales[wave][m][s * 4 + g];
+                } else {
+                    const int64_t m = min(t * 16 + r, p.m - 1);
+                    const uint8_t *a = p.a + m * p.a_s;
+                    const int b = (first + s) * 4;
+                    as = b + g < blocks ? p.a_scale[m * p.as_s + b + g] : 0;
+                    if constexpr (FORMAT == SSU_FORMAT_MXFP8) {
+                        const i32x4 lo = b + g / 2 < blocks ? *reinterpret_cast<const i32x4 *>(a + static_cast<int64_t>(b) * 32 + 16 * g) : i32x4{};
+                        const i32x4 hi = b + 2 + g / 2 < blocks ? *reinterpret_cast<const i32x4 *>(a + static_cast<int64_t>(b) * 32 + 64 + 16 * g) : i32x4{};
+                        av = wide(lo, hi);
+                    } else {
+                        av = wide(b + g < blocks ? *reinterpret_cast<const i32x4 *>(a + static_cast<int64_t>(b + g) * 16) : i32x4{});
+                    }
+                }
+                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    wide(wv[s]), av, acc[t], kE2M1, FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, 0, wsv[s], 0, as);
+            }
+        }
+        if constexpr (kFuse) {
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; t++)
+        sums[wave][t][l] = acc[t];
+    __syncthreads();
+    if (threadIdx.x < MT * 64) {
+        const int t = wave;
+        f32x4 v = sums[0][t][l];
+#pragma unroll
+        for (int j = 1; j < kStreamWaves; j++)
+            v += sums[j][t][l];
+        store_out4<OT>(p, t * 16 + r, n0 + 4 * g, add_bias<OT>(p, n0 + 4 * g, v));
+    }
+}
+
+// ---------------------------------------------------------------- many rows
+
+// K tile of the tiled kernels: an activation row's tile is 128 bytes in both formats.
+template <int FORMAT>
+struct KTile {
+    static constexpr int kDepth = FORMAT == SSU_FORMAT_MXFP8 ? 128 : 256;
+    static constexpr int kSteps = kDepth / 64;  // of the 32x32x64 instruction
+    static constexpr int kARow = 128, kWRow = kDepth / 2;  // bytes per row
+};
+__host__ __device__ constexpr int ktile_depth(int format) { return format == SSU_FORMAT_MXFP8 ? 128 : 256; }
+
+// Packed scales: for every 32 rows and K tile, 64 words, one per lane of an
+// operand (row l % 32, group h = l / 32); byte s is the scale of block STEPS h + s of the tile, 0
+// (2^-127) past the end of k. A tile reads its rows' scales without looking where the
+// rows end, so there is room for whole tiles; what lies past the last 32 rows
+// is not written and goes into sums that are not stored.
+__host__ __device__ constexpr int64_t packed_words(int64_t rows, int64_t ktiles) { return (rows + 31) / 32 * ktiles * 64; }
+constexpr int64_t packed_room(int64_t rows, int64_t ktiles) { return (rows + 255) / 256 * 8 * ktiles * 64; }
+
+struct PackParams {
+    // activations: floats to quantise (codes and packed scales), or codes whose scales are packed
+    const void *x;
+    const uint8_t *a_scale;
+    uint8_t *codes, *a_packed;
+    int64_t x_s, as_s;
+    // weights' scales
+    const uint8_t *w_scale;
+    uint32_t *w_packed;
+    int64_t ws_s;
+    int32_t m, n, k, ktiles;
+    int32_t a_groups;  // workgroups that work on the activations; the rest pack the weights' scales
+};
+
+template <int FORMAT>
+__device__ __forceinline__ void pack_scales(const uint8_t *scale, int64_t stride, int32_t rows, int32_t blocks, int32_t ktiles,
+                                            uint32_t *packed, int64_t first, int64_t step) {
+    constexpr int kSteps = KTile<FORMAT>::kSteps;
+    const int64_t words = packed_words(rows, ktiles);
+    for (int64_t i = first; i < words; i += step) {
+        const int l = static_cast<int>(i % 64);
+        const int64_t t = i / 64;
+        const int kt = static_cast<int>(t % ktiles);
+        const int64_t row = min(t / ktiles * 32 + l % 32, static_cast<int64_t>(rows) - 1);
+        const int b = (2 * kt + l / 32) * kSteps;
+        uint32_t v = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; s++)
+            if (b + s < blocks)
+                v |= static_cast<uint32_t>(scale[row * stride + b + s]) << (8 * s);
+        packed[i] = v;
+    }
+}
+
+// What the tiled kernels need besides the codes: the weights' scales packed,
+// and the activations' (quantised here when they come as floats).
+template <typename FT, int FORMAT>
+__global__ __launch_bounds__(kQuantThreads) void mx_pack_kernel(const PackParams p) {
+    constexpr int kSteps = KTile<FORMAT>::kSteps;
+    const int blocks = p.k / 32;
+    if (static_cast<int>(blockIdx.x) >= p.a_groups) {
+        const int64_t at = static_cast<int64_t>(blockIdx.x - p.a_groups) * kQuantThreads + threadIdx.x;
+        pack_scales<FORMAT>(p.w_scale, p.ws_s, p.n, blocks, p.ktiles, p.w_packed, at,
+                            static_cast<int64_t>(gridDim.x - p.a_groups) * kQuantThreads);
+        return;
+    }
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kQuantThreads + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(p.a_groups) * kQuantThreads;
+    if constexpr (std::is_void_v<FT>) {
+        pack_scales<FORMAT>(p.a_scale, p.as_s, p.m, blocks, p.ktiles, reinterpret_cast<uint32_t *>(p.a_packed), first, step);
+    } else {
+        // four lanes per block of 32, over whole K tiles: the blocks past the end of k get the scale byte 0 and no codes
+        const int64_t eighths = static_cast<int64_t>(p.ktiles) * (KTile<FORMAT>::kDepth / 8);
+        const int64_t total = p.m * eighths;
+        for (int64_t i = first; i < total; i += step) {
+            const int64_t row = i / eighths;
+            const int at = static_cast<int>(i % eighths) * 8, b = at / 32;
+            uint32_t sc = 0;
+            if (at < p.k) {
+                float v[8];
+                load8(static_cast<const FT *>(p.x) + row * p.x_s + at, v);
+                uint32_t code[2];
+                sc = mx_block<FORMAT>(v, code);
+                store_codes<FORMAT>(p.codes + row * (FORMAT == SSU_FORMAT_MXFP4 ? p.k / 2 : p.k), at, code);
+            }
+            if (i % 4 == 0) {
+                const int kt = b / (2 * kSteps), in = b % (2 * kSteps);
+                const int64_t word = (row / 32 * p.ktiles + kt) * 64 + in / kSteps * 32 + row % 32;
+                p.a_packed[word * 4 + in % kSteps] = static_cast<uint8_t>(sc);
+            }
+        }
+    }
+}
+
+struct TileParams {
+    MxParams p;
+    const uint32_t *a_packed, *w_packed;
+    int32_t ktiles, mtiles, ntiles;
+};
+
+// Byte offset of 16-byte chunk c of row r in an LDS image of rows of 128 or 64 bytes.
+// Eight lanes that read one chunk of eight neighbouring rows touch eight
+// different 16-byte columns of the 128-byte lines: no bank is asked twice.
+template <int ROW>
+__device__ __forceinline__ int lds_chunk(int r, int c) {
+    if constexpr (ROW == 128) {
+        return r * 128 + ((c ^ (r & 7)) * 16);
+    } else {
+        const int line = r / 2;
+        return line * 128 + ((((r & 1) * 4 + c) ^ (line & 7)) * 16);
+    }
+}
+
+// Workgroup id to tile: each XCD takes a run of tiles, in groups of eight rows of
+// tiles, so that the tiles at work on it share activations and weights in its L2.
+__device__ __forceinline__ void tile_at(int id, int mtiles, int ntiles, int *mt, int *nt) {
+    const int total = mtiles * ntiles;
+    const int per = total / kXcds, rest = total % kXcds, x = id % kXcds;
+    const int lin = x * per + min(x, rest) + id / kXcds;
+    const int group = lin / (8 * ntiles), first = group * 8, height = min(8, mtiles - first);
+    const int in = lin - first * ntiles;
+    *mt = first + in % height;
+    *nt = in / height;
+}
+
+// 16 bytes per lane from memory to 1 KiB of LDS: lane l's bytes go to dst + 16 l.
+__device__ __forceinline__ void load_to_lds(const uint8_t *src, uint8_t *dst) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                     (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
+// One operand's part in filling an LDS image of ROWS rows of ROW bytes: wave `wave` of
+// WAVES loads every WAVES-th KiB. A lane's LDS place is fixed, so the swizzle is in
+// which chunk it fetches. Rows past the end fetch the last row; chunks past the end
+// of k fetch the row's last chunk, which a scale of 2^-127 on either side takes out of the sum.
+template <int ROWS, int ROW, int WAVES>
+struct Filler {
+    static constexpr int kLoads = ROWS * ROW / 1024 / WAVES;
+    static_assert(kLoads * WAVES * 1024 == ROWS * ROW, "whole KiB per wave");
+    const uint8_t *row[kLoads];
+    int chunk;  // byte offset of this lane's chunk in its row's tile
+    int bytes;  // of a row
+
+    __device__ __forceinline__ Filler(const uint8_t *base, int64_t stride, int first, int rows, int row_bytes, int wave, int l) {
+        bytes = row_bytes;
+        const int line = l / 8, slot = (l % 8) ^ line;  // of the lane's KiB: line is line & 7 of the image
+        chunk = ROW == 128 ? slot * 16 : slot % 4 * 16;
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) {
+            const int at = (wave + WAVES * i) * 8 + line;
+            const int r = ROW == 128 ? at : 2 * at + slot / 4;
+            row[i] = base + min(first + r, rows - 1) * stride;
+        }
+    }
+    __device__ __forceinline__ void load(int kt, uint8_t *lds, int wave) const {
+        const int64_t at = min(kt * ROW + chunk, bytes - 16);
+#pragma unroll
+        for (int i = 0; i < kLoads; i++)
+            load_to_lds(row[i] + at, lds + (wave + WAVES * i) * 1024);
+    }
+};
+
+// TM x TN outputs per workgroup; the waves are WM x WN over the tile and WK over the
+// steps of a K tile (those join their sums in LDS at the end). Codes go straight
+// from memory to two LDS images: while one K tile is multiplied the next arrives. Each
+// step's operands are read during the step before, the next tile's first ones
+// during this one's last step, behind the only barrier of a tile; the image that
+// the tile leaves is filled from there on.
+template <typename OT, int FORMAT, int TM, int TN, int WM, int WN, int WK>
+__global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TileParams t) {
+    using KT = KTile<FORMAT>;
+    constexpr int kWaves = WM * WN * WK;
+    constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
+    constexpr int kSteps = KT::kSteps / WK;  // of this wave per K tile
+    constexpr int kABytes = TM * KT::kARow, kStage = kABytes + TN * KT::kWRow;
+    // two arrays, so that the compiler can tell a fill of one from a read of the other
+    __shared__ alignas(16) uint8_t lds0[kStage];
+    __shared__ alignas(16) uint8_t lds1[kStage];
+    const MxParams &p = t.p;
+    const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int r = l % 32, h = l / 32;
+    const int wm = wave % WM, wn = wave / WM % WN, wk = wave / (WM * WN);
+    int mt, nt;
+    tile_at(blockIdx.x, t.mtiles, t.ntiles, &mt, &nt);
+    const int m0 = mt * TM, n0 = nt * TN;
+
+    const Filler<TM, KT::kARow, kWaves> fill_a(p.a, p.a_s, m0, p.m, FORMAT == SSU_FORMAT_MXFP8 ? p.k : p.k / 2, wave, l);
+    const Filler<TN, KT::kWRow, kWaves> fill_w(p.w, p.w_s, n0, p.n, p.k / 2, wave, l);
+    auto fill = [&](uint8_t *lds, int kt) {
+        fill_a.load(kt, lds, wave);
+        fill_w.load(kt, lds + kABytes, wave);
+    };
+    // scales of this wave's fragments
+    const uint32_t *aps = t.a_packed + (static_cast<int64_t>(m0 / 32 + wm * FM) * t.ktiles) * 64 + l;
+    const uint32_t *wps = t.w_packed + (static_cast<int64_t>(n0 / 32 + wn * FN) * t.ktiles) * 64 + l;
+    int asc[FM], wsc[FN], asc_next[FM], wsc_next[FN];
+    auto load_scales = [&](int kt) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+            asc_next[i] = static_cast<int>(aps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64] >> (8 * wk));
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+            wsc_next[i] = static_cast<int>(wps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64] >> (8 * wk));
+    };
+    struct Frags {
+        std::conditional_t<FORMAT == SSU_FORMAT_MXFP8, i32x8, i32x4> a[FM];
+        i32x4 w[FN];
+    };
+    auto read = [&](const uint8_t *src, int j) {
+        Frags f;
+        const int s = wk + WK * j;
+#pragma unroll
+        for (int i = 0; i < FM; i++) {
+            const int row = (wm * FM + i) * 32 + r;
+            if constexpr (FORMAT == SSU_FORMAT_MXFP8)
+                f.a[i] = wide(*reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, 2 * s + h)),
+                              *reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, 2 * (KT::kSteps + s) + h)));
+            else
+                f.a[i] = *reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, KT::kSteps * h + s));
+        }
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+            f.w[i] = *reinterpret_cast<const i32x4 *>(src + kABytes +
+                                                      lds_chunk<KT::kWRow>((wn * FN + i) * 32 + r, KT::kSteps * h + s));
+        return f;
+    };
+    f32x16 acc[FM][FN] = {};
+    auto multiply = [&](const Frags &f, auto jc) {
+        constexpr int kByte = decltype(jc)::value * WK;
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    wide(f.w[j]), wide(f.a[i]), acc[i][j], kE2M1, FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, kByte, wsc[j], kByte, asc[i]);
+    };
+
+    if (t.ktiles > 0) {
+        fill(lds0, 0);
+        load_scales(0);
+        if (t.ktiles > 1)
+            fill(lds1, 1);
+        __syncthreads();
+        Frags cur = read(lds0, 0);
+        auto tile = [&](uint8_t *here, uint8_t *there, int kt) {
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+                asc[i] = asc_next[i];
+#pragma unroll
+            for (int i = 0; i < FN; i++)
+                wsc[i] = wsc_next[i];
+            if (kt + 1 < t.ktiles)
+                load_scales(kt + 1);
+            for_passes<0, kSteps>([&](auto jc) {
+                constexpr int j = decltype(jc)::value;
+                Frags next;
+                if constexpr (j + 1 < kSteps) {
+                    next = read(here, j + 1);
+                } else {
+                    __syncthreads();  // waits for the fills in flight too
+                    if (kt + 2 < t.ktiles)
+                        fill(here, kt + 2);
+                    next = read(there, 0);  // after the last tile: old bytes, not used
+                }
+                multiply(cur, jc);
+                cur = next;
+            });
+        };
+        for (int kt = 0; kt < t.ktiles; kt += 2) {
+            tile(lds0, lds1, kt);
+            if (kt + 1 < t.ktiles)
+                tile(lds1, lds0, kt + 1);
+        }
+    }
+
+    if constexpr (WK > 1) {
+        // each wave of the WK that share a part of the tile sums and stores its share of the
+        // fragments, half of the registers at a time: the others leave theirs in the LDS images
+        static_assert(FM * FN % WK == 0, "fragments divide over the waves");
+        constexpr int kShare = FM * FN / WK, kHalf = FM * FN * 8 * 64;  // floats of a wave
+        static_assert(WM * WN * WK * kHalf * 4 <= 2 * kStage, "sums fit the images");
+        constexpr int kIn0 = kStage / 4 / kHalf;  // waves whose floats go to the first image
+        auto sums = [&](int w) {
+            return w < kIn0 ? reinterpret_cast<float *>(lds0) + w * kHalf : reinterpret_cast<float *>(lds1) + (w - kIn0) * kHalf;
+        };
+        const int first = (wn * WM + wm), stride = WM * WN;  // waves first + stride * (0 .. WK - 1) share
+        for_passes<0, 2>([&](auto hc) {
+            constexpr int half = decltype(hc)::value;
+            __syncthreads();
+            float *mine = sums(first + stride * wk);
+#pragma unroll
+            for (int f = 0; f < FM * FN; f++)
+                if (f / kShare != wk)
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        mine[(f * 8 + i) * 64 + l] = acc[f / FN][f % FN][half * 8 + i];
+            __syncthreads();
+#pragma unroll
+            for (int f = 0; f < FM * FN; f++) {
+                if (f / kShare != wk)
+                    continue;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    v[i] = acc[f / FN][f % FN][half * 8 + i];
+                for (int o = 1; o < WK; o++) {
+                    const float *other = sums(first + stride * ((wk + o) % WK));
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        v[i] += other[(f * 8 + i) * 64 + l];
+                }
+                const int m = m0 + (wm * FM + f / FN) * 32 + r, n = n0 + (wn * FN + f % FN) * 32 + 4 * h + 16 * half;
+                store_out4<OT>(p, m, n, add_bias<OT>(p, n, f32x4{v[0], v[1], v[2], v[3]}));
+                store_out4<OT>(p, m, n + 8, add_bias<OT>(p, n + 8, f32x4{v[4], v[5], v[6], v[7]}));
+            }
+        });
+    } else {
+        if (p.bias) {
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const f32x4 b = add_bias<OT>(p, n0 + (wn * FN + j) * 32 + 4 * h + 8 * q, f32x4{});
+#pragma unroll
+                    for (int i = 0; i < FM; i++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            acc[i][j][4 * q + e] += b[e];
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++) {
+                const int m = m0 + (wm * FM + i) * 32 + r, n = n0 + (wn * FN + j) * 32 + 4 * h;
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    store_out4<OT>(p, m, n + 8 * q,
+                                   f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
+            }
+    }
+}
+
+// ---------------------------------------------------------------- launches
 
 template <typename T>
 const void *quantize_fn(int format) {
     return format == SSU_FORMAT_MXFP4 ? reinterpret_cast<const void *>(&mx_quantize_rows_kernel<T, SSU_FORMAT_MXFP4>)
                                       : reinterpret_cast<const void *>(&mx_quantize_rows_kernel<T, SSU_FORMAT_MXFP8>);
 }
-template <typename OT>
-const void *linear_fn(int format) {
-    return format == SSU_FORMAT_MXFP4 ? reinterpret_cast<const void *>(&mx_linear_kernel<OT, SSU_FORMAT_MXFP4>)
-                                      : reinterpret_cast<const void *>(&mx_linear_kernel<OT, SSU_FORMAT_MXFP8>);
+template <typename FT>
+const void *pack_fn(int format) {
+    return format == SSU_FORMAT_MXFP4 ? reinterpret_cast<const void *>(&mx_pack_kernel<FT, SSU_FORMAT_MXFP4>)
+                                      : reinterpret_cast<const void *>(&mx_pack_kernel<FT, SSU_FORMAT_MXFP8>);
+}
+template <typename OT, int FORMAT>
+const void *stream_fn(int m, bool fuse, int x_dtype) {
+    if (fuse)
+        return x_dtype == SSU_F32   ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 1, float>)
+               : x_dtype == SSU_F16 ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 1, _Float16>)
+                                    : reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 1, __bf16>);
+    return m <= 16   ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 1, void>)
+           : m <= 32 ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 2, void>)
+                     : reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 4, void>);
+}
+
+struct TileShape {
+    int tm, tn, threads;
+};
+constexpr TileShape kTileShapes[3] = {{256, 256, 256}, {128, 128, 256}, {64, 64, 256}};
+
+template <typename OT, int FORMAT>
+const void *tile_fn(int shape) {
+    constexpr int kWk = KTile<FORMAT>::kSteps;
+    switch (shape) {
+    case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 256, 256, 2, 2, 1>);
+    case 1: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 128, 128, 2, 2, 1>);
+    }
+    return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk>);
+}
+
+template <typename F>
+const void *by_out(int out_dtype, F &&f) {
+    return out_dtype == SSU_F32 ? f(0.0f) : out_dtype == SSU_F16 ? f(static_cast<_Float16>(0)) : f(static_cast<__bf16>(0));
+}
+
+int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
+int64_t code_bytes(int64_t m, int64_t k, int format) { return round256(format == SSU_FORMAT_MXFP4 ? m * k / 2 : m * k); }
+
+int run(const void *fn, int64_t grid, int block, void **args, void *stream) {
+    if (grid > INT32_MAX)
+        return static_cast<int>(hipErrorInvalidValue);
+    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(block), args, 0,
+                                            static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
@@ -107,21 +603,90 @@ int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t 
     blocks = blocks > 65536 ? 65536 : blocks;
     int32_t k32 = static_cast<int32_t>(k);
     void *args[] = {&src, &stride, &rows, &k32, &codes, &scales};
-    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(kQuantThreads), args, 0,
-                                            static_cast<hipStream_t>(stream)));
+    return run(fn, blocks, kQuantThreads, args, stream);
 }
 
-int launch_mx_linear(const MxParams &p, int format, int out_dtype, void *stream) {
-    const void *fn = out_dtype == SSU_F32   ? linear_fn<float>(format)
-                     : out_dtype == SSU_F16 ? linear_fn<_Float16>(format)
-                                            : linear_fn<__bf16>(format);
-    MxParams pc = p;
-    void *args[] = {&pc};
-    // grid.y ends at 65535
-    if ((p.m + 31) / 32 > 65535)
-        return static_cast<int>(hipErrorInvalidValue);
-    return static_cast<int>(hipLaunchKernel(fn, dim3((p.n + 31) / 32, (p.m + 31) / 32), dim3(64), args, 0,
-                                            static_cast<hipStream_t>(stream)));
+int64_t mx_linear_workspace(int64_t m, int64_t n, int64_t k, int format, bool floats) {
+    if (m <= kMxRowsMax)
+        return floats && m > kMxFuseRows ? code_bytes(m, k, format) + m * (k / 32) : 0;
+    const int64_t ktiles = (k + ktile_depth(format) - 1) / ktile_depth(format);
+    return (floats ? code_bytes(m, k, format) : 0) + 4 * (packed_room(m, ktiles) + packed_room(n, ktiles));
+}
+
+int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *stream) {
+    MxParams p = args_in;
+    const bool mx4 = format == SSU_FORMAT_MXFP4;
+    const bool floats = p.x != nullptr;
+    if (p.m <= kMxRowsMax) {
+        const bool fuse = floats && p.m <= kMxFuseRows;
+        if (floats && !fuse && p.k > 0) {
+            uint8_t *scales = p.workspace + code_bytes(p.m, p.k, format);
+            if (int e = launch_mx_quantize_rows(p.x, p.x_dtype, p.x_s, p.m, p.k, p.workspace, scales, format, stream))
+                return e;
+            p.a = p.workspace;
+            p.a_scale = scales;
+            p.a_s = mx4 ? p.k / 2 : p.k;
+            p.as_s = p.k / 32;
+        }
+        const void *fn = by_out(out_dtype, [&](auto o) {
+            using OT = decltype(o);
+            return mx4 ? stream_fn<OT, SSU_FORMAT_MXFP4>(p.m, fuse, p.x_dtype) : stream_fn<OT, SSU_FORMAT_MXFP8>(p.m, fuse, p.x_dtype);
+        });
+        void *args[] = {&p};
+        return run(fn, (p.n + kStreamRows - 1) / kStreamRows, kStreamWaves * 64, args, stream);
+    }
+
+    TileParams t = {};
+    t.ktiles = (p.k + ktile_depth(format) - 1) / ktile_depth(format);
+    uint8_t *ws = p.workspace;
+    PackParams q = {};
+    if (floats) {
+        q.x = p.x;
+        q.x_s = p.x_s;
+        q.codes = ws;
+        p.a = ws;
+        p.a_s = mx4 ? p.k / 2 : p.k;
+        ws += code_bytes(p.m, p.k, format);
+    } else {
+        q.a_scale = p.a_scale;
+        q.as_s = p.as_s;
+    }
+    q.a_packed = ws;
+    q.w_packed = reinterpret_cast<uint32_t *>(ws) + packed_room(p.m, t.ktiles);
+    q.w_scale = p.w_scale;
+    q.ws_s = p.ws_s;
+    q.m = p.m, q.n = p.n, q.k = p.k, q.ktiles = t.ktiles;
+    if (t.ktiles > 0) {
+        const int64_t a_work = floats ? static_cast<int64_t>(p.m) * t.ktiles * (ktile_depth(format) / 8) : packed_words(p.m, t.ktiles);
+        const int64_t w_work = packed_words(p.n, t.ktiles);
+        const auto groups = [](int64_t work) { return static_cast<int>(std::min<int64_t>((work + kQuantThreads - 1) / kQuantThreads, 32768)); };
+        q.a_groups = groups(a_work);
+        const void *fn = !floats                ? pack_fn<void>(format)
+                         : p.x_dtype == SSU_F32 ? pack_fn<float>(format)
+                         : p.x_dtype == SSU_F16 ? pack_fn<_Float16>(format)
+                                                : pack_fn<__bf16>(format);
+        void *args[] = {&q};
+        if (int e = run(fn, q.a_groups + groups(w_work), kQuantThreads, args, stream))
+            return e;
+    }
+    t.a_packed = reinterpret_cast<const uint32_t *>(q.a_packed);
+    t.w_packed = q.w_packed;
+    t.p = p;
+    // the largest tile that leaves every compute unit one
+    int shape = 0;
+    auto tiles = [&](int s) {
+        return static_cast<int64_t>((p.m + kTileShapes[s].tm - 1) / kTileShapes[s].tm) * ((p.n + kTileShapes[s].tn - 1) / kTileShapes[s].tn);
+    };
+    while (shape < 2 && tiles(shape) < 256)
+        shape++;
+    t.mtiles = (p.m + kTileShapes[shape].tm - 1) / kTileShapes[shape].tm;
+    t.ntiles = (p.n + kTileShapes[shape].tn - 1) / kTileShapes[shape].tn;
+    const void *fn = by_out(out_dtype, [&](auto o) {
+        using OT = decltype(o);
+        return mx4 ? tile_fn<OT, SSU_FORMAT_MXFP4>(shape) : tile_fn<OT, SSU_FORMAT_MXFP8>(shape);
+    });
+    void *args[] = {&t};
+    return run(fn, tiles(shape), kTileShapes[shape].threads, args, stream);
 }
 
 }  // namespace ssu

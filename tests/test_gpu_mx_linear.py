@@ -97,8 +97,12 @@ SHAPES = [(1, 1, 32), (1, 33, 64), (2, 64, 96), (1, 4096, 512), (3, 100, 160), (
           (255, 511, 256), (256, 256, 2048), (300, 770, 352), (513, 640, 640), (1, 18560, 64), (700, 72, 8192), (2050, 1030, 96)]
 
 
+# enough rows and outputs for the larger tiles
+LARGE = [(2100, 2090, 160), (1100, 2080, 1312), (4200, 4130, 288), (5000, 5000, 544)]
+
+
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
-@pytest.mark.parametrize("m,n,k", SHAPES)
+@pytest.mark.parametrize("m,n,k", SHAPES + LARGE)
 def test_exact_products(m, n, k, fmt):
     """Sums that fp32 holds exactly, in every output type and with a bias."""
     g = torch.Generator().manual_seed(m * 7 + n * 3 + k)
