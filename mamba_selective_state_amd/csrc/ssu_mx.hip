@@ -206,7 +206,9 @@ struct KTile {
     static constexpr int kSteps = kDepth / 64;  // of the 32x32x64 instruction
     static constexpr int kARow = 128, kWRow = kDepth / 2;  // bytes per row
 };
-__host__ __device__ constexpr int ktile_depth(int format) { return format == SSU_FORMAT_MXFP8 ? 128 : 256; }
+constexpr int ktile_depth(int format) { return format == SSU_FORMAT_MXFP8 ? 128 : 256; }
+// K tiles of k values: an even number.
+constexpr int64_t ktiles_of(int64_t k, int format) { return (k + 2 * ktile_depth(format) - 1) / (2 * ktile_depth(format)) * 2; }
 
 // Packed scales: for every 32 rows and K tile, 64 words, one per lane of an
 // operand (row l % 32, group h = l / 32); byte s is the scale of block STEPS h + s of the tile, 0
@@ -327,6 +329,14 @@ __device__ __forceinline__ void load_to_lds(const uint8_t *src, uint8_t *dst) {
                                      (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
 }
 
+// Barrier behind which every wave's fills have arrived. The wait is spelled out: the
+// compiler's own barrier waits for LDS instructions only, and a wave must not
+// pass while what it fetched for the others is on its way.
+__device__ __forceinline__ void fills_barrier() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __syncthreads();
+}
+
 // One operand's part in filling an LDS image of ROWS rows of ROW bytes: wave `wave` of
 // WAVES loads every WAVES-th KiB. A lane's LDS place is fixed, so the swizzle is in
 // which chunk it fetches. Rows past the end fetch the last row; chunks past the end
@@ -395,10 +405,10 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
     auto load_scales = [&](int kt) {
 #pragma unroll
         for (int i = 0; i < FM; i++)
-            asc_next[i] = static_cast<int>(aps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64] >> (8 * wk));
+            asc_next[i] = static_cast<int>(aps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64]);
 #pragma unroll
         for (int i = 0; i < FN; i++)
-            wsc_next[i] = static_cast<int>(wps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64] >> (8 * wk));
+            wsc_next[i] = static_cast<int>(wps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64]);
     };
     struct Frags {
         std::conditional_t<FORMAT == SSU_FORMAT_MXFP8, i32x8, i32x4> a[FM];
@@ -433,42 +443,56 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
                     wide(f.w[j]), wide(f.a[i]), acc[i][j], kE2M1, FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, kByte, wsc[j], kByte, asc[i]);
     };
 
+    // k is taken in pairs of tiles without a branch: what lies past its end is
+    // filled and multiplied like the rest, and comes to nothing by its scales
     if (t.ktiles > 0) {
         fill(lds0, 0);
         load_scales(0);
-        if (t.ktiles > 1)
-            fill(lds1, 1);
-        __syncthreads();
+        fill(lds1, 1);
+        fills_barrier();
         Frags cur = read(lds0, 0);
         auto tile = [&](uint8_t *here, uint8_t *there, int kt) {
 #pragma unroll
             for (int i = 0; i < FM; i++)
-                asc[i] = asc_next[i];
+                asc[i] = WK > 1 ? asc_next[i] >> (8 * wk) : asc_next[i];
 #pragma unroll
             for (int i = 0; i < FN; i++)
-                wsc[i] = wsc_next[i];
-            if (kt + 1 < t.ktiles)
-                load_scales(kt + 1);
+                wsc[i] = WK > 1 ? wsc_next[i] >> (8 * wk) : wsc_next[i];
+            load_scales(min(kt + 1, t.ktiles - 1));
             for_passes<0, kSteps>([&](auto jc) {
                 constexpr int j = decltype(jc)::value;
+                __builtin_amdgcn_sched_barrier(0);
                 Frags next;
                 if constexpr (j + 1 < kSteps) {
                     next = read(here, j + 1);
                 } else {
-                    __syncthreads();  // waits for the fills in flight too
-                    if (kt + 2 < t.ktiles)
-                        fill(here, kt + 2);
-                    next = read(there, 0);  // after the last tile: old bytes, not used
+                    fills_barrier();
+                    next = read(there, 0);
+                    fill(here, kt + 2);
                 }
                 multiply(cur, jc);
                 cur = next;
+                // the reads (and fills) one by one between the first products
+                constexpr int kReads = (FORMAT == SSU_FORMAT_MXFP8 ? 2 * FM : FM) + FN, kFirst = FM * FN > 1 ? FM * FN / 2 : 1;
+                constexpr int kFills = j + 1 == kSteps ? decltype(fill_a)::kLoads + decltype(fill_w)::kLoads : 0;
+                for_passes<0, kFirst>([&](auto ic) {
+                    constexpr int i = decltype(ic)::value;
+                    __builtin_amdgcn_sched_group_barrier(0x100, kReads * (i + 1) / kFirst - kReads * i / kFirst, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                });
+                for_passes<0, FM * FN - kFirst>([&](auto ic) {
+                    constexpr int i = decltype(ic)::value, n = FM * FN - kFirst;
+                    if constexpr (kFills > 0)
+                        __builtin_amdgcn_sched_group_barrier(0x010, kFills * (i + 1) / n - kFills * i / n, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                });
             });
         };
         for (int kt = 0; kt < t.ktiles; kt += 2) {
             tile(lds0, lds1, kt);
-            if (kt + 1 < t.ktiles)
-                tile(lds1, lds0, kt + 1);
+            tile(lds1, lds0, kt + 1);
         }
+        fills_barrier();
     }
 
     if constexpr (WK > 1) {
@@ -513,29 +537,55 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
             }
         });
     } else {
-        if (p.bias) {
+        // 32 rows at a time through this wave's part of the images, so that a store writes
+        // whole runs of a row: a lane holds four outputs of one row, 32 rows to an instruction
+        constexpr int kVec = 16 / static_cast<int>(sizeof(OT)), kCols = 32 * FN;
+        constexpr int kLanes = kCols / kVec, kRows = 64 / kLanes;  // lanes per row, rows per store
+        constexpr int kRow = kCols + kVec;                         // 16 bytes of padding: rows start on different banks
+        static_assert(32 * kRow * static_cast<int>(sizeof(OT)) <= 2 * kStage / kWaves && kWaves % 2 == 0, "slabs fit");
+        OT *slab = reinterpret_cast<OT *>((wave % 2 ? lds1 : lds0) + wave / 2 * (2 * kStage / kWaves));
+        typedef OT Vec4 __attribute__((ext_vector_type(4)));
+        typedef OT VecN __attribute__((ext_vector_type(kVec)));
+        typedef OT VecU __attribute__((ext_vector_type(kVec), aligned(sizeof(OT))));
+        const int n = n0 + wn * kCols + l % kLanes * kVec;
+        for_passes<0, FM>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
 #pragma unroll
             for (int j = 0; j < FN; j++)
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
-                    const f32x4 b = add_bias<OT>(p, n0 + (wn * FN + j) * 32 + 4 * h + 8 * q, f32x4{});
+                    Vec4 v;
+                    f32x4 sum = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                    sum = add_bias<OT>(p, n0 + (wn * FN + j) * 32 + 8 * q + 4 * h, sum);
 #pragma unroll
-                    for (int i = 0; i < FM; i++)
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            acc[i][j][4 * q + e] += b[e];
+                    for (int e = 0; e < 4; e++)
+                        v[e] = narrow<OT>(sum[e]);
+                    *reinterpret_cast<Vec4 *>(slab + r * kRow + j * 32 + 8 * q + 4 * h) = v;
                 }
-        }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            const int m = m0 + (wm * FM + i) * 32 + l / kLanes;
+            const OT *src = slab + l / kLanes * kRow + l % kLanes * kVec;
+            OT *dst = static_cast<OT *>(p.out) + m * p.out_s + n;
 #pragma unroll
-        for (int i = 0; i < FM; i++)
+            for (int k = 0; k < 32 / kRows; k++) {
+                const VecN v = *reinterpret_cast<const VecN *>(src + k * kRows * kRow);
+                if (m + k * kRows < p.m) {
+                    OT *at = dst + k * kRows * p.out_s;
+                    if (n + kVec <= p.n)
+                        *reinterpret_cast<VecU *>(at) = v;
+                    else
 #pragma unroll
-            for (int j = 0; j < FN; j++) {
-                const int m = m0 + (wm * FM + i) * 32 + r, n = n0 + (wn * FN + j) * 32 + 4 * h;
-#pragma unroll
-                for (int q = 0; q < 4; q++)
-                    store_out4<OT>(p, m, n + 8 * q,
-                                   f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
+                        for (int e = 0; e < kVec - 1; e++)
+                            if (n + e < p.n)
+                                at[e] = v[e];
+                }
             }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        });
     }
 }
 
@@ -609,7 +659,7 @@ int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t 
 int64_t mx_linear_workspace(int64_t m, int64_t n, int64_t k, int format, bool floats) {
     if (m <= kMxRowsMax)
         return floats && m > kMxFuseRows ? code_bytes(m, k, format) + m * (k / 32) : 0;
-    const int64_t ktiles = (k + ktile_depth(format) - 1) / ktile_depth(format);
+    const int64_t ktiles = ktiles_of(k, format);
     return (floats ? code_bytes(m, k, format) : 0) + 4 * (packed_room(m, ktiles) + packed_room(n, ktiles));
 }
 
@@ -637,7 +687,7 @@ int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *s
     }
 
     TileParams t = {};
-    t.ktiles = (p.k + ktile_depth(format) - 1) / ktile_depth(format);
+    t.ktiles = static_cast<int32_t>(ktiles_of(p.k, format));
     uint8_t *ws = p.workspace;
     PackParams q = {};
     if (floats) {
