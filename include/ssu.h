@@ -548,7 +548,10 @@ SSU_API ssu_status_t ssu_mx_linear(const ssu_mx_linear_args_t *args, void *works
  *   logprob, entropy  [rows] f32; rank [rows] i32; contiguous
  *   top_tokens i32, top_logprobs f32 [rows, top], contiguous, top <=
  *                SSU_TOP_MAX; both or neither
- * `workspace` as for ssu_mx_linear. */
+ * `workspace`: DEVICE memory of at least ssu_token_logprobs_workspace_bytes, 256-
+ * byte aligned (NULL where that is 0), whose first 2048 bytes are zero before its first use and
+ * which nothing else writes between calls (a call leaves them zero); two calls
+ * that overlap must not share one. */
 #define SSU_TOP_MAX 32
 typedef struct {
     ssu_tensor_t logits, tokens, mask, temperature;

@@ -57,7 +57,10 @@ struct LogprobParams {
     int64_t logits_s, tokens_s, mask_s, temp_s;
     int64_t rows;
     int32_t vocab, top, tokens_i64;
+    uint8_t *workspace;
 };
+// Workspace bytes (0 where a row is not split).
+int64_t logprobs_workspace(int64_t rows, int64_t vocab, int64_t top);
 int launch_logprobs(const LogprobParams &p, int dtype, void *stream);
 
 }  // namespace ssu

@@ -276,7 +276,11 @@ ssu_status_t ssu_mx_linear(const ssu_mx_linear_args_t *a, void *workspace, int64
     return done(ssu::launch_mx_linear(p, a->x_format, a->out.dtype, stream));
 }
 
-int64_t ssu_token_logprobs_workspace_bytes(const ssu_logprob_args_t *) { return 0; }
+int64_t ssu_token_logprobs_workspace_bytes(const ssu_logprob_args_t *a) {
+    if (!a || a->logits.ndim != 2 || a->logits.size[0] <= 0)
+        return 0;
+    return ssu::logprobs_workspace(a->logits.size[0], a->logits.size[1], present(a->top_tokens) ? a->top_tokens.size[1] : 0);
+}
 
 ssu_status_t ssu_token_logprobs(const ssu_logprob_args_t *a, void *workspace, int64_t workspace_bytes, void *stream) {
     if (!a)
@@ -348,6 +352,10 @@ ssu_status_t ssu_token_logprobs(const ssu_logprob_args_t *a, void *workspace, in
     p.rows = rows;
     p.vocab = static_cast<int32_t>(vocab);
     p.top = static_cast<int32_t>(top);
+    const int64_t need = ssu::logprobs_workspace(rows, vocab, top);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return fail(SSU_ERR_VALUE, "workspace must be 256-byte aligned and hold %lld bytes", (long long)need);
+    p.workspace = static_cast<uint8_t *>(workspace);
     return done(ssu::launch_logprobs(p, x.dtype, stream));
 }
 

@@ -1,5 +1,14 @@
 // Log probabilities of given tokens with entropy, rank and the top
-// alternatives (ssu_token_logprobs).
+// alternatives (ssu_token_logprobs), in one pass over the logits.
+//
+// With k = log2(e) / temperature and a reference m near the largest logit,
+//   s = sum 2^((x - m) k),  t = sum 2^((x - m) k) (x - m) k   (over allowed tokens)
+//   log p[token] = (x_token - m) / temperature - log s,  entropy = log s - t ln 2 / s.
+// m is one value per wave, raised (and the sums scaled) only when a logit passes it by
+// more than 2^16 times in probability: any reference within that is as good as the
+// largest logit, and the common vector costs no rescaling.
+#include <algorithm>
+
 #include "ssu_layer_device.h"
 
 namespace ssu {
@@ -7,134 +16,499 @@ namespace {
 
 constexpr int kLogprobThreads = 256;
 constexpr int kLogprobWaves = kLogprobThreads / kWaveLanes;
+constexpr int kVec = 8;                      // logits per lane and access
+constexpr int kTile = kVec * kWaveLanes;     // per wave and access
+constexpr int kInFlight = 4;                 // accesses in flight per wave
+constexpr int kWaveCand = 128;               // candidates a wave holds
+constexpr float kLowest = -3.402823466e38f;  // the lowest finite value
 
 // A logit's place in the order of alternatives: larger keys first. The high
 // word orders the values, the low one prefers the lower index. 0 is below
 // every allowed token's key.
+__device__ __forceinline__ uint32_t order_word(float v) {
+    const uint32_t b = __float_as_uint(v == 0.0f ? 0.0f : v);  // -0 and 0 are equal
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
 __device__ __forceinline__ uint64_t order_key(float v, uint32_t index) {
-    if (v == 0.0f)
-        v = 0.0f;  // -0 and 0 are equal
-    const uint32_t b = __float_as_uint(v);
-    const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
-    return (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - index);
+    return (static_cast<uint64_t>(order_word(v)) << 32) | (0xFFFFFFFFu - index);
 }
 __device__ __forceinline__ float key_value(uint64_t key) {
     const uint32_t o = static_cast<uint32_t>(key >> 32);
     return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
+__device__ __forceinline__ int32_t key_index(uint64_t key) {
+    return static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+}
+// The next float below and above a finite value.
+__device__ __forceinline__ float next_below(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return v == 0.0f ? __uint_as_float(0x80000001u) : __uint_as_float(v > 0.0f ? b - 1 : b + 1);
+}
+__device__ __forceinline__ float next_above(float v) { return -next_below(-v); }
 
-template <typename T>
-__device__ T block_reduce(T v, T *shared, T (*f)(T, T)) {
-    for (int d = 1; d < kWaveLanes; d *= 2) {
-        T o;
-        if constexpr (sizeof(T) == 8)
-            o = static_cast<T>(__shfl_xor(static_cast<unsigned long long>(v), d));
-        else
-            o = __shfl_xor(v, d);
-        v = f(v, o);
-    }
-    __syncthreads();
-    if (threadIdx.x % kWaveLanes == 0)
-        shared[threadIdx.x / kWaveLanes] = v;
-    __syncthreads();
-    v = shared[0];
-    for (int w = 1; w < kLogprobWaves; w++)
-        v = f(v, shared[w]);
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 1; d < kWaveLanes; d *= 2)
+        v = fmaxf(v, __shfl_xor(v, d));
     return v;
 }
-__device__ float add_f(float a, float b) { return a + b; }
-__device__ int add_i(int a, int b) { return a + b; }
-__device__ uint64_t max_k(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 1; d < kWaveLanes; d *= 2)
+        v += __shfl_xor(v, d);
+    return v;
+}
 
-// One workgroup per row; the row is read once for the largest logit, once
-// for the sums and once per alternative.
+// One workgroup's (or, joined, one row's) sums.
+struct Sums {
+    float m, s, t;
+    int32_t before;  // allowed tokens that stand before the given one
+};
+
+// `a` and `b` over a common reference.
+__device__ __forceinline__ Sums join(const Sums &a, const Sums &b, float k) {
+    const Sums &hi = a.m >= b.m ? a : b, &lo = a.m >= b.m ? b : a;
+    const float delta = (lo.m - hi.m) * k;  // not above 0; -inf where the references lie far apart
+    const float c = __builtin_amdgcn_exp2f(delta);
+    Sums r;
+    r.m = hi.m;
+    r.s = hi.s + c * lo.s;
+    // a factor of 0 takes an infinite delta with it, but not a NaN sum
+    r.t = hi.t + (c > 0.0f ? c * (lo.t + delta * lo.s) : 0.0f * lo.t);
+    r.before = a.before + b.before;
+    return r;
+}
+
 template <typename T>
-__global__ __launch_bounds__(kLogprobThreads) void logprob_kernel(const LogprobParams p) {
-    __shared__ float fsum[kLogprobWaves];
-    __shared__ int isum[kLogprobWaves];
-    __shared__ uint64_t ksum[kLogprobWaves];
-    const int64_t row = blockIdx.x;
-    const T *x = static_cast<const T *>(p.logits) + row * p.logits_s;
-    const int32_t *mask = p.mask ? p.mask + row * p.mask_s : nullptr;
+struct RowView {
+    const T *x;
+    const uint8_t *mask;  // bit i of byte j allows token 8 j + i; or null
+    float k;              // log2(e) / temperature
+    float inv;            // 1 / temperature
+    bool bad;             // the temperature is not above 0
+    int64_t token;
+    bool inside;  // the token lies in the vocabulary
+};
+
+template <typename T>
+__device__ __forceinline__ RowView<T> row_view(const LogprobParams &p, int64_t row) {
+    RowView<T> v;
+    v.x = static_cast<const T *>(p.logits) + row * p.logits_s;
+    v.mask = p.mask ? reinterpret_cast<const uint8_t *>(p.mask + row * p.mask_s) : nullptr;
     const float temp = p.temperature ? p.temperature[row * p.temp_s] : 1.0f;
-    const int64_t token =
-        p.tokens_i64 ? static_cast<const int64_t *>(p.tokens)[row * p.tokens_s]
-                     : static_cast<const int32_t *>(p.tokens)[row * p.tokens_s];
-    auto listed = [&](int i) { return !mask || ((static_cast<uint32_t>(mask[i / 32]) >> (i % 32)) & 1u); };
+    v.bad = !(temp > 0.0f);
+    // finite and above 0, so that 0 and -inf times it stay what they are
+    v.k = fminf(fmaxf(1.44269504088896341f / temp, 1.1754944e-38f), -kLowest);
+    v.inv = fminf(1.0f / temp, -kLowest);
+    v.token = p.tokens_i64 ? static_cast<const int64_t *>(p.tokens)[row * p.tokens_s]
+                           : static_cast<const int32_t *>(p.tokens)[row * p.tokens_s];
+    v.inside = v.token >= 0 && v.token < p.vocab;
+    return v;
+}
 
-    uint64_t best = 0;
-    int bad = temp > 0.0f ? 0 : 1;
-    for (int i = threadIdx.x; i < p.vocab; i += kLogprobThreads) {
-        if (!listed(i))
-            continue;
-        const float v = widen(x[i]);
-        if (!(v < __builtin_inff()))
-            bad = 1;
-        else if (v > -__builtin_inff())
-            best = max_k(best, order_key(v, i));
-    }
-    best = block_reduce(best, ksum, max_k);
-    bad = block_reduce(bad, isum, add_i);
-    const float m = key_value(best);
+// The given token's logit, -inf if it is not allowed.
+template <typename T>
+__device__ __forceinline__ float token_logit(const RowView<T> &v) {
+    if (!v.inside)
+        return -__builtin_inff();
+    const bool listed = !v.mask || (v.mask[v.token / 8] >> (v.token % 8)) & 1;
+    const float x = widen(v.x[v.token]);
+    return listed ? x : -__builtin_inff();
+}
 
-    const bool inside = token >= 0 && token < p.vocab;
-    const float mine = inside && listed(static_cast<int>(token)) ? widen(x[token]) : -__builtin_inff();
-    const uint64_t mine_key = mine > -__builtin_inff() ? order_key(mine, static_cast<uint32_t>(token)) : 0;
-    float s = 0.0f, t = 0.0f;
-    int before = 0;
-    for (int i = threadIdx.x; i < p.vocab; i += kLogprobThreads) {
-        if (!listed(i))
-            continue;
-        const float v = widen(x[i]);
-        if (!(v > -__builtin_inff()))
-            continue;
-        const float d = (v - m) / temp;
-        const float e = expf(d);
-        s += e;
-        t += e > 0.0f ? e * d : 0.0f;  // d may be -inf
-        before += order_key(v, i) > mine_key;
+// What the scan did not count: in the access that holds the token it took the logits
+// above the token's only; here come the equal ones at lower indices.
+template <typename T>
+__device__ __forceinline__ int equal_before(const RowView<T> &v, float mine) {
+    int n = 0;
+    for (int64_t i = v.token / kVec * kVec; i < v.token; i++)
+        n += (!v.mask || (v.mask[i / 8] >> (i % 8)) & 1) && widen(v.x[i]) == mine;
+    return n;
+}
+
+// Writes a row's results (one thread; `mine`: the token's logit, `logs`: log s).
+template <typename T>
+__device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, const RowView<T> &v, const Sums &r, float mine,
+                                          bool bad, float logs) {
+    const bool have = mine > -__builtin_inff();
+    const float nan = __builtin_nanf("");
+    p.logprob[row] = bad ? nan : have ? (mine - r.m) * v.inv - logs : -__builtin_inff();
+    p.entropy[row] = bad ? nan : r.s > 0.0f ? fmaxf(logs - r.t / r.s * 0.693147180559945309f, 0.0f) : 0.0f;
+    p.rank[row] = bad || !have ? -1 : r.before + equal_before(v, mine);
+}
+
+__device__ __forceinline__ void write_alternative(const LogprobParams &p, int64_t row, int place, uint64_t key, const Sums &r,
+                                                  float inv, bool bad, float logs) {
+    const bool have = !bad && key != 0;
+    p.top_tokens[row * p.top + place] = have ? key_index(key) : -1;
+    p.top_logprobs[row * p.top + place] = bad    ? __builtin_nanf("")
+                                          : have ? (key_value(key) - r.m) * inv - logs
+                                                 : -__builtin_inff();
+}
+
+// The candidates of one wave in LDS. Every key above `floor` that the wave has seen is
+// in the list, and at least `top` allowed tokens of the row are above or at the
+// floor's value, so what is below it can be dropped.
+struct Candidates {
+    uint64_t *list;  // [kWaveCand]
+    int n;
+    uint64_t floor;
+    float gate;  // accesses whose largest logit is below it hold nothing above the floor
+
+    // Sorts the list and cuts it to the first `top`.
+    __device__ __forceinline__ void prune(int top, int lane) {
+        const uint64_t a = lane < n ? list[lane] : 0, b = 64 + lane < n ? list[64 + lane] : 0;
+        int ra = 0, rb = 0;
+        for (int j = 0; j < n; j++) {
+            const uint64_t o = list[j];
+            ra += o > a;
+            rb += o > b;
+        }
+        __builtin_amdgcn_wave_barrier();
+        if (a != 0 && ra < top)
+            list[ra] = a;
+        if (b != 0 && rb < top)
+            list[rb] = b;
+        __builtin_amdgcn_wave_barrier();
+        if (n >= top) {
+            n = top;
+            floor = list[top - 1];
+            // accesses come in the order of their indices: an equal logit further on stays behind
+            gate = next_above(key_value(floor));
+        }
     }
-    s = block_reduce(s, fsum, add_f);
-    t = block_reduce(t, fsum, add_f);
-    before = block_reduce(before, isum, add_i);
-    const float ls = logf(s);
+    __device__ __forceinline__ void insert(bool pass, uint64_t key, int top, int lane) {
+        uint64_t lanes = __ballot(pass);
+        if (lanes == 0)
+            return;
+        if (n + 64 > kWaveCand) {
+            prune(top, lane);
+            lanes = __ballot(pass && key > floor);
+        }
+        const int at = n + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(lanes >> 32),
+                                                     __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(lanes), 0));
+        if ((lanes >> lane) & 1)
+            list[at] = key;
+        n += __popcll(lanes);
+    }
+};
+
+struct Split {
+    int32_t segments;  // workgroups per row
+    int32_t tiles;     // tiles per segment
+    uint32_t *tickets; // [rows]: workgroups of the row that are done; 0 between calls
+    Sums *sums;        // [rows, segments]
+    uint64_t *keys;    // [rows, segments, top]
+};
+
+constexpr int kMostSegments = 64;
+// Rows below which a row is split: enough workgroups for two on every compute unit.
+constexpr int kSplitBelow = 512;
+constexpr int kMergeCand = SSU_TOP_MAX * SSU_TOP_MAX;  // see merge
+
+template <typename T, bool MASK, bool TOP>
+__global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const LogprobParams p, const Split sp) {
+    __shared__ Sums wave_sums[kLogprobWaves];
+    __shared__ Sums total;
+    __shared__ uint64_t cand[TOP ? kLogprobWaves : 1][TOP ? kWaveCand : 1];
+    __shared__ uint64_t merged[TOP ? kMergeCand : 1];
+    __shared__ uint64_t floors[kLogprobWaves];
+    __shared__ int merged_n, last;
+    const int lane = threadIdx.x % kWaveLanes, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
+    const int64_t row = blockIdx.x / sp.segments;
+    const int segment = static_cast<int>(blockIdx.x % sp.segments);
+    const RowView<T> v = row_view<T>(p, row);
+    const int whole = p.vocab / kTile, tiles = (p.vocab + kTile - 1) / kTile;
+    const int first = segment * sp.tiles, end = min(tiles, first + sp.tiles);
+    const float mine = token_logit(v);
+    const bool counted = mine > -__builtin_inff();
+    // logits above it stand before the token: at lower indices the equal ones too
+    const float mine_low = counted ? next_below(mine) : __builtin_inff(), mine_high = counted ? mine : __builtin_inff();
+
+    typedef T Raw __attribute__((ext_vector_type(kVec), aligned(sizeof(T))));
+    Sums w = {kLowest, 0.0f, 0.0f, 0};
+    float limit = kLowest;
+    Candidates c = {cand[TOP ? wave : 0], 0, 0, 0.0f};
+
+    // tile `t`: its logits, and which of them count (bits)
+    auto fetch = [&](int t, Raw *raw, uint32_t *bits) {
+        const int at = t * kTile + lane * kVec;
+        *bits = MASK ? (at < p.vocab ? v.mask[at / 8] : 0u) : 0xFFu;
+        if (t < whole) {
+            *raw = *reinterpret_cast<const Raw *>(v.x + at);
+        } else {
+            const int n = max(0, min(kVec, p.vocab - at));
+            *bits &= (1u << n) - 1;
+#pragma unroll
+            for (int i = 0; i < kVec; i++)
+                (*raw)[i] = i < n ? v.x[at + i] : static_cast<T>(0.0f);
+        }
+    };
+    auto values = [&](const Raw &raw, uint32_t bits, auto all, float x[kVec]) {
+#pragma unroll
+        for (int i = 0; i < kVec; i++) {
+            x[i] = widen(raw[i]);
+            if constexpr (!decltype(all)::value)
+                x[i] = (bits >> i) & 1 ? x[i] : -__builtin_inff();
+        }
+    };
+    auto largest = [&](const float x[kVec]) {
+        float a = fmaxf(x[0], x[1]);
+#pragma unroll
+        for (int i = 2; i < kVec; i++)
+            a = fmaxf(a, x[i]);
+        return a;
+    };
+    auto take = [&](int t, const Raw &raw, uint32_t bits, auto all) {
+        float x[kVec];
+        values(raw, bits, all, x);
+        const int at = t * kTile + lane * kVec;
+        const float top = largest(x);
+        if (__ballot(top > limit)) {
+            const float m = fmaxf(w.m, wave_max(top));
+            const float delta = (w.m - m) * v.k, f = __builtin_amdgcn_exp2f(delta);
+            w.t = f > 0.0f ? f * (w.t + delta * w.s) : 0.0f * w.t;
+            w.s *= f;
+            w.m = m;
+            limit = m + 16.0f / v.k;
+        }
+        const float low = at < v.token ? (at + kVec <= v.token ? mine_low : mine_high) : mine_high;
+        int before = 0;
+#pragma unroll
+        for (int i = 0; i < kVec; i++) {
+            const float d = (x[i] - w.m) * v.k;
+            const float e = __builtin_amdgcn_exp2f(d);
+            w.s += e;
+            w.t += e * fmaxf(d, -1e30f);  // d may be -inf
+            before += __popcll(__ballot(x[i] > low));
+        }
+        w.before += before;
+        if constexpr (TOP) {
+            if (__ballot(top >= c.gate)) {
+#pragma unroll
+                for (int i = 0; i < kVec; i++) {
+                    const uint64_t key = order_key(x[i], at + i);
+                    c.insert(x[i] < __builtin_inff() && key > c.floor, key, p.top, lane);
+                }
+            }
+        }
+    };
+
+    for (int t0 = first + wave; t0 < end; t0 += kLogprobWaves * kInFlight) {
+        Raw raw[kInFlight];
+        uint32_t bits[kInFlight];
+#pragma unroll
+        for (int u = 0; u < kInFlight; u++)
+            if (t0 + u * kLogprobWaves < end)
+                fetch(t0 + u * kLogprobWaves, &raw[u], &bits[u]);
+        if (TOP && t0 == first + wave) {
+            // a first floor: of the lanes' largest logits of this round, the top-th largest
+            // (that many tokens are at or above it)
+            float best = -__builtin_inff();
+#pragma unroll
+            for (int u = 0; u < kInFlight; u++)
+                if (t0 + u * kLogprobWaves < end) {
+                    float x[kVec];
+                    values(raw[u], bits[u], std::false_type(), x);
+                    best = fmaxf(best, largest(x));
+                }
+            int above = 0;  // lanes before this one in the order of (best, lane)
+            for (int j = 0; j < kWaveLanes; j++) {
+                const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(best), j));
+                above += o > best || (o == best && j < lane);
+            }
+            const uint64_t at = __ballot(above == p.top - 1);
+            const float floor = at ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(best), __builtin_ctzll(at)))
+                                   : -__builtin_inff();
+            c.gate = fmaxf(floor, kLowest);
+            // keys of the floor's own value pass, those of -inf do not
+            c.floor = floor > -__builtin_inff() ? (static_cast<uint64_t>(order_word(floor)) << 32) - 1
+                                                : (static_cast<uint64_t>(order_word(-__builtin_inff())) << 32) | 0xFFFFFFFFu;
+        }
+#pragma unroll
+        for (int u = 0; u < kInFlight; u++) {
+            const int t = t0 + u * kLogprobWaves;
+            if (t >= end)
+                break;
+            if (!MASK && t < whole)
+                take(t, raw[u], bits[u], std::true_type());
+            else
+                take(t, raw[u], bits[u], std::false_type());
+        }
+    }
+
+    // the workgroup's sums and candidates
+    w.s = wave_sum(w.s);
+    w.t = wave_sum(w.t);
+    if (lane == 0) {
+        wave_sums[wave] = w;
+        floors[wave] = c.floor;
+    }
+    if (threadIdx.x == 0)
+        merged_n = 0;
+    __syncthreads();
+    Sums r = wave_sums[0];
+#pragma unroll
+    for (int i = 1; i < kLogprobWaves; i++)
+        r = join(r, wave_sums[i], v.k);
+    // the first p.top of merged[0 .. n) to their places
+    auto place = [&](int n, auto out) {
+        for (int i = threadIdx.x; i < n; i += kLogprobThreads) {
+            const uint64_t key = merged[i];
+            int at = 0;
+            for (int j = 0; j < n; j++)
+                at += merged[j] > key;
+            if (at < p.top)
+                out(at, key);
+        }
+        for (int i = n + static_cast<int>(threadIdx.x); i < p.top; i += kLogprobThreads)
+            out(i, static_cast<uint64_t>(0));
+    };
+    if constexpr (TOP) {
+        // the best of the waves' floors holds for all
+        uint64_t floor = floors[0];
+#pragma unroll
+        for (int i = 1; i < kLogprobWaves; i++)
+            floor = max(floor, floors[i]);
+        for (int i = lane; i < c.n; i += kWaveLanes) {
+            const uint64_t key = c.list[i];
+            if (key >= floor)
+                merged[atomicAdd(&merged_n, 1)] = key;
+        }
+        __syncthreads();
+    }
+    const bool bad_sum = r.s != r.s;
+    if (sp.segments == 1) {
+        const bool bad = v.bad || bad_sum;
+        const float logs = __builtin_amdgcn_logf(r.s) * 0.693147180559945309f;
+        if (threadIdx.x == 0)
+            write_row(p, row, v, r, mine, bad, logs);
+        if constexpr (TOP)
+            place(merged_n, [&](int at, uint64_t key) { write_alternative(p, row, at, key, r, v.inv, bad, logs); });
+        return;
+    }
+
+    // Several workgroups per row: each leaves its share in the workspace, and the last one
+    // to do so joins them. Shares and ticket go to the point where all dies meet: stores
+    // and loads of device scope around a release and an acquire.
+    const int64_t base = row * sp.segments;
+    auto put = [](auto *at, auto value) { __hip_atomic_store(at, value, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+    auto get = [](auto *at) { return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
     if (threadIdx.x == 0) {
-        const float nan = __builtin_nanf("");
-        p.logprob[row] = bad ? nan : mine_key ? (mine - m) / temp - ls : -__builtin_inff();
-        p.entropy[row] = bad ? nan : best ? ls - t / s : 0.0f;
-        p.rank[row] = bad || !mine_key ? -1 : before;
+        Sums *at = sp.sums + base + segment;
+        put(&at->m, r.m);
+        put(&at->s, r.s);
+        put(&at->t, r.t);
+        put(&at->before, r.before);
     }
-    for (int j = 0; j < p.top; j++) {
-        if (threadIdx.x == 0) {
-            p.top_tokens[row * p.top + j] = bad || !best ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-            p.top_logprobs[row * p.top + j] = bad    ? __builtin_nanf("")
-                                              : best ? (key_value(best) - m) / temp - ls
-                                                     : -__builtin_inff();
-        }
-        uint64_t next = 0;
-        for (int i = threadIdx.x; i < p.vocab; i += kLogprobThreads) {
-            if (!listed(i))
-                continue;
-            const float v = widen(x[i]);
-            if (!(v > -__builtin_inff()))
-                continue;
-            const uint64_t key = order_key(v, i);
-            if (key < best)
-                next = max_k(next, key);
-        }
-        best = block_reduce(next, ksum, max_k);
+    if constexpr (TOP)
+        place(merged_n, [&](int at, uint64_t key) { put(sp.keys + (base + segment) * p.top + at, key); });
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t done = __hip_atomic_fetch_add(sp.tickets + row, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        last = done + 1 == static_cast<uint32_t>(sp.segments);
+        if (last)
+            put(sp.tickets + row, 0u);
+        merged_n = 0;
     }
+    __syncthreads();
+    if (!last)
+        return;
+    __threadfence();
+    if (wave == 0) {
+        Sums mine_part = {kLowest, 0.0f, 0.0f, 0};
+        if (lane < sp.segments) {
+            Sums *at = sp.sums + base + lane;
+            mine_part = {get(&at->m), get(&at->s), get(&at->t), get(&at->before)};
+        }
+        // the order of the joins is fixed: by lane
+#pragma unroll
+        for (int d = 1; d < kWaveLanes; d *= 2) {
+            const Sums o = {__shfl_xor(mine_part.m, d), __shfl_xor(mine_part.s, d), __shfl_xor(mine_part.t, d),
+                            __shfl_xor(mine_part.before, d)};
+            mine_part = lane & d ? join(o, mine_part, v.k) : join(mine_part, o, v.k);
+        }
+        if (lane == 0)
+            total = mine_part;
+    }
+    if constexpr (TOP) {
+        // a segment whose first key is not among the `top` first keys has no alternative, so
+        // at most top * top keys are left (with fewer segments than that: all of theirs)
+        if (wave == 1) {
+            const uint64_t head = lane < sp.segments ? get(sp.keys + (base + lane) * p.top) : 0;
+            int at = 0;
+            for (int j = 0; j < sp.segments; j++) {
+                const uint64_t o = (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(head >> 32), j)) << 32) |
+                                   static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(head), j));
+                at += o > head || (o == head && j < lane);
+            }
+            const uint64_t here = __ballot(at == p.top - 1 && lane < sp.segments);
+            if (lane == (here ? __builtin_ctzll(here) : 0))
+                floors[0] = here ? head : 0;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < sp.segments * p.top; i += kLogprobThreads) {
+            const uint64_t key = get(sp.keys + base * p.top + i);
+            if (key != 0 && key >= floors[0])
+                merged[atomicAdd(&merged_n, 1)] = key;
+        }
+    }
+    __syncthreads();
+    r = total;
+    const bool bad = v.bad || r.s != r.s;
+    const float logs = __builtin_amdgcn_logf(r.s) * 0.693147180559945309f;
+    if (threadIdx.x == 0)
+        write_row(p, row, v, r, mine, bad, logs);
+    if constexpr (TOP)
+        place(merged_n, [&](int at, uint64_t key) { write_alternative(p, row, at, key, r, v.inv, bad, logs); });
+}
+
+template <typename T>
+const void *logprob_fn(bool mask, bool top) {
+    return mask ? (top ? reinterpret_cast<const void *>(&logprob_kernel<T, true, true>)
+                       : reinterpret_cast<const void *>(&logprob_kernel<T, true, false>))
+                : (top ? reinterpret_cast<const void *>(&logprob_kernel<T, false, true>)
+                       : reinterpret_cast<const void *>(&logprob_kernel<T, false, false>));
+}
+
+// Segments of a row and tiles per segment.
+void split(int64_t rows, int64_t vocab, int32_t *segments, int32_t *per) {
+    const int64_t tiles = (vocab + kTile - 1) / kTile;
+    int64_t s = rows < kSplitBelow ? (kSplitBelow + rows - 1) / rows : 1;
+    // a segment has a tile for each wave
+    s = std::min<int64_t>({s, kMostSegments, std::max<int64_t>(1, tiles / kLogprobWaves)});
+    *per = static_cast<int32_t>(std::max<int64_t>(1, (tiles + s - 1) / s));
+    *segments = static_cast<int32_t>(std::max<int64_t>(1, (tiles + *per - 1) / *per));
 }
 
 }  // namespace
 
+// The tickets come first, at a fixed size: what one call uses for shares is never
+// another's ticket.
+int64_t logprobs_workspace(int64_t rows, int64_t vocab, int64_t top) {
+    int32_t s, per;
+    split(rows, vocab, &s, &per);
+    return s == 1 ? 0 : 4 * kSplitBelow + rows * s * static_cast<int64_t>(sizeof(Sums) + 8 * top);
+}
+
 int launch_logprobs(const LogprobParams &p, int dtype, void *stream) {
-    const void *fn = dtype == SSU_F32   ? reinterpret_cast<const void *>(&logprob_kernel<float>)
-                     : dtype == SSU_F16 ? reinterpret_cast<const void *>(&logprob_kernel<_Float16>)
-                                        : reinterpret_cast<const void *>(&logprob_kernel<__bf16>);
+    Split sp = {};
+    split(p.rows, p.vocab, &sp.segments, &sp.tiles);
+    if (sp.segments > 1) {
+        sp.tickets = reinterpret_cast<uint32_t *>(p.workspace);
+        sp.sums = reinterpret_cast<Sums *>(p.workspace + 4 * kSplitBelow);
+        sp.keys = reinterpret_cast<uint64_t *>(sp.sums + p.rows * sp.segments);
+    }
+    if (p.rows * sp.segments > INT32_MAX)
+        return static_cast<int>(hipErrorInvalidValue);
+    const bool mask = p.mask != nullptr, top = p.top > 0;
+    const void *fn = dtype == SSU_F32   ? logprob_fn<float>(mask, top)
+                     : dtype == SSU_F16 ? logprob_fn<_Float16>(mask, top)
+                                        : logprob_fn<__bf16>(mask, top);
     LogprobParams pc = p;
-    void *args[] = {&pc};
-    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(p.rows)), dim3(kLogprobThreads), args, 0,
+    void *args[] = {&pc, &sp};
+    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(p.rows * sp.segments)), dim3(kLogprobThreads), args, 0,
                                             static_cast<hipStream_t>(stream)));
 }
 

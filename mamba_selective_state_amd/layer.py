@@ -96,17 +96,17 @@ def ssu_token_logprobs(args, workspace=None, workspace_bytes=0, stream=None):
 _workspaces = {}
 
 
-def _workspace(device, stream, nbytes):
-    """The cached workspace of (`device`, `stream`), grown to at least `nbytes`,
-    as (pointer, bytes). One per stream, allocated on it: calls on one stream
+def _workspace(what, device, stream, nbytes, make=torch.empty):
+    """The cached workspace of an operator on (`device`, `stream`), grown to at least
+    `nbytes`, as (pointer, bytes). One per stream, allocated on it: calls on one stream
     are ordered, so they can share it, and the caching allocator hands a
     grown one's predecessor out again only behind the kernels that used it."""
     if nbytes == 0:
         return None, 0
-    key = (device, stream)
+    key = (what, device, stream)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = make(nbytes, dtype=torch.uint8, device=device)
         _workspaces[key] = ws
     return ws.data_ptr(), ws.numel()
 
@@ -234,7 +234,8 @@ def mx_linear(x, weight, weight_scale, bias=None, activation="mxfp8", out=None, 
     args = make_mx_linear_args(_rows(x, "x"), weight, weight_scale, _rows(out, "out"),
                                _rows(x_scale, "x_scale"), bias, fmt)
     stream = torch.cuda.current_stream(x.device).cuda_stream
-    ssu_mx_linear(args, *_workspace(x.device, stream, ssu_mx_linear_workspace_bytes(args)), stream)
+    ssu_mx_linear(args, *_workspace("mx_linear", x.device, stream,
+                                    ssu_mx_linear_workspace_bytes(args)), stream)
     return out
 
 
@@ -280,6 +281,8 @@ def token_logprobs(logits, tokens, top=0, mask=None, temperature=None):
     args = make_logprob_args(logits, tokens, logprob, entropy, rank, top_tokens, top_logprobs, mask,
                              temperature)
     stream = torch.cuda.current_stream(dev).cuda_stream
-    ssu_token_logprobs(args, *_workspace(dev, stream, ssu_token_logprobs_workspace_bytes(args)),
-                       stream)
+    # its tickets start at zero and every call leaves them there
+    ws = _workspace("token_logprobs", dev, stream, ssu_token_logprobs_workspace_bytes(args),
+                    torch.zeros)
+    ssu_token_logprobs(args, *ws, stream)
     return TokenLogprobs(logprob, entropy, rank, top_tokens, top_logprobs)
