@@ -170,19 +170,49 @@ struct Candidates {
             gate = fmaxf(gate, word_value(fw));
         }
     }
-    // Element `i` of an access at `at` (this lane's first index), `x` its logit.
-    __device__ __forceinline__ void offer(float x, uint32_t at, int i, int top, int lane) {
-        uint64_t todo = __ballot(x >= gate && x < __builtin_inff());
-        if (todo == 0)
-            return;
-        const uint32_t w = order_word(x);
-        auto before_floor = [&] { return w > floor_word || (w == floor_word && at + i < floor_index); };
-        todo &= __ballot(before_floor());
-        while (todo) {
-            const int from = __builtin_ctzll(todo);
-            insert(__builtin_amdgcn_readlane(w, from), __builtin_amdgcn_readlane(at, from) + i, top, lane);
-            todo &= ~(1ull << from);
-            todo &= __ballot(before_floor());
+    // An access's logits (destroyed), the lane's first index `at`: the lanes' largest ones are
+    // offered and taken out until none is left that could enter.
+    __device__ __forceinline__ void offer(float x[kVec], uint32_t at, int top, int lane) {
+        while (true) {
+            float best = x[0];
+            uint32_t i = 0;
+#pragma unroll
+            for (int j = 1; j < kVec; j++) {
+                const bool larger = x[j] > best;
+                best = larger ? x[j] : best;
+                i = larger ? j : i;
+            }
+            const uint32_t w = order_word(best);
+            auto before_floor = [&] { return w > floor_word || (w == floor_word && at + i < floor_index); };
+            const bool pass = best >= gate && best < __builtin_inff() && before_floor();
+            uint64_t todo = __ballot(pass);
+            if (todo == 0)
+                return;
+            while (todo) {
+                const int from = __builtin_ctzll(todo);
+                insert(__builtin_amdgcn_readlane(w, from), __builtin_amdgcn_readlane(at + i, from), top, lane);
+                todo &= todo - 1;
+                todo &= __ballot(before_floor());
+            }
+#pragma unroll
+            for (int j = 0; j < kVec; j++)
+                x[j] = pass && i == static_cast<uint32_t>(j) ? -__builtin_inff() : x[j];
+        }
+    }
+    // A bound before anything has entered, from each lane's largest logit: at least `top` lanes
+    // are at or above it (their words' leading 16 bits, found bit by bit).
+    __device__ __forceinline__ void bound(float best, int top) {
+        const uint32_t w = order_word(best);
+        uint32_t b = 0;
+#pragma unroll
+        for (int bit = 31; bit >= 16; bit--) {
+            const uint32_t t = b | (1u << bit);
+            if (__popcll(__ballot(w >= t)) >= top)
+                b = t;
+        }
+        if (b > 0x007FFFFFu) {  // above -inf's word
+            floor_word = b;     // with the index that stands behind every other
+            gate = word_value(b);
         }
     }
 };
@@ -207,7 +237,7 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
     __shared__ uint64_t merged[TOP ? kMergeCand : 1];
     __shared__ uint64_t floor;  // of the joined segments
     __shared__ int merged_n, last;
-    __shared__ volatile float floors[kLogprobWaves];  // what a wave's top-th token is at least
+    __shared__ float floors[kLogprobWaves];  // what a wave's top-th token is at least
     const int lane = threadIdx.x % kWaveLanes, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
     const int64_t row = blockIdx.x / sp.segments;
     const int segment = static_cast<int>(blockIdx.x % sp.segments);
@@ -317,13 +347,11 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
         w.before += before;
         if constexpr (TOP) {
             if (__ballot(top >= c.gate)) {
-#pragma unroll
-                for (int i = 0; i < kVec; i++)
-                    c.offer(x[i], at, i, p.top, lane);
+                c.offer(x, at, p.top, lane);
                 if (c.floor_word != 0) {
                     const float floor = word_value(c.floor_word);
                     if (lane == 0)
-                        floors[wave] = floor;
+                        __hip_atomic_store(&floors[wave], floor, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
                     // accesses come in the order of their indices: what only equals a token of
                     // this wave stays behind it from here on
                     if (c.floor_index != 0xFFFFFFFFu)
@@ -338,23 +366,7 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
         if constexpr (TOP) {
 #pragma unroll
             for (int i = 0; i < kLogprobWaves; i++)
-                c.gate = fmaxf(c.gate, floors[i]);
-        }
-    };
-    // a first floor, of a lane's largest logit each: the top-th largest of them (that many
-    // tokens are at or above it)
-    auto first_floor = [&](float best) {
-        int above = 0;  // lanes before this one in the order of (best, lane)
-        for (int j = 0; j < kWaveLanes; j++) {
-            const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(best), j));
-            above += o > best || (o == best && j < lane);
-        }
-        const uint64_t at = __ballot(above == p.top - 1);
-        const float bound = at ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(best), __builtin_ctzll(at)))
-                               : -__builtin_inff();
-        if (bound > -__builtin_inff() && bound < __builtin_inff()) {
-            c.gate = bound;
-            c.floor_word = order_word(bound);  // with the index that stands behind every other
+                c.gate = fmaxf(c.gate, __hip_atomic_load(&floors[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
         }
     };
     if (TOP && t < end) {
@@ -367,39 +379,26 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
             values(raw[u], bits[u], std::false_type(), x);
             best = fmaxf(best, largest(x));
         }
-        first_floor(best);
+        c.bound(best, p.top);
     }
     while (round) {
-        const int next = t + kInFlight * kLogprobWaves;
-        round = next + (kInFlight - 1) * kLogprobWaves < whole_end;
-        Raw ahead[kInFlight];
-        uint32_t ahead_bits[kInFlight];
-        if (round)
-            fetch_round(next, ahead, ahead_bits);
-        else if (next < end)
-            fetch_one(next, ahead, ahead_bits);
         read_floors();
 #pragma unroll
         for (int u = 0; u < kInFlight; u++)
             take(t + u * kLogprobWaves, raw[u], bits[u], Every());
-#pragma unroll
-        for (int u = 0; u < kInFlight; u++) {
-            raw[u] = ahead[u];
-            bits[u] = ahead_bits[u];
-        }
-        t = next;
+        t += kInFlight * kLogprobWaves;
+        round = t + (kInFlight - 1) * kLogprobWaves < whole_end;
+        if (round)
+            fetch_round(t, raw, bits);
+        else if (t < end)
+            fetch_one(t, raw, bits);
     }
     while (t < end) {
-        const int next = t + kLogprobWaves;
-        Raw ahead;
-        uint32_t ahead_bits = 0;
-        if (next < end)
-            fetch_one(next, &ahead, &ahead_bits);
         read_floors();
         take(t, raw[0], bits[0], std::false_type());
-        raw[0] = ahead;
-        bits[0] = ahead_bits;
-        t = next;
+        t += kLogprobWaves;
+        if (t < end)
+            fetch_one(t, raw, bits);
     }
 
     // the workgroup's sums and candidates
