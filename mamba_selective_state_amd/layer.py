@@ -4,14 +4,17 @@ around the state update"): argument marshalling only, like ssu.py.
 Low level, same names as the C ABI: ssu_add_rms_norm, ssu_mx_quantize,
 ssu_mx_linear, ssu_token_logprobs. High level: add_rms_norm, mx_quantize,
 mx_linear and token_logprobs, which take torch tensors and allocate what they
-return.
+return; the marshalling of the three that a decode step calls is in C++
+(csrc/ssu_torch.cpp), since their kernels take no longer than it takes in
+Python. Without that module, as without the library, the import fails.
 """
 import collections
 import ctypes
 
 import torch
 
-from .ssu import OK, SsuTensor, _lib, _raise, tensor_desc
+from .ssu import OK, SsuError, SsuTensor, _lib, _raise, tensor_desc
+from . import _ssu_torch as _native
 
 FORMAT_SAME, FORMAT_MXFP4, FORMAT_MXFP8 = 0, 4, 8
 TOP_MAX = 32  # SSU_TOP_MAX
@@ -49,6 +52,16 @@ _lib.ssu_token_logprobs_workspace_bytes.restype = ctypes.c_int64
 _lib.ssu_token_logprobs.argtypes = [ctypes.POINTER(SsuLogprobArgs), ctypes.c_void_p, ctypes.c_int64,
                                     ctypes.c_void_p]
 _lib.ssu_token_logprobs.restype = ctypes.c_int
+
+
+_native.set_error_type(SsuError)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(t):
+    """The handle of the current stream of a tensor's GPU (0 for a tensor that has none: the
+    operators refuse it)."""
+    return _raw_stream(t.get_device()) if t.is_cuda else 0
 
 
 def _stream(stream):
@@ -91,24 +104,6 @@ def ssu_token_logprobs(args, workspace=None, workspace_bytes=0, stream=None):
     st = _lib.ssu_token_logprobs(ctypes.byref(args), workspace, workspace_bytes, _stream(stream))
     if st != OK:
         _raise(st, "ssu_token_logprobs")
-
-
-_workspaces = {}
-
-
-def _workspace(what, device, stream, nbytes, make=torch.empty):
-    """The cached workspace of an operator on (`device`, `stream`), grown to at least
-    `nbytes`, as (pointer, bytes). One per stream, allocated on it: calls on one stream
-    are ordered, so they can share it, and the caching allocator hands a
-    grown one's predecessor out again only behind the kernels that used it."""
-    if nbytes == 0:
-        return None, 0
-    key = (what, device, stream)
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = make(nbytes, dtype=torch.uint8, device=device)
-        _workspaces[key] = ws
-    return ws.data_ptr(), ws.numel()
 
 
 def _format(name):
@@ -165,21 +160,11 @@ def add_rms_norm(x, weight, residual=None, gate=None, groups=1, eps=1e-5, out_fo
     dtype. Outputs are allocated unless given; residual_out may be residual
     and out may be x. u is not rounded before the norm."""
     fmt = FORMAT_SAME if out_format is None else _format(out_format)
-    if out is None:
-        if fmt == FORMAT_SAME:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            out = torch.empty(_mx_shapes(x.shape, fmt)[0], dtype=torch.uint8, device=x.device)
-    if out_scales is None and fmt != FORMAT_SAME:
-        out_scales = torch.empty(_mx_shapes(x.shape, fmt)[1], dtype=torch.uint8, device=x.device)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty(residual.shape, dtype=residual.dtype, device=x.device)
-    args = make_norm_args(_rows(x, "x"), weight, _rows(out, "out"), _rows(out_scales, "out_scales"),
-                          _rows(residual, "residual"), _rows(residual_out, "residual_out"),
-                          _rows(gate, "gate"), groups, eps, fmt)
-    ssu_add_rms_norm(args, torch.cuda.current_stream(x.device).cuda_stream)
-    y = out if fmt == FORMAT_SAME else (out, out_scales)
-    return y if residual is None else (y, residual_out)
+    y, scales, u = _native.add_rms_norm(x, weight, residual, gate, groups, eps, fmt, out,
+                                        out_scales, residual_out, _stream_of(x))
+    if scales is not None:
+        y = (y, scales)
+    return y if residual is None else (y, u)
 
 
 def mx_quantize(x, out_format="mxfp4", codes=None, scales=None):
@@ -196,7 +181,7 @@ def mx_quantize(x, out_format="mxfp4", codes=None, scales=None):
     dev = x.device
     ssu_mx_quantize(tensor_desc(_rows(x, "x"), dev), tensor_desc(_rows(codes, "codes"), dev),
                     tensor_desc(_rows(scales, "scales"), dev), fmt,
-                    torch.cuda.current_stream(dev).cuda_stream)
+                    _stream_of(x))
     return codes, scales
 
 
@@ -227,16 +212,10 @@ def mx_linear(x, weight, weight_scale, bias=None, activation="mxfp8", out=None, 
         fmt = FORMAT_MXFP4 if four else FORMAT_MXFP8
     else:
         fmt = _format(activation)
-    if out is None:
-        if out_dtype is None:
-            out_dtype = torch.bfloat16 if x_scale is not None else x.dtype
+    like = x if x_scale is None else None  # of the result's dtype; None: bfloat16
+    if out is None and out_dtype is not None and out_dtype != (x.dtype if like is x else torch.bfloat16):
         out = torch.empty(x.shape[:-1] + weight.shape[:1], dtype=out_dtype, device=x.device)
-    args = make_mx_linear_args(_rows(x, "x"), weight, weight_scale, _rows(out, "out"),
-                               _rows(x_scale, "x_scale"), bias, fmt)
-    stream = torch.cuda.current_stream(x.device).cuda_stream
-    ssu_mx_linear(args, *_workspace("mx_linear", x.device, stream,
-                                    ssu_mx_linear_workspace_bytes(args)), stream)
-    return out
+    return _native.mx_linear(x, x_scale, weight, weight_scale, bias, fmt, out, like, _stream_of(x))
 
 
 TokenLogprobs = collections.namedtuple(
@@ -267,22 +246,5 @@ def token_logprobs(logits, tokens, top=0, mask=None, temperature=None):
     alternatives are -1 and -inf. Returns a TokenLogprobs of float32 logprob and
     entropy, int32 rank, and int32 top_tokens and float32 top_logprobs
     [rows, top] (None without top)."""
-    dev = logits.device
-    rows = tokens.shape[0]
-    logprob = torch.empty(rows, dtype=torch.float32, device=dev)
-    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
-    rank = torch.empty(rows, dtype=torch.int32, device=dev)
-    top_tokens = top_logprobs = None
-    if top:
-        top_tokens = torch.empty((rows, top), dtype=torch.int32, device=dev)
-        top_logprobs = torch.empty((rows, top), dtype=torch.float32, device=dev)
-    if mask is not None and mask.shape[0] == 1 and rows != 1:
-        mask = mask.expand(rows, -1)
-    args = make_logprob_args(logits, tokens, logprob, entropy, rank, top_tokens, top_logprobs, mask,
-                             temperature)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    # its tickets start at zero and every call leaves them there
-    ws = _workspace("token_logprobs", dev, stream, ssu_token_logprobs_workspace_bytes(args),
-                    torch.zeros)
-    ssu_token_logprobs(args, *ws, stream)
-    return TokenLogprobs(logprob, entropy, rank, top_tokens, top_logprobs)
+    return TokenLogprobs(*_native.token_logprobs(logits, tokens, mask, temperature, top,
+                                                 _stream_of(logits)))
