@@ -48,6 +48,37 @@ __device__ __forceinline__ void store8(T *dst, int n, const float v[8]) {
             dst[i] = narrow<T>(v[i]);
 }
 
+// Sum over the wave, the same in every lane; all lanes must be active.
+__device__ __forceinline__ float wave64_sum(float v) {
+    const int s = __float_as_int(row16_sum(v));
+    return (__int_as_float(__builtin_amdgcn_readlane(s, 0)) + __int_as_float(__builtin_amdgcn_readlane(s, 16))) +
+           (__int_as_float(__builtin_amdgcn_readlane(s, 32)) + __int_as_float(__builtin_amdgcn_readlane(s, 48)));
+}
+
+// Codes of four finite values over 2^k (see e4m3_codes4 and e2m1_codes4, whose care for NaN
+// elements a finite block does without).
+template <int FORMAT>
+__device__ __forceinline__ uint32_t finite_codes4(const float v[4], int k) {
+    const float X = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+    if constexpr (FORMAT == SSU_FORMAT_MXFP8) {
+        const float lim = 448.0f * X;  // the conversion makes NaN of what lies beyond
+        float c[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            c[i] = __builtin_amdgcn_fmed3f(v[i], -lim, lim);
+        typedef short short2_t __attribute__((ext_vector_type(2)));
+        short2_t r = {0, 0};
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c[0], c[1], X, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c[2], c[3], X, true);
+        return __builtin_bit_cast(uint32_t, r);
+    } else {
+        uint32_t r = 0;  // the conversion saturates
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], X, 0);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], X, 1);
+        return r & 0xFFFFu;
+    }
+}
+
 // Four consecutive lanes hold a block of 32 values, eight each; every lane
 // gives the codes of its eight (MXFP8: two words, MXFP4: the first) and the
 // block's scale byte. The largest magnitude is taken over the bit patterns, where
@@ -63,11 +94,10 @@ __device__ __forceinline__ uint32_t mx_block(const float v[8], uint32_t code[2])
     a = max(a, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(a), 0x4E, 0xF, 0xF, false)));
     const float amax = __uint_as_float(a);
     const int k = FORMAT == SSU_FORMAT_MXFP8 ? mx8_exponent(amax) : mx4_exponent(amax);
-    if constexpr (FORMAT == SSU_FORMAT_MXFP8) {
-        code[0] = e4m3_codes4(v, k);
-        code[1] = e4m3_codes4(v + 4, k);
-    } else {
-        code[0] = e2m1_codes4(v, k) | (e2m1_codes4(v + 4, k) << 16);
+    code[0] = finite_codes4<FORMAT>(v, k);
+    code[1] = finite_codes4<FORMAT>(v + 4, k);
+    if constexpr (FORMAT == SSU_FORMAT_MXFP4) {
+        code[0] |= code[1] << 16;
         code[1] = 0;
     }
     const bool finite = a < 0x7F800000u;

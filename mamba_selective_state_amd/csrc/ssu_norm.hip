@@ -1,5 +1,9 @@
 // Gated, residual-adding RMS norm (ssu_add_rms_norm): per part of a row,
 //   u = x * silu(gate) + residual,  y = u * rsqrt(mean u^2 + eps) * weight.
+// The bytes bound it: every input is read once, u stays in registers between the sum
+// and the outputs, and the MX codes are made where y is.
+#include <algorithm>
+
 #include "ssu_layer_device.h"
 
 namespace ssu {
@@ -7,103 +11,267 @@ namespace {
 
 constexpr int kNormThreads = 256;
 
-// Eight values of u at `at` of row `row` (n of them exist).
+// z * sigmoid(z) to within 2 ulps: the codes of an MX output go by y's last bits, and the plain
+// exp2(z log2 e) loses |z| / 2 of them. log2 e is taken in two parts, the reciprocal is
+// refined once. Below -87 the result is under 1e-36 and taken as at -87.
+__device__ __forceinline__ float silu_exact(float z) {
+    constexpr float kHi = 1.44269504088896341f, kLo = 1.925963033500011e-8f;
+    z = z < -87.0f ? -87.0f : z;  // a NaN stays
+    const float c = fminf(z, 87.0f);
+    const float hi = -c * kHi;
+    const float lo = fmaf(-c, kHi, -hi) - c * kLo;
+    const float e = __builtin_amdgcn_exp2f(hi);
+    const float d = 1.0f + fmaf(e * lo, 0.693147180559945309f, e);
+    const float r = __builtin_amdgcn_rcpf(d);
+    return z * fmaf(fmaf(-d, r, 1.0f), r, r);
+}
+
+// Eight elements of a row as loaded.
 template <typename T>
-__device__ __forceinline__ void load_u(const NormParams &p, int64_t row, int at, int n, float u[8]) {
-    load8(static_cast<const T *>(p.x) + row * p.x_s + at, n, u);
-    if (p.gate) {
-        float z[8];
-        load8(static_cast<const T *>(p.gate) + row * p.gate_s + at, n, z);
+struct Raw8 {
+    typedef T Vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+    Vec v;
+    // the first n (at most 8) from src, zeros after
+    __device__ __forceinline__ void load(const T *src, int n) {
+        if (n >= 8) {
+            v = *reinterpret_cast<const Vec *>(src);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            u[i] *= z[i] / (1.0f + __expf(-z[i]));
+            for (int i = 0; i < 8; i++)
+                v[i] = i < n ? src[i] : static_cast<T>(0.0f);
+        }
     }
-    if (p.residual) {
-        float r[8];
-        if (p.res_f32)
-            load8(static_cast<const float *>(p.residual) + row * p.res_s + at, n, r);
+};
+// The same of a tensor that has the activations' type or is f32.
+template <typename T>
+struct Raw8Or32 {
+    Raw8<T> t;
+    Raw8<float> f;
+    __device__ __forceinline__ void load(const void *base, bool f32, int64_t at, int n) {
+        if (f32)
+            f.load(static_cast<const float *>(base) + at, n);
         else
-            load8(static_cast<const T *>(p.residual) + row * p.res_s + at, n, r);
+            t.load(static_cast<const T *>(base) + at, n);
+    }
+    __device__ __forceinline__ float get(bool f32, int i) const { return f32 ? f.v[i] : widen(t.v[i]); }
+};
+
+template <typename T, int FORMAT>
+__device__ __forceinline__ void store_result(const NormParams &p, int64_t row, int at, int n, int lane, const float y[8]) {
+    if constexpr (FORMAT == SSU_FORMAT_SAME) {
+        store8(static_cast<T *>(p.out) + row * p.out_s + at, n, y);
+    } else {
+        uint32_t code[2];
+        const uint32_t s = mx_block<FORMAT>(y, code);
+        store_codes<FORMAT>(static_cast<uint8_t *>(p.out) + row * p.out_s, at, code);
+        if (lane % 4 == 0)
+            p.scales[(row * p.groups * p.part + at) / 32] = static_cast<uint8_t>(s);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_residual(const NormParams &p, int64_t row, int at, int n, const float u[8]) {
+    if (p.res_f32)
+        store8(static_cast<float *>(p.residual_out) + row * p.res_out_s + at, n, u);
+    else
+        store8(static_cast<T *>(p.residual_out) + row * p.res_out_s + at, n, u);
+}
+
+// LANES lanes per part, each with up to NV runs of eight elements in registers.
+template <typename T, int FORMAT, int LANES, int NV>
+__global__ __launch_bounds__(LANES < kNormThreads ? kNormThreads : LANES) void norm_kernel(const NormParams p) {
+    constexpr int kThreads = LANES < kNormThreads ? kNormThreads : LANES;
+    constexpr int kWaves = LANES / kWaveLanes;  // per part
+    const int64_t part = LANES < kNormThreads ? static_cast<int64_t>(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES
+                                              : static_cast<int64_t>(blockIdx.x);
+    if (part >= p.parts)
+        return;  // a whole wave: LANES is a multiple of 64
+    const int lane = threadIdx.x % LANES;
+    const int64_t row = part / p.groups;
+    const int first = static_cast<int>(part - row * p.groups) * p.part;
+    Raw8<T> x[NV], z[NV];
+    Raw8Or32<T> r[NV], g[NV];
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            u[i] += r[i];
+    for (int v = 0; v < NV; v++) {
+        const int i = (v * LANES + lane) * 8;
+        x[v].load(static_cast<const T *>(p.x) + row * p.x_s + first + i, p.part - i);
+    }
+    if (p.gate)
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            const int i = (v * LANES + lane) * 8;
+            z[v].load(static_cast<const T *>(p.gate) + row * p.gate_s + first + i, p.part - i);
+        }
+    if (p.residual)
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            const int i = (v * LANES + lane) * 8;
+            r[v].load(p.residual, p.res_f32, row * p.res_s + first + i, p.part - i);
+        }
+    // one run: the weights come with the rest; more: they are fetched (mostly from the caches)
+    // when the inputs' registers are free
+    if constexpr (NV == 1)
+        g[0].load(p.weight, p.weight_f32, first + lane * 8, p.part - lane * 8);
+    float u[NV][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            u[v][j] = widen(x[v].v[j]);
+        if (p.gate)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                u[v][j] *= silu_exact(widen(z[v].v[j]));
+        if (p.residual)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                u[v][j] += r[v].get(p.res_f32, j);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            ss = fmaf(u[v][j], u[v][j], ss);
+    }
+    ss = wave64_sum(ss);
+    if constexpr (kWaves > 1) {
+        __shared__ float sums[kWaves];
+        if (threadIdx.x % kWaveLanes == 0)
+            sums[threadIdx.x / kWaveLanes] = ss;
+        __syncthreads();
+        ss = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++)
+            ss += sums[w];
+    }
+    const float scale = 1.0f / sqrtf(ss / static_cast<float>(p.part) + p.eps);
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+        const int i = (v * LANES + lane) * 8, n = p.part - i;
+        if (n <= 0)
+            break;
+        if (p.residual)
+            store_residual<T>(p, row, first + i, n, u[v]);
+        if constexpr (NV > 1)
+            g[v].load(p.weight, p.weight_f32, first + i, n);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            y[j] = u[v][j] * scale * g[v].get(p.weight_f32, j);
+        store_result<T, FORMAT>(p, row, first + i, n, lane, y);
     }
 }
 
+// Parts that no workgroup's registers hold: the inputs are read again for the outputs.
+constexpr int kLongThreads = 1024;
 template <typename T, int FORMAT>
-__global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormParams p) {
-    __shared__ float sums[kNormThreads / kWaveLanes];
+__global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const NormParams p) {
+    __shared__ float sums[kLongThreads / kWaveLanes];
     const int64_t part = blockIdx.x;
     const int64_t row = part / p.groups;
-    const int first = static_cast<int>(part % p.groups) * p.part;
+    const int first = static_cast<int>(part - row * p.groups) * p.part;
     const int tid = threadIdx.x;
-    float ss = 0.0f;
-    for (int i = tid * 8; i < p.part; i += kNormThreads * 8) {
-        float u[8];
-        load_u<T>(p, row, first + i, min(8, p.part - i), u);
+    auto load_u = [&](int i, int n, float u[8]) {
+        Raw8<T> x;
+        x.load(static_cast<const T *>(p.x) + row * p.x_s + first + i, n);
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            ss += u[j] * u[j];
-    }
+            u[j] = widen(x.v[j]);
+        if (p.gate) {
+            x.load(static_cast<const T *>(p.gate) + row * p.gate_s + first + i, n);
 #pragma unroll
-    for (int d = 1; d < kWaveLanes; d *= 2)
-        ss += __shfl_xor(ss, d);
+            for (int j = 0; j < 8; j++)
+                u[j] *= silu_exact(widen(x.v[j]));
+        }
+        if (p.residual) {
+            Raw8Or32<T> r;
+            r.load(p.residual, p.res_f32, row * p.res_s + first + i, n);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                u[j] += r.get(p.res_f32, j);
+        }
+    };
+    float ss = 0.0f;
+    for (int i = tid * 8; i < p.part; i += kLongThreads * 8) {
+        float u[8];
+        load_u(i, p.part - i, u);
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            s = fmaf(u[j], u[j], s);
+        ss += s;
+    }
+    ss = wave64_sum(ss);
     if (tid % kWaveLanes == 0)
         sums[tid / kWaveLanes] = ss;
     __syncthreads();
     ss = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kNormThreads / kWaveLanes; w++)
+    for (int w = 0; w < kLongThreads / kWaveLanes; w++)
         ss += sums[w];
     const float scale = 1.0f / sqrtf(ss / static_cast<float>(p.part) + p.eps);
-    for (int i = tid * 8; i < p.part; i += kNormThreads * 8) {
-        const int n = min(8, p.part - i);
-        float u[8], g[8];
-        load_u<T>(p, row, first + i, n, u);
-        if (p.weight_f32)
-            load8(static_cast<const float *>(p.weight) + first + i, n, g);
-        else
-            load8(static_cast<const T *>(p.weight) + first + i, n, g);
-        if (p.residual) {
-            if (p.res_f32)
-                store8(static_cast<float *>(p.residual_out) + row * p.res_out_s + first + i, n, u);
-            else
-                store8(static_cast<T *>(p.residual_out) + row * p.res_out_s + first + i, n, u);
-        }
+    for (int i = tid * 8; i < p.part; i += kLongThreads * 8) {
+        const int n = p.part - i;
+        float u[8];
+        load_u(i, n, u);
+        Raw8Or32<T> g;
+        g.load(p.weight, p.weight_f32, first + i, n);
+        if (p.residual)
+            store_residual<T>(p, row, first + i, n, u);
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            u[j] = u[j] * scale * g[j];
-        if constexpr (FORMAT == SSU_FORMAT_SAME) {
-            store8(static_cast<T *>(p.out) + row * p.out_s + first + i, n, u);
-        } else {
-            uint32_t code[2];
-            const uint32_t s = mx_block<FORMAT>(u, code);
-            store_codes<FORMAT>(static_cast<uint8_t *>(p.out) + row * p.out_s, first + i, code);
-            if (tid % 4 == 0)
-                p.scales[(row * p.groups * p.part + first + i) / 32] = static_cast<uint8_t>(s);
-        }
+            u[j] = u[j] * scale * g.get(p.weight_f32, j);
+        store_result<T, FORMAT>(p, row, first + i, n, tid, u);
     }
 }
 
-template <typename T>
-const void *norm_fn(int format) {
-    switch (format) {
-    case SSU_FORMAT_MXFP8: return reinterpret_cast<const void *>(&norm_kernel<T, SSU_FORMAT_MXFP8>);
-    case SSU_FORMAT_MXFP4: return reinterpret_cast<const void *>(&norm_kernel<T, SSU_FORMAT_MXFP4>);
+struct NormShape {
+    int lanes, nv;  // nv 0: the long kernel
+};
+
+// Lanes per part. Many parts: the fewest lanes that keep a part in registers (no barrier
+// for up to 2048 elements). Few parts: as many lanes as have a run of eight each, for the time of
+// one part is then the time of the call.
+NormShape shape_for(int64_t parts, int part) {
+    const int runs = (part + 7) / 8;
+    constexpr NormShape kShapes[] = {{64, 1}, {64, 2}, {64, 4}, {256, 1}, {256, 2}, {256, 4}, {1024, 1}, {1024, 2}, {1024, 4}};
+    const bool many = parts >= 2048;
+    for (const NormShape &s : kShapes)
+        if (runs <= s.lanes * s.nv && (many ? !(s.lanes == 256 && s.nv == 1) : s.nv == 1 || s.lanes == 1024))
+            return s;
+    return {kLongThreads, 0};
+}
+
+template <typename T, int FORMAT>
+const void *norm_fn(NormShape s) {
+    switch (s.lanes * 8 + s.nv) {
+    case 64 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 64, 1>);
+    case 64 * 8 + 2: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 64, 2>);
+    case 64 * 8 + 4: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 64, 4>);
+    case 256 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 256, 1>);
+    case 256 * 8 + 2: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 256, 2>);
+    case 256 * 8 + 4: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 256, 4>);
+    case 1024 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 1024, 1>);
+    case 1024 * 8 + 2: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 1024, 2>);
+    case 1024 * 8 + 4: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 1024, 4>);
     }
-    return reinterpret_cast<const void *>(&norm_kernel<T, SSU_FORMAT_SAME>);
+    return reinterpret_cast<const void *>(&norm_long_kernel<T, FORMAT>);
+}
+template <typename T>
+const void *norm_fn(int format, NormShape s) {
+    return format == SSU_FORMAT_MXFP8   ? norm_fn<T, SSU_FORMAT_MXFP8>(s)
+           : format == SSU_FORMAT_MXFP4 ? norm_fn<T, SSU_FORMAT_MXFP4>(s)
+                                        : norm_fn<T, SSU_FORMAT_SAME>(s);
 }
 
 }  // namespace
 
 int launch_norm(const NormParams &p, int dtype, int format, void *stream) {
-    const void *fn = dtype == SSU_F32   ? norm_fn<float>(format)
-                     : dtype == SSU_F16 ? norm_fn<_Float16>(format)
-                                        : norm_fn<__bf16>(format);
+    const NormShape s = shape_for(p.parts, p.part);
+    const void *fn = dtype == SSU_F32   ? norm_fn<float>(format, s)
+                     : dtype == SSU_F16 ? norm_fn<_Float16>(format, s)
+                                        : norm_fn<__bf16>(format, s);
+    const int per = s.lanes < kNormThreads ? kNormThreads / s.lanes : 1;
     NormParams pc = p;
     void *args[] = {&pc};
-    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(p.parts)), dim3(kNormThreads), args, 0,
-                                            static_cast<hipStream_t>(stream)));
+    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>((p.parts + per - 1) / per)), dim3(s.lanes * per), args,
+                                            0, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace ssu
