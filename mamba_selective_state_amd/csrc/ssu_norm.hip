@@ -31,9 +31,14 @@ template <typename T>
 struct Raw8 {
     typedef T Vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
     Vec v;
-    // the first n (at most 8) from src, zeros after
+    // the first n (at most 8) from src, zeros after; WHOLE: n is at least 8 or not above 0
+    template <bool WHOLE>
     __device__ __forceinline__ void load(const T *src, int n) {
-        if (n >= 8) {
+        if constexpr (WHOLE) {
+            v = Vec{};
+            if (n > 0)
+                v = *reinterpret_cast<const Vec *>(src);
+        } else if (n >= 8) {
             v = *reinterpret_cast<const Vec *>(src);
         } else {
 #pragma unroll
@@ -47,19 +52,20 @@ template <typename T>
 struct Raw8Or32 {
     Raw8<T> t;
     Raw8<float> f;
+    template <bool WHOLE>
     __device__ __forceinline__ void load(const void *base, bool f32, int64_t at, int n) {
         if (f32)
-            f.load(static_cast<const float *>(base) + at, n);
+            f.template load<WHOLE>(static_cast<const float *>(base) + at, n);
         else
-            t.load(static_cast<const T *>(base) + at, n);
+            t.template load<WHOLE>(static_cast<const T *>(base) + at, n);
     }
     __device__ __forceinline__ float get(bool f32, int i) const { return f32 ? f.v[i] : widen(t.v[i]); }
 };
 
-template <typename T, int FORMAT>
+template <typename T, int FORMAT, bool WHOLE>
 __device__ __forceinline__ void store_result(const NormParams &p, int64_t row, int at, int n, int lane, const float y[8]) {
     if constexpr (FORMAT == SSU_FORMAT_SAME) {
-        store8(static_cast<T *>(p.out) + row * p.out_s + at, n, y);
+        store8(static_cast<T *>(p.out) + row * p.out_s + at, WHOLE ? 8 : n, y);
     } else {
         uint32_t code[2];
         const uint32_t s = mx_block<FORMAT>(y, code);
@@ -68,23 +74,26 @@ __device__ __forceinline__ void store_result(const NormParams &p, int64_t row, i
             p.scales[(row * p.groups * p.part + at) / 32] = static_cast<uint8_t>(s);
     }
 }
-template <typename T>
+template <typename T, bool WHOLE>
 __device__ __forceinline__ void store_residual(const NormParams &p, int64_t row, int at, int n, const float u[8]) {
+    if (WHOLE)
+        n = 8;
     if (p.res_f32)
         store8(static_cast<float *>(p.residual_out) + row * p.res_out_s + at, n, u);
     else
         store8(static_cast<T *>(p.residual_out) + row * p.res_out_s + at, n, u);
 }
 
-// LANES lanes per part, each with up to NV runs of eight elements in registers.
-template <typename T, int FORMAT, int LANES, int NV>
+// LANES lanes per part (16, or whole waves), each with up to NV runs of eight elements in registers.
+// WHOLE: a part is a multiple of eight.
+template <typename T, int FORMAT, int LANES, int NV, bool WHOLE>
 __global__ __launch_bounds__(LANES < kNormThreads ? kNormThreads : LANES) void norm_kernel(const NormParams p) {
     constexpr int kThreads = LANES < kNormThreads ? kNormThreads : LANES;
     constexpr int kWaves = LANES / kWaveLanes;  // per part
     const int64_t part = LANES < kNormThreads ? static_cast<int64_t>(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES
                                               : static_cast<int64_t>(blockIdx.x);
     if (part >= p.parts)
-        return;  // a whole wave: LANES is a multiple of 64
+        return;  // whole waves, or with 16 lanes whole DPP rows
     const int lane = threadIdx.x % LANES;
     const int64_t row = part / p.groups;
     const int first = static_cast<int>(part - row * p.groups) * p.part;
@@ -93,24 +102,24 @@ __global__ __launch_bounds__(LANES < kNormThreads ? kNormThreads : LANES) void n
 #pragma unroll
     for (int v = 0; v < NV; v++) {
         const int i = (v * LANES + lane) * 8;
-        x[v].load(static_cast<const T *>(p.x) + row * p.x_s + first + i, p.part - i);
+        x[v].template load<WHOLE>(static_cast<const T *>(p.x) + row * p.x_s + first + i, p.part - i);
     }
     if (p.gate)
 #pragma unroll
         for (int v = 0; v < NV; v++) {
             const int i = (v * LANES + lane) * 8;
-            z[v].load(static_cast<const T *>(p.gate) + row * p.gate_s + first + i, p.part - i);
+            z[v].template load<WHOLE>(static_cast<const T *>(p.gate) + row * p.gate_s + first + i, p.part - i);
         }
     if (p.residual)
 #pragma unroll
         for (int v = 0; v < NV; v++) {
             const int i = (v * LANES + lane) * 8;
-            r[v].load(p.residual, p.res_f32, row * p.res_s + first + i, p.part - i);
+            r[v].template load<WHOLE>(p.residual, p.res_f32, row * p.res_s + first + i, p.part - i);
         }
     // one run: the weights come with the rest; more: they are fetched (mostly from the caches)
     // when the inputs' registers are free
     if constexpr (NV == 1)
-        g[0].load(p.weight, p.weight_f32, first + lane * 8, p.part - lane * 8);
+        g[0].template load<WHOLE>(p.weight, p.weight_f32, first + lane * 8, p.part - lane * 8);
     float u[NV][8];
     float ss = 0.0f;
 #pragma unroll
@@ -130,7 +139,7 @@ __global__ __launch_bounds__(LANES < kNormThreads ? kNormThreads : LANES) void n
         for (int j = 0; j < 8; j++)
             ss = fmaf(u[v][j], u[v][j], ss);
     }
-    ss = wave64_sum(ss);
+    ss = LANES == 16 ? row16_sum(ss) : wave64_sum(ss);
     if constexpr (kWaves > 1) {
         __shared__ float sums[kWaves];
         if (threadIdx.x % kWaveLanes == 0)
@@ -148,14 +157,14 @@ __global__ __launch_bounds__(LANES < kNormThreads ? kNormThreads : LANES) void n
         if (n <= 0)
             break;
         if (p.residual)
-            store_residual<T>(p, row, first + i, n, u[v]);
+            store_residual<T, WHOLE>(p, row, first + i, n, u[v]);
         if constexpr (NV > 1)
-            g[v].load(p.weight, p.weight_f32, first + i, n);
+            g[v].template load<WHOLE>(p.weight, p.weight_f32, first + i, n);
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; j++)
             y[j] = u[v][j] * scale * g[v].get(p.weight_f32, j);
-        store_result<T, FORMAT>(p, row, first + i, n, lane, y);
+        store_result<T, FORMAT, WHOLE>(p, row, first + i, n, lane, y);
     }
 }
 
@@ -170,19 +179,19 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const NormParam
     const int tid = threadIdx.x;
     auto load_u = [&](int i, int n, float u[8]) {
         Raw8<T> x;
-        x.load(static_cast<const T *>(p.x) + row * p.x_s + first + i, n);
+        x.template load<false>(static_cast<const T *>(p.x) + row * p.x_s + first + i, n);
 #pragma unroll
         for (int j = 0; j < 8; j++)
             u[j] = widen(x.v[j]);
         if (p.gate) {
-            x.load(static_cast<const T *>(p.gate) + row * p.gate_s + first + i, n);
+            x.template load<false>(static_cast<const T *>(p.gate) + row * p.gate_s + first + i, n);
 #pragma unroll
             for (int j = 0; j < 8; j++)
                 u[j] *= silu_exact(widen(x.v[j]));
         }
         if (p.residual) {
             Raw8Or32<T> r;
-            r.load(p.residual, p.res_f32, row * p.res_s + first + i, n);
+            r.template load<false>(p.residual, p.res_f32, row * p.res_s + first + i, n);
 #pragma unroll
             for (int j = 0; j < 8; j++)
                 u[j] += r.get(p.res_f32, j);
@@ -211,13 +220,13 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const NormParam
         float u[8];
         load_u(i, n, u);
         Raw8Or32<T> g;
-        g.load(p.weight, p.weight_f32, first + i, n);
+        g.template load<false>(p.weight, p.weight_f32, first + i, n);
         if (p.residual)
-            store_residual<T>(p, row, first + i, n, u);
+            store_residual<T, false>(p, row, first + i, n, u);
 #pragma unroll
         for (int j = 0; j < 8; j++)
             u[j] = u[j] * scale * g.get(p.weight_f32, j);
-        store_result<T, FORMAT>(p, row, first + i, n, tid, u);
+        store_result<T, FORMAT, false>(p, row, first + i, n, tid, u);
     }
 }
 
@@ -226,47 +235,51 @@ struct NormShape {
 };
 
 // Lanes per part. Many parts: the fewest lanes that keep a part in registers (no barrier
-// for up to 2048 elements). Few parts: as many lanes as have a run of eight each, for the time of
-// one part is then the time of the call.
+// for up to 2048 elements). Few parts: the time of one part is the time of the call, so up to two
+// runs for each of 256 lanes, then as many lanes as a workgroup has.
 NormShape shape_for(int64_t parts, int part) {
     const int runs = (part + 7) / 8;
-    constexpr NormShape kShapes[] = {{64, 1}, {64, 2}, {64, 4}, {256, 1}, {256, 2}, {256, 4}, {1024, 1}, {1024, 2}, {1024, 4}};
-    const bool many = parts >= 2048;
+    constexpr NormShape kShapes[] = {{16, 1},  {64, 1},  {64, 2},   {64, 4},   {256, 1},
+                                     {256, 2}, {256, 4}, {1024, 1}, {1024, 2}, {1024, 4}};
+    const bool many = parts >= 1024;
     for (const NormShape &s : kShapes)
-        if (runs <= s.lanes * s.nv && (many ? !(s.lanes == 256 && s.nv == 1) : s.nv == 1 || s.lanes == 1024))
+        if (runs <= s.lanes * s.nv && (many || s.nv == 1 || s.lanes * s.nv == 512 || s.lanes == 1024))
             return s;
     return {kLongThreads, 0};
 }
 
-template <typename T, int FORMAT>
+template <typename T, int FORMAT, bool WHOLE>
 const void *norm_fn(NormShape s) {
     switch (s.lanes * 8 + s.nv) {
-    case 64 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 64, 1>);
-    case 64 * 8 + 2: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 64, 2>);
-    case 64 * 8 + 4: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 64, 4>);
-    case 256 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 256, 1>);
-    case 256 * 8 + 2: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 256, 2>);
-    case 256 * 8 + 4: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 256, 4>);
-    case 1024 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 1024, 1>);
-    case 1024 * 8 + 2: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 1024, 2>);
-    case 1024 * 8 + 4: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 1024, 4>);
+    case 16 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 16, 1, WHOLE>);
+    case 64 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 64, 1, WHOLE>);
+    case 64 * 8 + 2: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 64, 2, WHOLE>);
+    case 64 * 8 + 4: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 64, 4, WHOLE>);
+    case 256 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 256, 1, WHOLE>);
+    case 256 * 8 + 2: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 256, 2, WHOLE>);
+    case 256 * 8 + 4: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 256, 4, WHOLE>);
+    case 1024 * 8 + 1: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 1024, 1, WHOLE>);
+    case 1024 * 8 + 2: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 1024, 2, WHOLE>);
+    case 1024 * 8 + 4: return reinterpret_cast<const void *>(&norm_kernel<T, FORMAT, 1024, 4, WHOLE>);
     }
     return reinterpret_cast<const void *>(&norm_long_kernel<T, FORMAT>);
 }
 template <typename T>
-const void *norm_fn(int format, NormShape s) {
-    return format == SSU_FORMAT_MXFP8   ? norm_fn<T, SSU_FORMAT_MXFP8>(s)
-           : format == SSU_FORMAT_MXFP4 ? norm_fn<T, SSU_FORMAT_MXFP4>(s)
-                                        : norm_fn<T, SSU_FORMAT_SAME>(s);
+const void *norm_fn(int format, bool whole, NormShape s) {
+    return format == SSU_FORMAT_MXFP8   ? norm_fn<T, SSU_FORMAT_MXFP8, true>(s)
+           : format == SSU_FORMAT_MXFP4 ? norm_fn<T, SSU_FORMAT_MXFP4, true>(s)
+           : whole                      ? norm_fn<T, SSU_FORMAT_SAME, true>(s)
+                                        : norm_fn<T, SSU_FORMAT_SAME, false>(s);
 }
 
 }  // namespace
 
 int launch_norm(const NormParams &p, int dtype, int format, void *stream) {
     const NormShape s = shape_for(p.parts, p.part);
-    const void *fn = dtype == SSU_F32   ? norm_fn<float>(format, s)
-                     : dtype == SSU_F16 ? norm_fn<_Float16>(format, s)
-                                        : norm_fn<__bf16>(format, s);
+    const bool whole = p.part % 8 == 0;
+    const void *fn = dtype == SSU_F32   ? norm_fn<float>(format, whole, s)
+                     : dtype == SSU_F16 ? norm_fn<_Float16>(format, whole, s)
+                                        : norm_fn<__bf16>(format, whole, s);
     const int per = s.lanes < kNormThreads ? kNormThreads / s.lanes : 1;
     NormParams pc = p;
     void *args[] = {&pc};
