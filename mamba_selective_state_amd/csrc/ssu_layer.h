@@ -30,7 +30,7 @@ int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t 
 // elements. Up to kMxRowsMax rows run in the streaming kernel, which reads
 // scales where they are (and quantises up to kMxFuseRows rows by itself); more rows run
 // in the tiled kernels, which take codes and scales packed in a workspace.
-constexpr int kMxRowsMax = 64;
+constexpr int kMxRowsMax = 16;
 constexpr int kMxFuseRows = 4;
 struct MxParams {
     const void *x;  // float activations, or null

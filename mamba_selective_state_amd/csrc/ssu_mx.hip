@@ -92,21 +92,41 @@ __device__ __forceinline__ void store_out4(const MxParams &p, int m, int n, f32x
 
 // ---------------------------------------------------------------- few rows
 //
-// The weights' bytes bound it. A workgroup takes 16 outputs; its waves split k
-// and join their sums in LDS.
+// The weights' bytes bound it. A workgroup takes 16 outputs of up to 16 rows; its waves split
+// k and join their sums in LDS.
 
 constexpr int kStreamWaves = 8;
 constexpr int kStreamRows = 16;  // weight rows per workgroup
-constexpr int kStreamSteps = 4;  // 128-deep steps whose loads are in flight together
+constexpr int kStreamSteps = 4;  // 128-deep steps of a round, whose loads are in flight together (see round_scales)
 
-// FT: the activations' float type when this kernel quantises them (one row tile of
-// at most kMxFuseRows rows), else void.
-template <typename OT, int FORMAT, int MT, typename FT>
+// The scale bytes of a lane's blocks first + 4 s + g (s = 0..3) of a row, each in the lowest byte of
+// its word; 0 past the last block. One 16-byte access for the four lanes of a row: a byte
+// for each lane and step took a third of the kernel's time.
+__device__ __forceinline__ i32x4 round_scales(const uint8_t *row, int first, int blocks, int g) {
+    typedef int Vec __attribute__((ext_vector_type(4), aligned(1)));
+    i32x4 v = {};
+    if (first + 16 <= blocks) {
+        v = *reinterpret_cast<const Vec *>(row + first);
+    } else {
+#pragma unroll
+        for (int s = 0; s < 4; s++)
+            if (first + 4 * s + g < blocks)
+                v[s] = row[first + 4 * s + g] << (8 * g);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; s++)
+        v[s] = static_cast<int>(static_cast<uint32_t>(v[s]) >> (8 * g));
+    return v;
+}
+
+// FT: the activations' float type when this kernel quantises them (at most kMxFuseRows rows),
+// else void.
+template <typename OT, int FORMAT, typename FT>
 __global__ __launch_bounds__(kStreamWaves * 64) void mx_stream_kernel(const MxParams p) {
     constexpr bool kFuse = !std::is_void_v<FT>;
     constexpr int kChunk = kStreamSteps * 128;  // k values per round
     constexpr int kRowBytes = FORMAT == SSU_FORMAT_MXFP8 ? kChunk : kChunk / 2;
-    __shared__ f32x4 sums[kStreamWaves][MT][64];
+    __shared__ f32x4 sums[kStreamWaves][64];
     __shared__ alignas(16) uint8_t qcodes[kFuse ? kStreamWaves : 1][kMxFuseRows][kRowBytes];
     __shared__ uint8_t qscales[kFuse ? kStreamWaves : 1][kMxFuseRows][kChunk / 32];
     const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -118,18 +138,16 @@ __global__ __launch_bounds__(kStreamWaves * 64) void mx_stream_kernel(const MxPa
     const int blocks = p.k / 32;
     const int steps = (blocks + 3) / 4;
     const int rounds = (steps + kStreamSteps - 1) / kStreamSteps;
-    f32x4 acc[MT] = {};
+    f32x4 acc = {};
     for (int round = wave; round < rounds; round += kStreamWaves) {
         const int first = round * kStreamSteps;
         i32x4 wv[kStreamSteps];
-        int wsv[kStreamSteps];
 #pragma unroll
         for (int s = 0; s < kStreamSteps; s++) {
             const int b = (first + s) * 4 + g;
-            const bool live = b < blocks;
-            wv[s] = live ? *reinterpret_cast<const i32x4 *>(w + static_cast<int64_t>(b) * 16) : i32x4{};
-            wsv[s] = live ? ws[b] : 0;
+            wv[s] = b < blocks ? *reinterpret_cast<const i32x4 *>(w + static_cast<int64_t>(b) * 16) : i32x4{};
         }
+        const i32x4 wsv = round_scales(ws, first * 4, blocks, g);
         if constexpr (kFuse) {
             // this wave's own slice of every activation row, quantised for itself
             const int at = round * kChunk + l * 8;
@@ -147,53 +165,49 @@ __global__ __launch_bounds__(kStreamWaves * 64) void mx_stream_kernel(const MxPa
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
+        const int m = min(r, p.m - 1);
+        const uint8_t *a = kFuse ? nullptr : p.a + m * p.a_s;
+        i32x4 asv = {};
+        if constexpr (!kFuse)
+            asv = round_scales(p.a_scale + m * p.as_s, first * 4, blocks, g);
 #pragma unroll
         for (int s = 0; s < kStreamSteps; s++) {
-#pragma unroll
-            for (int t = 0; t < MT; t++) {
-                i32x8 av;
-                int as;
-                if constexpr (kFuse) {
-                    const int m = min(r, p.m - 1);
-                    if constexpr (FORMAT == SSU_FORMAT_MXFP8)
-                        av = wide(*reinterpret_cast<const i32x4 *>(&qcodes[wave][m][s * 128 + 16 * g]),
-                                  *reinterpret_cast<const i32x4 *>(&qcodes[wave][m][s * 128 + 64 + 16 * g]));
-                    else
-                        av = wide(*reinterpret_cast<const i32x4 *>(&qcodes[wave][m][s * 64 + 16 * g]));
-                    as = qscales[wave][m][s * 4 + g];
+            i32x8 av;
+            int as;
+            if constexpr (kFuse) {
+                if constexpr (FORMAT == SSU_FORMAT_MXFP8)
+                    av = wide(*reinterpret_cast<const i32x4 *>(&qcodes[wave][m][s * 128 + 16 * g]),
+                              *reinterpret_cast<const i32x4 *>(&qcodes[wave][m][s * 128 + 64 + 16 * g]));
+                else
+                    av = wide(*reinterpret_cast<const i32x4 *>(&qcodes[wave][m][s * 64 + 16 * g]));
+                as = qscales[wave][m][s * 4 + g];
+            } else {
+                const int b = (first + s) * 4;
+                as = asv[s];
+                if constexpr (FORMAT == SSU_FORMAT_MXFP8) {
+                    const i32x4 lo = b + g / 2 < blocks ? *reinterpret_cast<const i32x4 *>(a + static_cast<int64_t>(b) * 32 + 16 * g) : i32x4{};
+                    const i32x4 hi = b + 2 + g / 2 < blocks ? *reinterpret_cast<const i32x4 *>(a + static_cast<int64_t>(b) * 32 + 64 + 16 * g) : i32x4{};
+                    av = wide(lo, hi);
                 } else {
-                    const int64_t m = min(t * 16 + r, p.m - 1);
-                    const uint8_t *a = p.a + m * p.a_s;
-                    const int b = (first + s) * 4;
-                    as = b + g < blocks ? p.a_scale[m * p.as_s + b + g] : 0;
-                    if constexpr (FORMAT == SSU_FORMAT_MXFP8) {
-                        const i32x4 lo = b + g / 2 < blocks ? *reinterpret_cast<const i32x4 *>(a + static_cast<int64_t>(b) * 32 + 16 * g) : i32x4{};
-                        const i32x4 hi = b + 2 + g / 2 < blocks ? *reinterpret_cast<const i32x4 *>(a + static_cast<int64_t>(b) * 32 + 64 + 16 * g) : i32x4{};
-                        av = wide(lo, hi);
-                    } else {
-                        av = wide(b + g < blocks ? *reinterpret_cast<const i32x4 *>(a + static_cast<int64_t>(b + g) * 16) : i32x4{});
-                    }
+                    av = wide(b + g < blocks ? *reinterpret_cast<const i32x4 *>(a + static_cast<int64_t>(b + g) * 16) : i32x4{});
                 }
-                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    wide(wv[s]), av, acc[t], kE2M1, FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, 0, wsv[s], 0, as);
             }
+            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(wv[s]), av, acc, kE2M1,
+                                                                   FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, 0, wsv[s], 0, as);
         }
         if constexpr (kFuse) {
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
     }
-#pragma unroll
-    for (int t = 0; t < MT; t++)
-        sums[wave][t][l] = acc[t];
+    sums[wave][l] = acc;
     __syncthreads();
-    if (threadIdx.x < MT * 64) {
-        const int t = wave;
-        f32x4 v = sums[0][t][l];
+    if (wave == 0) {
+        f32x4 v = sums[0][l];
 #pragma unroll
         for (int j = 1; j < kStreamWaves; j++)
-            v += sums[j][t][l];
-        store_out4<OT>(p, t * 16 + r, n0 + 4 * g, add_bias<OT>(p, n0 + 4 * g, v));
+            v += sums[j][l];
+        store_out4<OT>(p, r, n0 + 4 * g, add_bias<OT>(p, n0 + 4 * g, v));
     }
 }
 
@@ -243,12 +257,17 @@ __device__ __forceinline__ void pack_scales(const uint8_t *scale, int64_t stride
         const int kt = static_cast<int>(t % ktiles);
         const int64_t row = min(t / ktiles * 32 + l % 32, static_cast<int64_t>(rows) - 1);
         const int b = (2 * kt + l / 32) * kSteps;
+        typedef uint32_t Word __attribute__((aligned(1)));
         uint32_t v = 0;
+        if (b + 4 <= blocks) {
+            v = *reinterpret_cast<const Word *>(scale + row * stride + b);
+        } else {
 #pragma unroll
-        for (int s = 0; s < kSteps; s++)
-            if (b + s < blocks)
-                v |= static_cast<uint32_t>(scale[row * stride + b + s]) << (8 * s);
-        packed[i] = v;
+            for (int s = 0; s < kSteps; s++)
+                if (b + s < blocks)
+                    v |= static_cast<uint32_t>(scale[row * stride + b + s]) << (8 * s);
+        }
+        packed[i] = v;  // of MXFP8 the low half counts
     }
 }
 
@@ -294,20 +313,23 @@ __global__ __launch_bounds__(kQuantThreads) void mx_pack_kernel(const PackParams
 
 struct TileParams {
     MxParams p;
-    const uint32_t *a_packed, *w_packed;
+    const uint8_t *a_scales, *w_scales;  // packed words, or rows of scale bytes (p.as_s, p.ws_s)
+    int32_t packed;
     int32_t ktiles, mtiles, ntiles;
 };
 
 // Byte offset of 16-byte chunk c of row r in an LDS image of rows of 128 or 64 bytes.
-// Eight lanes that read one chunk of eight neighbouring rows touch eight
-// different 16-byte columns of the 128-byte lines: no bank is asked twice.
+// The 64 banks hold two 128-byte lines; a 16-byte read is served for 16 lanes at a time, lanes 0-3,
+// 12-15, 20-23 and 24-27 of a half wave together, and these read one chunk of as many rows. With
+// the chunks of a line permuted by half its number no two of them share a bank (by its number alone
+// every second read collided).
 template <int ROW>
 __device__ __forceinline__ int lds_chunk(int r, int c) {
     if constexpr (ROW == 128) {
-        return r * 128 + ((c ^ (r & 7)) * 16);
+        return r * 128 + ((c ^ ((r >> 1) & 7)) * 16);
     } else {
         const int line = r / 2;
-        return line * 128 + ((((r & 1) * 4 + c) ^ (line & 7)) * 16);
+        return line * 128 + ((((r & 1) * 4 + c) ^ ((line >> 1) & 7)) * 16);
     }
 }
 
@@ -351,7 +373,8 @@ struct Filler {
 
     __device__ __forceinline__ Filler(const uint8_t *base, int64_t stride, int first, int rows, int row_bytes, int wave, int l) {
         bytes = row_bytes;
-        const int line = l / 8, slot = (l % 8) ^ line;  // of the lane's KiB: line is line & 7 of the image
+        static_assert(WAVES % 2 == 0, "a wave's KiBs are all even ones of the image or all odd ones");
+        const int line = l / 8, slot = (l % 8) ^ (wave % 2 * 4 + line / 2);  // as lds_chunk permutes them
         chunk = ROW == 128 ? slot * 16 : slot % 4 * 16;
 #pragma unroll
         for (int i = 0; i < kLoads; i++) {
@@ -368,133 +391,14 @@ struct Filler {
     }
 };
 
-// TM x TN outputs per workgroup; the waves are WM x WN over the tile and WK over the
-// steps of a K tile (those join their sums in LDS at the end). Codes go straight
-// from memory to two LDS images: while one K tile is multiplied the next arrives. Each
-// step's operands are read during the step before, the next tile's first ones
-// during this one's last step, behind the only barrier of a tile; the image that
-// the tile leaves is filled from there on.
-template <typename OT, int FORMAT, int TM, int TN, int WM, int WN, int WK>
-__global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TileParams t) {
-    using KT = KTile<FORMAT>;
-    constexpr int kWaves = WM * WN * WK;
-    constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
-    constexpr int kSteps = KT::kSteps / WK;  // of this wave per K tile
-    constexpr int kABytes = TM * KT::kARow, kStage = kABytes + TN * KT::kWRow;
-    // two arrays, so that the compiler can tell a fill of one from a read of the other
-    __shared__ alignas(16) uint8_t lds0[kStage];
-    __shared__ alignas(16) uint8_t lds1[kStage];
-    const MxParams &p = t.p;
-    const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+// The end of a tile: sums joined over the waves that split k, bias, rounding and stores, through
+// two LDS images of STAGE bytes that are free by now.
+template <typename OT, int FM, int FN, int WM, int WN, int WK, int STAGE>
+__device__ __forceinline__ void finish_tile(const MxParams &p, f32x16 (&acc)[FM][FN], uint8_t *lds0, uint8_t *lds1, int m0, int n0,
+                                            int l, int wave) {
+    constexpr int kWaves = WM * WN * WK, kStage = STAGE;
     const int r = l % 32, h = l / 32;
     const int wm = wave % WM, wn = wave / WM % WN, wk = wave / (WM * WN);
-    int mt, nt;
-    tile_at(blockIdx.x, t.mtiles, t.ntiles, &mt, &nt);
-    const int m0 = mt * TM, n0 = nt * TN;
-
-    const Filler<TM, KT::kARow, kWaves> fill_a(p.a, p.a_s, m0, p.m, FORMAT == SSU_FORMAT_MXFP8 ? p.k : p.k / 2, wave, l);
-    const Filler<TN, KT::kWRow, kWaves> fill_w(p.w, p.w_s, n0, p.n, p.k / 2, wave, l);
-    auto fill = [&](uint8_t *lds, int kt) {
-        fill_a.load(kt, lds, wave);
-        fill_w.load(kt, lds + kABytes, wave);
-    };
-    // scales of this wave's fragments
-    const uint32_t *aps = t.a_packed + (static_cast<int64_t>(m0 / 32 + wm * FM) * t.ktiles) * 64 + l;
-    const uint32_t *wps = t.w_packed + (static_cast<int64_t>(n0 / 32 + wn * FN) * t.ktiles) * 64 + l;
-    int asc[FM], wsc[FN], asc_next[FM], wsc_next[FN];
-    auto load_scales = [&](int kt) {
-#pragma unroll
-        for (int i = 0; i < FM; i++)
-            asc_next[i] = static_cast<int>(aps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64]);
-#pragma unroll
-        for (int i = 0; i < FN; i++)
-            wsc_next[i] = static_cast<int>(wps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64]);
-    };
-    struct Frags {
-        std::conditional_t<FORMAT == SSU_FORMAT_MXFP8, i32x8, i32x4> a[FM];
-        i32x4 w[FN];
-    };
-    auto read = [&](const uint8_t *src, int j) {
-        Frags f;
-        const int s = wk + WK * j;
-#pragma unroll
-        for (int i = 0; i < FM; i++) {
-            const int row = (wm * FM + i) * 32 + r;
-            if constexpr (FORMAT == SSU_FORMAT_MXFP8)
-                f.a[i] = wide(*reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, 2 * s + h)),
-                              *reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, 2 * (KT::kSteps + s) + h)));
-            else
-                f.a[i] = *reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, KT::kSteps * h + s));
-        }
-#pragma unroll
-        for (int i = 0; i < FN; i++)
-            f.w[i] = *reinterpret_cast<const i32x4 *>(src + kABytes +
-                                                      lds_chunk<KT::kWRow>((wn * FN + i) * 32 + r, KT::kSteps * h + s));
-        return f;
-    };
-    f32x16 acc[FM][FN] = {};
-    auto multiply = [&](const Frags &f, auto jc) {
-        constexpr int kByte = decltype(jc)::value * WK;
-#pragma unroll
-        for (int i = 0; i < FM; i++)
-#pragma unroll
-            for (int j = 0; j < FN; j++)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    wide(f.w[j]), wide(f.a[i]), acc[i][j], kE2M1, FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, kByte, wsc[j], kByte, asc[i]);
-    };
-
-    // k is taken in pairs of tiles without a branch: what lies past its end is
-    // filled and multiplied like the rest, and comes to nothing by its scales
-    if (t.ktiles > 0) {
-        fill(lds0, 0);
-        load_scales(0);
-        fill(lds1, 1);
-        fills_barrier();
-        Frags cur = read(lds0, 0);
-        auto tile = [&](uint8_t *here, uint8_t *there, int kt) {
-#pragma unroll
-            for (int i = 0; i < FM; i++)
-                asc[i] = WK > 1 ? asc_next[i] >> (8 * wk) : asc_next[i];
-#pragma unroll
-            for (int i = 0; i < FN; i++)
-                wsc[i] = WK > 1 ? wsc_next[i] >> (8 * wk) : wsc_next[i];
-            load_scales(min(kt + 1, t.ktiles - 1));
-            for_passes<0, kSteps>([&](auto jc) {
-                constexpr int j = decltype(jc)::value;
-                __builtin_amdgcn_sched_barrier(0);
-                Frags next;
-                if constexpr (j + 1 < kSteps) {
-                    next = read(here, j + 1);
-                } else {
-                    fills_barrier();
-                    next = read(there, 0);
-                    fill(here, kt + 2);
-                }
-                multiply(cur, jc);
-                cur = next;
-                // the reads (and fills) one by one between the first products
-                constexpr int kReads = (FORMAT == SSU_FORMAT_MXFP8 ? 2 * FM : FM) + FN, kFirst = FM * FN > 1 ? FM * FN / 2 : 1;
-                constexpr int kFills = j + 1 == kSteps ? decltype(fill_a)::kLoads + decltype(fill_w)::kLoads : 0;
-                for_passes<0, kFirst>([&](auto ic) {
-                    constexpr int i = decltype(ic)::value;
-                    __builtin_amdgcn_sched_group_barrier(0x100, kReads * (i + 1) / kFirst - kReads * i / kFirst, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                });
-                for_passes<0, FM * FN - kFirst>([&](auto ic) {
-                    constexpr int i = decltype(ic)::value, n = FM * FN - kFirst;
-                    if constexpr (kFills > 0)
-                        __builtin_amdgcn_sched_group_barrier(0x010, kFills * (i + 1) / n - kFills * i / n, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                });
-            });
-        };
-        for (int kt = 0; kt < t.ktiles; kt += 2) {
-            tile(lds0, lds1, kt);
-            tile(lds1, lds0, kt + 1);
-        }
-        fills_barrier();
-    }
-
     if constexpr (WK > 1) {
         // each wave of the WK that share a part of the tile sums and stores its share of the
         // fragments, half of the registers at a time: the others leave theirs in the LDS images
@@ -589,6 +493,344 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
     }
 }
 
+// TM x TN outputs per workgroup; the waves are WM x WN over the tile and WK over the
+// steps of a K tile (those join their sums in LDS at the end). Codes go straight
+// from memory to two LDS images: while one K tile is multiplied the next arrives. Each
+// step's operands are read during the step before, the next tile's first ones
+// during this one's last step, behind the only barrier of a tile; the image that
+// the tile leaves is filled from there on.
+template <typename OT, int FORMAT, int TM, int TN, int WM, int WN, int WK>
+__global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TileParams t) {
+    using KT = KTile<FORMAT>;
+    constexpr int kWaves = WM * WN * WK;
+    constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
+    constexpr int kSteps = KT::kSteps / WK;  // of this wave per K tile
+    constexpr int kABytes = TM * KT::kARow, kStage = kABytes + TN * KT::kWRow;
+    // two arrays, so that the compiler can tell a fill of one from a read of the other
+    __shared__ alignas(16) uint8_t lds0[kStage];
+    __shared__ alignas(16) uint8_t lds1[kStage];
+    const MxParams &p = t.p;
+    const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int r = l % 32, h = l / 32;
+    const int wm = wave % WM, wn = wave / WM % WN, wk = wave / (WM * WN);
+    int mt, nt;
+    tile_at(blockIdx.x, t.mtiles, t.ntiles, &mt, &nt);
+    const int m0 = mt * TM, n0 = nt * TN;
+
+    const Filler<TM, KT::kARow, kWaves> fill_a(p.a, p.a_s, m0, p.m, FORMAT == SSU_FORMAT_MXFP8 ? p.k : p.k / 2, wave, l);
+    const Filler<TN, KT::kWRow, kWaves> fill_w(p.w, p.w_s, n0, p.n, p.k / 2, wave, l);
+    auto fill = [&](uint8_t *lds, int kt) {
+        fill_a.load(kt, lds, wave);
+        fill_w.load(kt, lds + kABytes, wave);
+    };
+    // scales of this wave's fragments
+    const uint32_t *aps = reinterpret_cast<const uint32_t *>(t.a_scales) + (static_cast<int64_t>(m0 / 32 + wm * FM) * t.ktiles) * 64 + l;
+    const uint32_t *wps = reinterpret_cast<const uint32_t *>(t.w_scales) + (static_cast<int64_t>(n0 / 32 + wn * FN) * t.ktiles) * 64 + l;
+    int asc[FM], wsc[FN], asc_next[FM], wsc_next[FN];
+    auto load_scales = [&](int kt) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+            asc_next[i] = static_cast<int>(aps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64]);
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+            wsc_next[i] = static_cast<int>(wps[(static_cast<int64_t>(i) * t.ktiles + kt) * 64]);
+    };
+    struct Frags {
+        std::conditional_t<FORMAT == SSU_FORMAT_MXFP8, i32x8, i32x4> a[FM];
+        i32x4 w[FN];
+    };
+    auto read = [&](const uint8_t *src, int j) {
+        Frags f;
+        const int s = wk + WK * j;
+#pragma unroll
+        for (int i = 0; i < FM; i++) {
+            const int row = (wm * FM + i) * 32 + r;
+            if constexpr (FORMAT == SSU_FORMAT_MXFP8)
+                f.a[i] = wide(*reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, 2 * s + h)),
+                              *reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, 2 * (KT::kSteps + s) + h)));
+            else
+                f.a[i] = *reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, KT::kSteps * h + s));
+        }
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+            f.w[i] = *reinterpret_cast<const i32x4 *>(src + kABytes +
+                                                      lds_chunk<KT::kWRow>((wn * FN + i) * 32 + r, KT::kSteps * h + s));
+        return f;
+    };
+    f32x16 acc[FM][FN] = {};
+    auto multiply = [&](const Frags &f, auto jc) {
+        constexpr int kByte = decltype(jc)::value * WK;
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    wide(f.w[j]), wide(f.a[i]), acc[i][j], kE2M1, FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, kByte, wsc[j], kByte, asc[i]);
+    };
+
+    // k is taken in pairs of tiles without a branch: what lies past its end is
+    // filled and multiplied like the rest, and comes to nothing by its scales
+    if (t.ktiles > 0) {
+        fill(lds0, 0);
+        load_scales(0);
+        fill(lds1, 1);
+        fills_barrier();
+        Frags cur = read(lds0, 0);
+        auto tile = [&](uint8_t *here, uint8_t *there, int kt) {
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+                asc[i] = WK > 1 ? asc_next[i] >> (8 * wk) : asc_next[i];
+#pragma unroll
+            for (int i = 0; i < FN; i++)
+                wsc[i] = WK > 1 ? wsc_next[i] >> (8 * wk) : wsc_next[i];
+            load_scales(min(kt + 1, t.ktiles - 1));
+            for_passes<0, kSteps>([&](auto jc) {
+                constexpr int j = decltype(jc)::value;
+                __builtin_amdgcn_sched_barrier(0);
+                Frags next;
+                if constexpr (j + 1 < kSteps) {
+                    next = read(here, j + 1);
+                } else {
+                    fills_barrier();
+                    next = read(there, 0);
+                    fill(here, kt + 2);
+                }
+                multiply(cur, jc);
+                cur = next;
+                // the reads (and fills) one by one between the first products
+                constexpr int kReads = (FORMAT == SSU_FORMAT_MXFP8 ? 2 * FM : FM) + FN, kFirst = FM * FN > 1 ? FM * FN / 2 : 1;
+                constexpr int kFills = j + 1 == kSteps ? decltype(fill_a)::kLoads + decltype(fill_w)::kLoads : 0;
+                for_passes<0, kFirst>([&](auto ic) {
+                    constexpr int i = decltype(ic)::value;
+                    __builtin_amdgcn_sched_group_barrier(0x100, kReads * (i + 1) / kFirst - kReads * i / kFirst, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                });
+                for_passes<0, FM * FN - kFirst>([&](auto ic) {
+                    constexpr int i = decltype(ic)::value, n = FM * FN - kFirst;
+                    if constexpr (kFills > 0)
+                        __builtin_amdgcn_sched_group_barrier(0x010, kFills * (i + 1) / n - kFills * i / n, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                });
+            });
+        };
+        for (int kt = 0; kt < t.ktiles; kt += 2) {
+            tile(lds0, lds1, kt);
+            tile(lds1, lds0, kt + 1);
+        }
+        fills_barrier();
+    }
+
+    finish_tile<OT, FM, FN, WM, WN, WK, kStage>(p, acc, lds0, lds1, m0, n0, l, wave);
+}
+
+// The smaller tiles: too little work per K tile to hide a fetch behind one of them, so STAGES images
+// take turns and a fetch has STAGES - 1 tiles' time. A wave waits for the fetches that the
+// next tile needs and no more: only fetches count in vmcnt here (scales come through LDS as well),
+// every tile issues the same number of them, and they arrive in order.
+template <typename OT, int FORMAT, int TM, int TN, int WM, int WN, int WK, int STAGES>
+__global__ __launch_bounds__(64 * WM * WN * WK) void mx_ring_kernel(const TileParams t) {
+    using KT = KTile<FORMAT>;
+    constexpr int kWaves = WM * WN * WK;
+    constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
+    constexpr int kSteps = KT::kSteps / WK;
+    constexpr int kABytes = TM * KT::kARow, kCodes = kABytes + TN * KT::kWRow;
+    constexpr int kScaleTiles = (TM + TN) / 32, kScaleLoads = kScaleTiles / kWaves;  // of 64 words
+    constexpr int kStage = kCodes + kScaleTiles * 256;
+    static_assert(kScaleLoads * kWaves == kScaleTiles, "whole words per wave");
+    static_assert(STAGES == 4 || STAGES == 8, "images");
+    // arrays of their own: the compiler tells fills of one from reads of another
+    __shared__ alignas(16) uint8_t s0[kStage], s1[kStage], s2[kStage], s3[kStage];
+    __shared__ alignas(16) uint8_t s4[STAGES > 4 ? kStage : 16], s5[STAGES > 4 ? kStage : 16], s6[STAGES > 4 ? kStage : 16],
+        s7[STAGES > 4 ? kStage : 16];
+    const MxParams &p = t.p;
+    const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int r = l % 32, h = l / 32;
+    const int wm = wave % WM, wn = wave / WM % WN, wk = wave / (WM * WN);
+    int mt, nt;
+    tile_at(blockIdx.x, t.mtiles, t.ntiles, &mt, &nt);
+    const int m0 = mt * TM, n0 = nt * TN;
+
+    const Filler<TM, KT::kARow, kWaves> fill_a(p.a, p.a_s, m0, p.m, FORMAT == SSU_FORMAT_MXFP8 ? p.k : p.k / 2, wave, l);
+    const Filler<TN, KT::kWRow, kWaves> fill_w(p.w, p.w_s, n0, p.n, p.k / 2, wave, l);
+    // scale words: packed, or straight from rows of bytes (a word of MXFP4's is the four of
+    // half h, of MXFP8's the four of the tile)
+    const uint8_t *scale[kScaleLoads];
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; i++) {
+        const int tile = wave + kWaves * i;
+        const bool is_a = tile < TM / 32;
+        const int row0 = is_a ? m0 + tile * 32 : n0 + (tile - TM / 32) * 32;
+        const uint8_t *base = is_a ? t.a_scales : t.w_scales;
+        if (t.packed)
+            scale[i] = base + (static_cast<int64_t>(row0 / 32) * t.ktiles * 64 + l) * 4;
+        else
+            scale[i] = base + static_cast<int64_t>(min(row0 + r, (is_a ? p.m : p.n) - 1)) * (is_a ? p.as_s : p.ws_s) +
+                       (FORMAT == SSU_FORMAT_MXFP8 ? 0 : 4 * h);
+    }
+    const int scale_step = t.packed ? 256 : KT::kDepth / 32;
+    const int shift = 8 * wk + (FORMAT == SSU_FORMAT_MXFP8 && !t.packed ? 16 * h : 0);
+    constexpr int kLoads = decltype(fill_a)::kLoads + decltype(fill_w)::kLoads + kScaleLoads;
+    auto fill = [&](uint8_t *lds, int kt) {
+        fill_a.load(kt, lds, wave);
+        fill_w.load(kt, lds + kABytes, wave);
+        const int64_t at = static_cast<int64_t>(min(kt, t.ktiles - 1)) * scale_step;
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; i++)
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void *)(scale[i] + at),
+                (__attribute__((address_space(3))) void *)(lds + kCodes + (wave + kWaves * i) * 256), 4, 0, 0);
+    };
+    struct Frags {
+        std::conditional_t<FORMAT == SSU_FORMAT_MXFP8, i32x8, i32x4> a[FM];
+        i32x4 w[FN];
+    };
+    auto read = [&](const uint8_t *src, int j) {
+        Frags f;
+        const int s = wk + WK * j;
+#pragma unroll
+        for (int i = 0; i < FM; i++) {
+            const int row = (wm * FM + i) * 32 + r;
+            if constexpr (FORMAT == SSU_FORMAT_MXFP8)
+                f.a[i] = wide(*reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, 2 * s + h)),
+                              *reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, 2 * (KT::kSteps + s) + h)));
+            else
+                f.a[i] = *reinterpret_cast<const i32x4 *>(src + lds_chunk<KT::kARow>(row, KT::kSteps * h + s));
+        }
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+            f.w[i] = *reinterpret_cast<const i32x4 *>(src + kABytes +
+                                                      lds_chunk<KT::kWRow>((wn * FN + i) * 32 + r, KT::kSteps * h + s));
+        return f;
+    };
+    int asc[FM], wsc[FN];
+    auto read_scales = [&](const uint8_t *src) {
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(src + kCodes) + l;
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+            asc[i] = static_cast<int>(words[(wm * FM + i) * 64]);
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+            wsc[i] = static_cast<int>(words[(TM / 32 + wn * FN + i) * 64]);
+    };
+    f32x16 acc[FM][FN] = {};
+    auto multiply = [&](const Frags &f, auto jc) {
+        constexpr int kByte = decltype(jc)::value * WK;
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    wide(f.w[j]), wide(f.a[i]), acc[i][j], kE2M1, FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, kByte, wsc[j], kByte, asc[i]);
+    };
+    // waits until at most `pending` fetches of this wave are outstanding (and no LDS access, if
+    // `lds`), then for the other waves
+    auto arrive = [](auto pending, auto lds) {
+        constexpr int n = decltype(pending)::value;
+        static_assert(n < 64, "vmcnt has six bits");
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((decltype(lds)::value ? 0x0070 : 0x0F70) | (n & 15) | ((n >> 4) << 14));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    uint8_t *const images[8] = {s0, s1, s2, s3, s4, s5, s6, s7};
+    if (t.ktiles > 0) {
+        for_passes<0, STAGES>([&](auto sc) { fill(images[decltype(sc)::value], decltype(sc)::value); });
+        if constexpr (kSteps == 1) {
+            // A wave has one step per K tile: its operands are read two tiles ahead, so that neither
+            // the fetch nor the LDS is waited for. When a wave arrives, it has multiplied tile
+            // kt, so its reads of that image are complete and the image can be filled.
+            arrive(std::integral_constant<int, (STAGES - 2) * kLoads>(), std::true_type());
+            Frags cur = read(s0, 0), next = read(s1, 0);
+            int a0[FM], w0[FN], a1[FM], w1[FN];
+            auto words = [&](const uint8_t *src, int (&a)[FM], int (&w)[FN]) {
+                read_scales(src);
+#pragma unroll
+                for (int i = 0; i < FM; i++)
+                    a[i] = asc[i];
+#pragma unroll
+                for (int i = 0; i < FN; i++)
+                    w[i] = wsc[i];
+            };
+            words(s0, a0, w0);
+            words(s1, a1, w1);
+            int kt = 0;
+            bool done = false;
+            while (!done) {
+                for_passes<0, STAGES>([&](auto sc) {
+                    constexpr int s = decltype(sc)::value;
+                    if (done)
+                        return;
+#pragma unroll
+                    for (int i = 0; i < FM; i++)
+                        asc[i] = a0[i] >> shift;
+#pragma unroll
+                    for (int i = 0; i < FN; i++)
+                        wsc[i] = w0[i] >> shift;
+                    multiply(cur, std::integral_constant<int, 0>());
+                    __builtin_amdgcn_sched_barrier(0);
+                    arrive(std::integral_constant<int, (STAGES - 3) * kLoads>(), std::false_type());
+                    cur = next;
+#pragma unroll
+                    for (int i = 0; i < FM; i++)
+                        a0[i] = a1[i];
+#pragma unroll
+                    for (int i = 0; i < FN; i++)
+                        w0[i] = w1[i];
+                    next = read(images[(s + 2) % STAGES], 0);
+                    words(images[(s + 2) % STAGES], a1, w1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    fill(images[s], kt + STAGES);
+                    done = ++kt >= t.ktiles;
+                });
+            }
+        } else {
+            arrive(std::integral_constant<int, (STAGES - 1) * kLoads>(), std::true_type());
+            Frags cur = read(s0, 0);
+            auto shifted_scales = [&](const uint8_t *src) {
+                read_scales(src);
+#pragma unroll
+                for (int i = 0; i < FM; i++)
+                    asc[i] >>= shift;
+#pragma unroll
+                for (int i = 0; i < FN; i++)
+                    wsc[i] >>= shift;
+            };
+            shifted_scales(s0);
+            auto tile = [&](uint8_t *here, uint8_t *there, int kt) {
+                for_passes<0, kSteps>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    Frags next;
+                    if constexpr (j + 1 < kSteps) {
+                        next = read(here, j + 1);
+                        multiply(cur, jc);
+                    } else {
+                        // the products first: they need nothing that is still on its way
+                        multiply(cur, jc);
+                        arrive(std::integral_constant<int, (STAGES - 2) * kLoads>(), std::true_type());
+                        next = read(there, 0);
+                        shifted_scales(there);
+                        fill(here, kt + STAGES);
+                    }
+                    cur = next;
+                });
+            };
+            int kt = 0;
+            bool done = false;
+            while (!done) {
+                for_passes<0, STAGES>([&](auto sc) {
+                    constexpr int s = decltype(sc)::value;
+                    if (done)
+                        return;
+                    tile(images[s], images[(s + 1) % STAGES], kt);
+                    done = ++kt >= t.ktiles;
+                });
+            }
+        }
+        arrive(std::integral_constant<int, 0>(), std::true_type());  // the last fills and reads
+    }
+    finish_tile<OT, FM, FN, WM, WN, WK, kStage>(p, acc, s0, s1, m0, n0, l, wave);
+}
+
 // ---------------------------------------------------------------- launches
 
 template <typename T>
@@ -602,29 +844,44 @@ const void *pack_fn(int format) {
                                       : reinterpret_cast<const void *>(&mx_pack_kernel<FT, SSU_FORMAT_MXFP8>);
 }
 template <typename OT, int FORMAT>
-const void *stream_fn(int m, bool fuse, int x_dtype) {
+const void *stream_fn(bool fuse, int x_dtype) {
     if (fuse)
-        return x_dtype == SSU_F32   ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 1, float>)
-               : x_dtype == SSU_F16 ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 1, _Float16>)
-                                    : reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 1, __bf16>);
-    return m <= 16   ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 1, void>)
-           : m <= 32 ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 2, void>)
-                     : reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, 4, void>);
+        return x_dtype == SSU_F32   ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, float>)
+               : x_dtype == SSU_F16 ? reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, _Float16>)
+                                    : reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, __bf16>);
+    return reinterpret_cast<const void *>(&mx_stream_kernel<OT, FORMAT, void>);
 }
 
 struct TileShape {
-    int tm, tn, threads;
+    int tm, tn;
 };
-constexpr TileShape kTileShapes[3] = {{256, 256, 256}, {128, 128, 256}, {64, 64, 256}};
+constexpr TileShape kTileShapes[4] = {{256, 256}, {128, 128}, {64, 64}, {64, 64}};
+constexpr int kTileThreads = 256;
 
 template <typename OT, int FORMAT>
 const void *tile_fn(int shape) {
     constexpr int kWk = KTile<FORMAT>::kSteps;
     switch (shape) {
     case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 256, 256, 2, 2, 1>);
-    case 1: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 128, 128, 2, 2, 1>);
+    case 1: return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 128, 128, 2, 2, 1, 4>);
+    case 2: return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 4>);
     }
-    return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk>);
+    return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 8>);
+}
+
+// The largest tile that leaves every compute unit one; of the smallest, the form with eight
+// images if no unit gets a second one, else the one with four, of which two fit a unit.
+int tile_shape(int64_t m, int64_t n) {
+    for (int s = 0; s < 3; s++)
+        if (((m + kTileShapes[s].tm - 1) / kTileShapes[s].tm) * ((n + kTileShapes[s].tn - 1) / kTileShapes[s].tn) >= (s < 2 ? 256 : 257))
+            return s;
+    return 3;
+}
+// Whether a tile's scale words can be fetched where the bytes are: the large tile packs them first (it
+// would fetch a line for eight bytes of each of 512 rows), and so do words that are not aligned or
+// reach past the end of k.
+bool scales_in_place(int shape, const void *base, int64_t stride, int64_t k, int format) {
+    return shape != 0 && k % ktile_depth(format) == 0 && stride % 4 == 0 && reinterpret_cast<uintptr_t>(base) % 4 == 0;
 }
 
 template <typename F>
@@ -657,78 +914,80 @@ int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t 
 }
 
 int64_t mx_linear_workspace(int64_t m, int64_t n, int64_t k, int format, bool floats) {
+    const int64_t quantised = floats && m > kMxFuseRows ? code_bytes(m, k, format) + round256(m * (k / 32)) : 0;
     if (m <= kMxRowsMax)
-        return floats && m > kMxFuseRows ? code_bytes(m, k, format) + m * (k / 32) : 0;
+        return quantised;
     const int64_t ktiles = ktiles_of(k, format);
-    return (floats ? code_bytes(m, k, format) : 0) + 4 * (packed_room(m, ktiles) + packed_room(n, ktiles));
+    return quantised + 4 * (packed_room(m, ktiles) + packed_room(n, ktiles));
 }
 
 int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *stream) {
     MxParams p = args_in;
     const bool mx4 = format == SSU_FORMAT_MXFP4;
     const bool floats = p.x != nullptr;
+    uint8_t *ws = p.workspace;
+    const bool fuse = floats && p.m <= kMxFuseRows;
+    const int shape = tile_shape(p.m, p.n);
+    // where scales are packed, the activations are quantised in the same launch
+    const bool packs_floats = floats && p.m > kMxRowsMax && !scales_in_place(shape, p.w_scale, p.ws_s, p.k, format);
+    if (floats && !fuse && !packs_floats && p.k > 0) {
+        uint8_t *scales = ws + code_bytes(p.m, p.k, format);
+        if (int e = launch_mx_quantize_rows(p.x, p.x_dtype, p.x_s, p.m, p.k, ws, scales, format, stream))
+            return e;
+        p.a = ws;
+        p.a_scale = scales;
+        p.a_s = mx4 ? p.k / 2 : p.k;
+        p.as_s = p.k / 32;
+    }
+    if (floats && !fuse)
+        ws += code_bytes(p.m, p.k, format) + round256(static_cast<int64_t>(p.m) * (p.k / 32));
     if (p.m <= kMxRowsMax) {
-        const bool fuse = floats && p.m <= kMxFuseRows;
-        if (floats && !fuse && p.k > 0) {
-            uint8_t *scales = p.workspace + code_bytes(p.m, p.k, format);
-            if (int e = launch_mx_quantize_rows(p.x, p.x_dtype, p.x_s, p.m, p.k, p.workspace, scales, format, stream))
-                return e;
-            p.a = p.workspace;
-            p.a_scale = scales;
-            p.a_s = mx4 ? p.k / 2 : p.k;
-            p.as_s = p.k / 32;
-        }
         const void *fn = by_out(out_dtype, [&](auto o) {
             using OT = decltype(o);
-            return mx4 ? stream_fn<OT, SSU_FORMAT_MXFP4>(p.m, fuse, p.x_dtype) : stream_fn<OT, SSU_FORMAT_MXFP8>(p.m, fuse, p.x_dtype);
+            return mx4 ? stream_fn<OT, SSU_FORMAT_MXFP4>(fuse, p.x_dtype) : stream_fn<OT, SSU_FORMAT_MXFP8>(fuse, p.x_dtype);
         });
         void *args[] = {&p};
         return run(fn, (p.n + kStreamRows - 1) / kStreamRows, kStreamWaves * 64, args, stream);
     }
 
     TileParams t = {};
-    t.ktiles = static_cast<int32_t>(ktiles_of(p.k, format));
-    uint8_t *ws = p.workspace;
-    PackParams q = {};
-    if (floats) {
-        q.x = p.x;
-        q.x_s = p.x_s;
-        q.codes = ws;
-        p.a = ws;
-        p.a_s = mx4 ? p.k / 2 : p.k;
-        ws += code_bytes(p.m, p.k, format);
-    } else {
-        q.a_scale = p.a_scale;
-        q.as_s = p.as_s;
-    }
-    q.a_packed = ws;
-    q.w_packed = reinterpret_cast<uint32_t *>(ws) + packed_room(p.m, t.ktiles);
-    q.w_scale = p.w_scale;
-    q.ws_s = p.ws_s;
-    q.m = p.m, q.n = p.n, q.k = p.k, q.ktiles = t.ktiles;
-    if (t.ktiles > 0) {
-        const int64_t a_work = floats ? static_cast<int64_t>(p.m) * t.ktiles * (ktile_depth(format) / 8) : packed_words(p.m, t.ktiles);
+    t.packed = packs_floats || !scales_in_place(shape, p.a_scale, p.as_s, p.k, format) ||
+               !scales_in_place(shape, p.w_scale, p.ws_s, p.k, format);
+    t.ktiles = static_cast<int32_t>(t.packed ? ktiles_of(p.k, format) : p.k / ktile_depth(format));
+    t.a_scales = p.a_scale;
+    t.w_scales = p.w_scale;
+    if (t.packed && t.ktiles > 0) {
+        PackParams q = {};
+        if (packs_floats) {
+            q.x = p.x;
+            q.x_s = p.x_s;
+            q.codes = p.workspace;
+            p.a = p.workspace;
+            p.a_s = mx4 ? p.k / 2 : p.k;
+        } else {
+            q.a_scale = p.a_scale;
+            q.as_s = p.as_s;
+        }
+        q.a_packed = ws;
+        q.w_packed = reinterpret_cast<uint32_t *>(ws) + packed_room(p.m, t.ktiles);
+        q.w_scale = p.w_scale;
+        q.ws_s = p.ws_s;
+        q.m = p.m, q.n = p.n, q.k = p.k, q.ktiles = t.ktiles;
+        const int64_t a_work = packs_floats ? static_cast<int64_t>(p.m) * t.ktiles * (ktile_depth(format) / 8) : packed_words(p.m, t.ktiles);
         const int64_t w_work = packed_words(p.n, t.ktiles);
         const auto groups = [](int64_t work) { return static_cast<int>(std::min<int64_t>((work + kQuantThreads - 1) / kQuantThreads, 32768)); };
         q.a_groups = groups(a_work);
-        const void *fn = !floats                ? pack_fn<void>(format)
+        const void *fn = !packs_floats          ? pack_fn<void>(format)
                          : p.x_dtype == SSU_F32 ? pack_fn<float>(format)
                          : p.x_dtype == SSU_F16 ? pack_fn<_Float16>(format)
                                                 : pack_fn<__bf16>(format);
         void *args[] = {&q};
         if (int e = run(fn, q.a_groups + groups(w_work), kQuantThreads, args, stream))
             return e;
+        t.a_scales = q.a_packed;
+        t.w_scales = reinterpret_cast<const uint8_t *>(q.w_packed);
     }
-    t.a_packed = reinterpret_cast<const uint32_t *>(q.a_packed);
-    t.w_packed = q.w_packed;
     t.p = p;
-    // the largest tile that leaves every compute unit one
-    int shape = 0;
-    auto tiles = [&](int s) {
-        return static_cast<int64_t>((p.m + kTileShapes[s].tm - 1) / kTileShapes[s].tm) * ((p.n + kTileShapes[s].tn - 1) / kTileShapes[s].tn);
-    };
-    while (shape < 2 && tiles(shape) < 256)
-        shape++;
     t.mtiles = (p.m + kTileShapes[shape].tm - 1) / kTileShapes[shape].tm;
     t.ntiles = (p.n + kTileShapes[shape].tn - 1) / kTileShapes[shape].tn;
     const void *fn = by_out(out_dtype, [&](auto o) {
@@ -736,7 +995,7 @@ int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *s
         return mx4 ? tile_fn<OT, SSU_FORMAT_MXFP4>(shape) : tile_fn<OT, SSU_FORMAT_MXFP8>(shape);
     });
     void *args[] = {&t};
-    return run(fn, tiles(shape), kTileShapes[shape].threads, args, stream);
+    return run(fn, static_cast<int64_t>(t.mtiles) * t.ntiles, kTileThreads, args, stream);
 }
 
 }  // namespace ssu
