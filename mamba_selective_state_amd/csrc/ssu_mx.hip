@@ -224,72 +224,85 @@ constexpr int ktile_depth(int format) { return format == SSU_FORMAT_MXFP8 ? 128 
 // K tiles of k values: an even number.
 constexpr int64_t ktiles_of(int64_t k, int format) { return (k + 2 * ktile_depth(format) - 1) / (2 * ktile_depth(format)) * 2; }
 
-// Packed scales: for every 32 rows and K tile, 64 words, one per lane of an
-// operand (row l % 32, group h = l / 32); byte s is the scale of block STEPS h + s of the tile, 0
+// Scales for the large tile, packed: for every 32 rows and K tile, 64 words, one per lane of
+// an operand (row l % 32, group h = l / 32); byte s is the scale of block STEPS h + s of the tile, 0
 // (2^-127) past the end of k. A tile reads its rows' scales without looking where the
 // rows end, so there is room for whole tiles; what lies past the last 32 rows
 // is not written and goes into sums that are not stored.
 __host__ __device__ constexpr int64_t packed_words(int64_t rows, int64_t ktiles) { return (rows + 31) / 32 * ktiles * 64; }
 constexpr int64_t packed_room(int64_t rows, int64_t ktiles) { return (rows + 255) / 256 * 8 * ktiles * 64; }
+// Scales for the smaller tiles: rows of bytes as they are, if they consist of aligned runs of 16
+// (k a multiple of 512); else copied to such rows, with 0 past the end of k.
+__host__ __device__ constexpr int64_t padded_scales(int64_t k) { return (k + 511) / 512 * 16; }
 
 struct PackParams {
-    // activations: floats to quantise (codes and packed scales), or codes whose scales are packed
+    // activations: floats to quantise, or scale bytes to lay out
     const void *x;
     const uint8_t *a_scale;
-    uint8_t *codes, *a_packed;
+    uint8_t *codes, *a_out;
     int64_t x_s, as_s;
     // weights' scales
     const uint8_t *w_scale;
-    uint32_t *w_packed;
+    uint8_t *w_out;
     int64_t ws_s;
-    int32_t m, n, k, ktiles;
-    int32_t a_groups;  // workgroups that work on the activations; the rest pack the weights' scales
+    int32_t m, n, k;
+    int32_t ktiles;    // even; 0: padded rows
+    int32_t a_groups;  // workgroups that work on the activations; the rest lay out the weights' scales
 };
 
 template <int FORMAT>
-__device__ __forceinline__ void pack_scales(const uint8_t *scale, int64_t stride, int32_t rows, int32_t blocks, int32_t ktiles,
-                                            uint32_t *packed, int64_t first, int64_t step) {
+__device__ __forceinline__ void lay_out_scales(const uint8_t *scale, int64_t stride, int32_t rows, int32_t k, int32_t ktiles,
+                                               uint8_t *out, int64_t first, int64_t step) {
     constexpr int kSteps = KTile<FORMAT>::kSteps;
-    const int64_t words = packed_words(rows, ktiles);
-    for (int64_t i = first; i < words; i += step) {
-        const int l = static_cast<int>(i % 64);
-        const int64_t t = i / 64;
-        const int kt = static_cast<int>(t % ktiles);
-        const int64_t row = min(t / ktiles * 32 + l % 32, static_cast<int64_t>(rows) - 1);
-        const int b = (2 * kt + l / 32) * kSteps;
-        typedef uint32_t Word __attribute__((aligned(1)));
+    typedef uint32_t Word __attribute__((aligned(1)));
+    const int blocks = k / 32;
+    // the four bytes of a row from block b on
+    auto word = [&](int64_t row, int b, int want) {
+        if (b + 4 <= blocks)
+            return static_cast<uint32_t>(*reinterpret_cast<const Word *>(scale + row * stride + b));
         uint32_t v = 0;
-        if (b + 4 <= blocks) {
-            v = *reinterpret_cast<const Word *>(scale + row * stride + b);
-        } else {
-#pragma unroll
-            for (int s = 0; s < kSteps; s++)
-                if (b + s < blocks)
-                    v |= static_cast<uint32_t>(scale[row * stride + b + s]) << (8 * s);
+        for (int s = 0; s < want; s++)
+            if (b + s < blocks)
+                v |= static_cast<uint32_t>(scale[row * stride + b + s]) << (8 * s);
+        return v;
+    };
+    uint32_t *words = reinterpret_cast<uint32_t *>(out);
+    if (ktiles > 0) {
+        const int64_t total = packed_words(rows, ktiles);
+        for (int64_t i = first; i < total; i += step) {
+            const int l = static_cast<int>(i % 64);
+            const int64_t t = i / 64;
+            const int kt = static_cast<int>(t % ktiles);
+            const int64_t row = min(t / ktiles * 32 + l % 32, static_cast<int64_t>(rows) - 1);
+            words[i] = word(row, (2 * kt + l / 32) * kSteps, kSteps);  // of MXFP8 the low half counts
         }
-        packed[i] = v;  // of MXFP8 the low half counts
+    } else {
+        const int64_t per = padded_scales(k) / 4;
+        for (int64_t i = first; i < rows * per; i += step)
+            words[i] = word(i / per, static_cast<int>(i % per) * 4, 4);
     }
 }
 
-// What the tiled kernels need besides the codes: the weights' scales packed,
-// and the activations' (quantised here when they come as floats).
+// What the tiled kernels need besides the codes: scales laid out, and activations that come as
+// floats quantised.
 template <typename FT, int FORMAT>
 __global__ __launch_bounds__(kQuantThreads) void mx_pack_kernel(const PackParams p) {
     constexpr int kSteps = KTile<FORMAT>::kSteps;
-    const int blocks = p.k / 32;
     if (static_cast<int>(blockIdx.x) >= p.a_groups) {
         const int64_t at = static_cast<int64_t>(blockIdx.x - p.a_groups) * kQuantThreads + threadIdx.x;
-        pack_scales<FORMAT>(p.w_scale, p.ws_s, p.n, blocks, p.ktiles, p.w_packed, at,
-                            static_cast<int64_t>(gridDim.x - p.a_groups) * kQuantThreads);
+        lay_out_scales<FORMAT>(p.w_scale, p.ws_s, p.n, p.k, p.ktiles, p.w_out, at,
+                               static_cast<int64_t>(gridDim.x - p.a_groups) * kQuantThreads);
         return;
     }
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kQuantThreads + threadIdx.x;
     const int64_t step = static_cast<int64_t>(p.a_groups) * kQuantThreads;
     if constexpr (std::is_void_v<FT>) {
-        pack_scales<FORMAT>(p.a_scale, p.as_s, p.m, blocks, p.ktiles, reinterpret_cast<uint32_t *>(p.a_packed), first, step);
+        lay_out_scales<FORMAT>(p.a_scale, p.as_s, p.m, p.k, p.ktiles, p.a_out, first, step);
     } else {
-        // four lanes per block of 32, over whole K tiles: the blocks past the end of k get the scale byte 0 and no codes
-        const int64_t eighths = static_cast<int64_t>(p.ktiles) * (KTile<FORMAT>::kDepth / 8);
+        // four lanes per block of 32, over whole K tiles (or padded rows): the blocks past the end of k
+        // get the scale byte 0 and no codes
+        const int64_t row_scales = p.ktiles > 0 ? static_cast<int64_t>(p.ktiles) * (KTile<FORMAT>::kDepth / 32) : padded_scales(p.k);
+        const int64_t eighths = row_scales * 4;
         const int64_t total = p.m * eighths;
         for (int64_t i = first; i < total; i += step) {
             const int64_t row = i / eighths;
@@ -303,9 +316,12 @@ __global__ __launch_bounds__(kQuantThreads) void mx_pack_kernel(const PackParams
                 store_codes<FORMAT>(p.codes + row * (FORMAT == SSU_FORMAT_MXFP4 ? p.k / 2 : p.k), at, code);
             }
             if (i % 4 == 0) {
-                const int kt = b / (2 * kSteps), in = b % (2 * kSteps);
-                const int64_t word = (row / 32 * p.ktiles + kt) * 64 + in / kSteps * 32 + row % 32;
-                p.a_packed[word * 4 + in % kSteps] = static_cast<uint8_t>(sc);
+                int64_t to = row * row_scales + b;
+                if (p.ktiles > 0) {
+                    const int kt = b / (2 * kSteps), in = b % (2 * kSteps);
+                    to = ((row / 32 * p.ktiles + kt) * 64 + in / kSteps * 32 + row % 32) * 4 + in % kSteps;
+                }
+                p.a_out[to] = static_cast<uint8_t>(sc);
             }
         }
     }
@@ -313,8 +329,7 @@ __global__ __launch_bounds__(kQuantThreads) void mx_pack_kernel(const PackParams
 
 struct TileParams {
     MxParams p;
-    const uint8_t *a_scales, *w_scales;  // packed words, or rows of scale bytes (p.as_s, p.ws_s)
-    int32_t packed;
+    const uint8_t *a_scales, *w_scales;  // packed words, or rows of scale bytes (p.as_s, p.ws_s: multiples of 16)
     int32_t ktiles, mtiles, ntiles;
 };
 
@@ -623,25 +638,30 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
     finish_tile<OT, FM, FN, WM, WN, WK, kStage>(p, acc, lds0, lds1, m0, n0, l, wave);
 }
 
-// The smaller tiles: too little work per K tile to hide a fetch behind one of them, so STAGES images
-// take turns and a fetch has STAGES - 1 tiles' time. A wave waits for the fetches that the
-// next tile needs and no more: only fetches count in vmcnt here (scales come through LDS as well),
-// every tile issues the same number of them, and they arrive in order.
-template <typename OT, int FORMAT, int TM, int TN, int WM, int WN, int WK, int STAGES>
+// The smaller tiles: too little work per K tile to hide a fetch behind one of them, so four images
+// of SUB K tiles take turns. A wave waits for the fetches that the next products need and no
+// more: only fetches count in vmcnt here, every image issues the same number of them, and they
+// arrive in order. The scale bytes of four images (a round) come together, 16 bytes of a row at a time, into
+// one of two places: a word for each lane and K tile took as long as all the codes.
+template <typename OT, int FORMAT, int TM, int TN, int WM, int WN, int WK, int SUB>
 __global__ __launch_bounds__(64 * WM * WN * WK) void mx_ring_kernel(const TileParams t) {
     using KT = KTile<FORMAT>;
     constexpr int kWaves = WM * WN * WK;
     constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
     constexpr int kSteps = KT::kSteps / WK;
-    constexpr int kABytes = TM * KT::kARow, kCodes = kABytes + TN * KT::kWRow;
-    constexpr int kScaleTiles = (TM + TN) / 32, kScaleLoads = kScaleTiles / kWaves;  // of 64 words
-    constexpr int kStage = kCodes + kScaleTiles * 256;
-    static_assert(kScaleLoads * kWaves == kScaleTiles, "whole words per wave");
-    static_assert(STAGES == 4 || STAGES == 8, "images");
+    constexpr int kImages = 4;
+    constexpr int kABytes = TM * KT::kARow, kOne = kABytes + TN * KT::kWRow, kStage = SUB * kOne;  // of a K tile, of an image
+    // scale bytes of a round: kRuns runs of 16 per row, the runs permuted so that 16 neighbouring rows'
+    // words lie on different banks
+    constexpr int kRoundK = kImages * SUB * KT::kDepth;
+    constexpr int kRuns = kRoundK / 512, kScaleRow = 16 * kRuns;
+    constexpr int kScaleKiB = (TM + TN) * kScaleRow / 1024;
+    constexpr int kScaleLoads = kScaleKiB > kWaves ? kScaleKiB / kWaves : 1;
+    static_assert(kScaleKiB % kWaves == 0 || kWaves % kScaleKiB == 0, "every wave fetches as many");
+    static_assert(SUB == 1 || kSteps == 1, "images of several K tiles are for one step per tile");
     // arrays of their own: the compiler tells fills of one from reads of another
     __shared__ alignas(16) uint8_t s0[kStage], s1[kStage], s2[kStage], s3[kStage];
-    __shared__ alignas(16) uint8_t s4[STAGES > 4 ? kStage : 16], s5[STAGES > 4 ? kStage : 16], s6[STAGES > 4 ? kStage : 16],
-        s7[STAGES > 4 ? kStage : 16];
+    __shared__ alignas(16) uint8_t c0[(TM + TN) * kScaleRow], c1[(TM + TN) * kScaleRow];
     const MxParams &p = t.p;
     const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int r = l % 32, h = l / 32;
@@ -652,40 +672,47 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_ring_kernel(const TilePa
 
     const Filler<TM, KT::kARow, kWaves> fill_a(p.a, p.a_s, m0, p.m, FORMAT == SSU_FORMAT_MXFP8 ? p.k : p.k / 2, wave, l);
     const Filler<TN, KT::kWRow, kWaves> fill_w(p.w, p.w_s, n0, p.n, p.k / 2, wave, l);
-    // scale words: packed, or straight from rows of bytes (a word of MXFP4's is the four of
-    // half h, of MXFP8's the four of the tile)
+    constexpr int kLoads = SUB * (decltype(fill_a)::kLoads + decltype(fill_w)::kLoads);
+    // the waits count fetches in the order in which they are written down here
+    auto in_order = [] {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // image number `n` of the sequence
+    auto fill = [&](uint8_t *lds, int n) {
+        in_order();
+#pragma unroll
+        for (int u = 0; u < SUB; u++) {
+            fill_a.load(n * SUB + u, lds + u * kOne, wave);
+            fill_w.load(n * SUB + u, lds + u * kOne + kABytes, wave);
+        }
+        in_order();
+    };
+    auto permuted = [](int row, int run) { return kRuns == 4 ? run ^ ((row >> 2) & 3) : kRuns == 2 ? run ^ ((row >> 3) & 1) : run; };
     const uint8_t *scale[kScaleLoads];
+    int scale_at[kScaleLoads];
 #pragma unroll
     for (int i = 0; i < kScaleLoads; i++) {
-        const int tile = wave + kWaves * i;
-        const bool is_a = tile < TM / 32;
-        const int row0 = is_a ? m0 + tile * 32 : n0 + (tile - TM / 32) * 32;
-        const uint8_t *base = is_a ? t.a_scales : t.w_scales;
-        if (t.packed)
-            scale[i] = base + (static_cast<int64_t>(row0 / 32) * t.ktiles * 64 + l) * 4;
-        else
-            scale[i] = base + static_cast<int64_t>(min(row0 + r, (is_a ? p.m : p.n) - 1)) * (is_a ? p.as_s : p.ws_s) +
-                       (FORMAT == SSU_FORMAT_MXFP8 ? 0 : 4 * h);
+        const int unit = (wave + kWaves * i) % kScaleKiB * 64 + l, row = unit / kRuns;  // waves too many fetch the same again
+        const bool is_a = row < TM;
+        scale[i] = is_a ? t.a_scales + min(m0 + row, p.m - 1) * p.as_s : t.w_scales + min(n0 + row - TM, p.n - 1) * p.ws_s;
+        scale_at[i] = permuted(row, unit % kRuns) * 16;
     }
-    const int scale_step = t.packed ? 256 : KT::kDepth / 32;
-    const int shift = 8 * wk + (FORMAT == SSU_FORMAT_MXFP8 && !t.packed ? 16 * h : 0);
-    constexpr int kLoads = decltype(fill_a)::kLoads + decltype(fill_w)::kLoads + kScaleLoads;
-    auto fill = [&](uint8_t *lds, int kt) {
-        fill_a.load(kt, lds, wave);
-        fill_w.load(kt, lds + kABytes, wave);
-        const int64_t at = static_cast<int64_t>(min(kt, t.ktiles - 1)) * scale_step;
+    const int scale_last = t.ktiles * (KT::kDepth / 32) - 16;
+    // the scales of round `n`; past the end the last run
+    auto fill_scales = [&](uint8_t *lds, int n) {
 #pragma unroll
         for (int i = 0; i < kScaleLoads; i++)
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void *)(scale[i] + at),
-                (__attribute__((address_space(3))) void *)(lds + kCodes + (wave + kWaves * i) * 256), 4, 0, 0);
+            load_to_lds(scale[i] + min(n * kScaleRow + scale_at[i], scale_last), lds + (wave + kWaves * i) % kScaleKiB * 1024);
+        in_order();
     };
-    struct Frags {
+    struct Operands {
         std::conditional_t<FORMAT == SSU_FORMAT_MXFP8, i32x8, i32x4> a[FM];
         i32x4 w[FN];
     };
+    // operands of this wave's step `j` of the K tile at `src`
     auto read = [&](const uint8_t *src, int j) {
-        Frags f;
+        Operands f;
         const int s = wk + WK * j;
 #pragma unroll
         for (int i = 0; i < FM; i++) {
@@ -702,25 +729,43 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_ring_kernel(const TilePa
                                                       lds_chunk<KT::kWRow>((wn * FN + i) * 32 + r, KT::kSteps * h + s));
         return f;
     };
-    int asc[FM], wsc[FN];
-    auto read_scales = [&](const uint8_t *src) {
-        const uint32_t *words = reinterpret_cast<const uint32_t *>(src + kCodes) + l;
+    // Words with the scales of K tile `kt` of a round: of MXFP4 the four bytes of half h, of
+    // MXFP8 all four, of which the half is the upper or the lower two.
+    struct Scales {
+        uint32_t a[FM], w[FN];
+    };
+    constexpr int kWord = FORMAT == SSU_FORMAT_MXFP8 ? 4 : 8;  // bytes of a row per K tile
+    auto read_scales = [&](const uint8_t *src, int kt) {
+        Scales f;
+        auto word = [&](int row) {
+            const int byte = kt * kWord + (FORMAT == SSU_FORMAT_MXFP8 ? 0 : 4 * h);
+            return *reinterpret_cast<const uint32_t *>(src + row * kScaleRow + permuted(row, byte / 16) * 16 + byte % 16);
+        };
 #pragma unroll
         for (int i = 0; i < FM; i++)
-            asc[i] = static_cast<int>(words[(wm * FM + i) * 64]);
+            f.a[i] = word((wm * FM + i) * 32 + r);
 #pragma unroll
         for (int i = 0; i < FN; i++)
-            wsc[i] = static_cast<int>(words[(TM / 32 + wn * FN + i) * 64]);
+            f.w[i] = word(TM + (wn * FN + i) * 32 + r);
+        return f;
     };
+    const int shift = 8 * wk + (FORMAT == SSU_FORMAT_MXFP8 ? 16 * h : 0);
     f32x16 acc[FM][FN] = {};
-    auto multiply = [&](const Frags &f, auto jc) {
+    auto multiply = [&](const Operands &f, const Scales &sc, auto jc) {
         constexpr int kByte = decltype(jc)::value * WK;
+        int as[FM], ws[FN];
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+            as[i] = static_cast<int>(sc.a[i] >> shift);
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+            ws[i] = static_cast<int>(sc.w[i] >> shift);
 #pragma unroll
         for (int i = 0; i < FM; i++)
 #pragma unroll
             for (int j = 0; j < FN; j++)
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    wide(f.w[j]), wide(f.a[i]), acc[i][j], kE2M1, FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, kByte, wsc[j], kByte, asc[i]);
+                    wide(f.w[j]), wide(f.a[i]), acc[i][j], kE2M1, FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, kByte, ws[j], kByte, as[i]);
     };
     // waits until at most `pending` fetches of this wave are outstanding (and no LDS access, if
     // `lds`), then for the other waves
@@ -732,97 +777,93 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_ring_kernel(const TilePa
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    uint8_t *const images[8] = {s0, s1, s2, s3, s4, s5, s6, s7};
-    if (t.ktiles > 0) {
-        for_passes<0, STAGES>([&](auto sc) { fill(images[decltype(sc)::value], decltype(sc)::value); });
+    uint8_t *const images[kImages] = {s0, s1, s2, s3};
+    uint8_t *const places[2] = {c0, c1};
+    const int all = t.ktiles / SUB;
+    if (all > 0) {
+        int n = 0;
+        bool done = false;
         if constexpr (kSteps == 1) {
-            // A wave has one step per K tile: its operands are read two tiles ahead, so that neither
-            // the fetch nor the LDS is waited for. When a wave arrives, it has multiplied tile
-            // kt, so its reads of that image are complete and the image can be filled.
-            arrive(std::integral_constant<int, (STAGES - 2) * kLoads>(), std::true_type());
-            Frags cur = read(s0, 0), next = read(s1, 0);
-            int a0[FM], w0[FN], a1[FM], w1[FN];
-            auto words = [&](const uint8_t *src, int (&a)[FM], int (&w)[FN]) {
-                read_scales(src);
-#pragma unroll
-                for (int i = 0; i < FM; i++)
-                    a[i] = asc[i];
-#pragma unroll
-                for (int i = 0; i < FN; i++)
-                    w[i] = wsc[i];
+            // A wave has one step per K tile: its operands are read two images ahead, so that neither
+            // the fetch nor the LDS is waited for. When the waves have arrived, all have multiplied image
+            // n, so their reads of it, and of the scales up to its own, are complete: it can be filled
+            // again, and behind a round's last image the place of its scales. In order of issue:
+            // image 4 i + 3, scales of round i + 1, image 4 i + 4, ...
+            fill_scales(c0, 0);
+            fill(s0, 0);
+            fill(s1, 1);
+            fill(s2, 2);
+            fill(s3, 3);
+            fill_scales(c1, 1);
+            arrive(std::integral_constant<int, 2 * kLoads + kScaleLoads>(), std::true_type());
+            struct Image {
+                Operands f[SUB];
+                Scales s[SUB];
             };
-            words(s0, a0, w0);
-            words(s1, a1, w1);
-            int kt = 0;
-            bool done = false;
+            auto read_all = [&](const uint8_t *src, const uint8_t *scales, int i) {
+                Image o;
+#pragma unroll
+                for (int u = 0; u < SUB; u++) {
+                    o.f[u] = read(src + u * kOne, 0);
+                    o.s[u] = read_scales(scales, i * SUB + u);
+                }
+                return o;
+            };
+            Image cur = read_all(s0, c0, 0), next = read_all(s1, c0, 1);
             while (!done) {
-                for_passes<0, STAGES>([&](auto sc) {
-                    constexpr int s = decltype(sc)::value;
+                for_passes<0, 2 * kImages>([&](auto ic) {
+                    constexpr int i = decltype(ic)::value % kImages, round = decltype(ic)::value / kImages;
+                    constexpr bool kBehindScales = i < 2;  // the scales were issued after what is waited for
                     if (done)
                         return;
 #pragma unroll
-                    for (int i = 0; i < FM; i++)
-                        asc[i] = a0[i] >> shift;
-#pragma unroll
-                    for (int i = 0; i < FN; i++)
-                        wsc[i] = w0[i] >> shift;
-                    multiply(cur, std::integral_constant<int, 0>());
+                    for (int u = 0; u < SUB; u++)
+                        multiply(cur.f[u], cur.s[u], std::integral_constant<int, 0>());
                     __builtin_amdgcn_sched_barrier(0);
-                    arrive(std::integral_constant<int, (STAGES - 3) * kLoads>(), std::false_type());
+                    arrive(std::integral_constant<int, kLoads + (kBehindScales ? kScaleLoads : 0)>(), std::false_type());
                     cur = next;
-#pragma unroll
-                    for (int i = 0; i < FM; i++)
-                        a0[i] = a1[i];
-#pragma unroll
-                    for (int i = 0; i < FN; i++)
-                        w0[i] = w1[i];
-                    next = read(images[(s + 2) % STAGES], 0);
-                    words(images[(s + 2) % STAGES], a1, w1);
-                    __builtin_amdgcn_sched_barrier(0);
-                    fill(images[s], kt + STAGES);
-                    done = ++kt >= t.ktiles;
+                    next = read_all(images[(i + 2) % kImages], places[i < 2 ? round : 1 - round], (i + 2) % kImages);
+                    fill(images[i], n + kImages);
+                    if constexpr (i == kImages - 1)
+                        fill_scales(places[round], n / kImages + 2);
+                    done = ++n >= all;
                 });
             }
         } else {
-            arrive(std::integral_constant<int, (STAGES - 1) * kLoads>(), std::true_type());
-            Frags cur = read(s0, 0);
-            auto shifted_scales = [&](const uint8_t *src) {
-                read_scales(src);
-#pragma unroll
-                for (int i = 0; i < FM; i++)
-                    asc[i] >>= shift;
-#pragma unroll
-                for (int i = 0; i < FN; i++)
-                    wsc[i] >>= shift;
-            };
-            shifted_scales(s0);
-            auto tile = [&](uint8_t *here, uint8_t *there, int kt) {
-                for_passes<0, kSteps>([&](auto jc) {
-                    constexpr int j = decltype(jc)::value;
-                    Frags next;
-                    if constexpr (j + 1 < kSteps) {
-                        next = read(here, j + 1);
-                        multiply(cur, jc);
-                    } else {
-                        // the products first: they need nothing that is still on its way
-                        multiply(cur, jc);
-                        arrive(std::integral_constant<int, (STAGES - 2) * kLoads>(), std::true_type());
-                        next = read(there, 0);
-                        shifted_scales(there);
-                        fill(here, kt + STAGES);
-                    }
-                    cur = next;
-                });
-            };
-            int kt = 0;
-            bool done = false;
+            // The same with operands read a step ahead.
+            fill_scales(c0, 0);
+            fill(s0, 0);
+            fill(s1, 1);
+            fill(s2, 2);
+            fill(s3, 3);
+            fill_scales(c1, 1);
+            arrive(std::integral_constant<int, 3 * kLoads + kScaleLoads>(), std::true_type());
+            Operands cur = read(s0, 0);
+            Scales sc = read_scales(c0, 0);
             while (!done) {
-                for_passes<0, STAGES>([&](auto sc) {
-                    constexpr int s = decltype(sc)::value;
+                for_passes<0, 2 * kImages>([&](auto ic) {
+                    constexpr int i = decltype(ic)::value % kImages, round = decltype(ic)::value / kImages;
                     if (done)
                         return;
-                    tile(images[s], images[(s + 1) % STAGES], kt);
-                    done = ++kt >= t.ktiles;
+                    for_passes<0, kSteps>([&](auto jc) {
+                        constexpr int j = decltype(jc)::value;
+                        Operands next;
+                        if constexpr (j + 1 < kSteps) {
+                            next = read(images[i], j + 1);
+                            multiply(cur, sc, jc);
+                        } else {
+                            // the products first: they need nothing that is still on its way
+                            multiply(cur, sc, jc);
+                            arrive(std::integral_constant<int, 2 * kLoads + (i < kImages - 1 ? kScaleLoads : 0)>(), std::true_type());
+                            next = read(images[(i + 1) % kImages], 0);
+                            sc = read_scales(places[i < 3 ? round : 1 - round], (i + 1) % kImages);
+                            fill(images[i], n + kImages);
+                            if constexpr (i == kImages - 1)
+                                fill_scales(places[round], n / kImages + 2);
+                        }
+                        cur = next;
+                    });
+                    done = ++n >= all;
                 });
             }
         }
@@ -863,25 +904,24 @@ const void *tile_fn(int shape) {
     constexpr int kWk = KTile<FORMAT>::kSteps;
     switch (shape) {
     case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 256, 256, 2, 2, 1>);
-    case 1: return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 128, 128, 2, 2, 1, 4>);
-    case 2: return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 4>);
+    case 1: return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 128, 128, 2, 2, 1, 1>);
+    case 2: return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 1>);
     }
-    return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 8>);
+    return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 2>);
 }
 
-// The largest tile that leaves every compute unit one; of the smallest, the form with eight
-// images if no unit gets a second one, else the one with four, of which two fit a unit.
+// The largest tile that leaves every compute unit one; of the smallest, the form with images of
+// two K tiles if no unit gets a second workgroup, else the one with images of one, of which two
+// workgroups fit a unit.
 int tile_shape(int64_t m, int64_t n) {
     for (int s = 0; s < 3; s++)
         if (((m + kTileShapes[s].tm - 1) / kTileShapes[s].tm) * ((n + kTileShapes[s].tn - 1) / kTileShapes[s].tn) >= (s < 2 ? 256 : 257))
             return s;
     return 3;
 }
-// Whether a tile's scale words can be fetched where the bytes are: the large tile packs them first (it
-// would fetch a line for eight bytes of each of 512 rows), and so do words that are not aligned or
-// reach past the end of k.
-bool scales_in_place(int shape, const void *base, int64_t stride, int64_t k, int format) {
-    return shape != 0 && k % ktile_depth(format) == 0 && stride % 4 == 0 && reinterpret_cast<uintptr_t>(base) % 4 == 0;
+// Whether a smaller tile can fetch scale bytes where they are (see padded_scales).
+bool scales_in_place(const void *base, int64_t stride, int64_t k) {
+    return k % 512 == 0 && stride % 16 == 0 && reinterpret_cast<uintptr_t>(base) % 16 == 0;
 }
 
 template <typename F>
@@ -914,34 +954,29 @@ int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t 
 }
 
 int64_t mx_linear_workspace(int64_t m, int64_t n, int64_t k, int format, bool floats) {
-    const int64_t quantised = floats && m > kMxFuseRows ? code_bytes(m, k, format) + round256(m * (k / 32)) : 0;
+    const int64_t codes = floats && m > kMxFuseRows ? code_bytes(m, k, format) : 0;
     if (m <= kMxRowsMax)
-        return quantised;
-    const int64_t ktiles = ktiles_of(k, format);
-    return quantised + 4 * (packed_room(m, ktiles) + packed_room(n, ktiles));
+        return codes > 0 ? codes + m * (k / 32) : 0;
+    if (tile_shape(m, n) == 0)
+        return codes + 4 * (packed_room(m, ktiles_of(k, format)) + packed_room(n, ktiles_of(k, format)));
+    return codes + (m + n) * padded_scales(k);
 }
 
 int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *stream) {
     MxParams p = args_in;
     const bool mx4 = format == SSU_FORMAT_MXFP4;
     const bool floats = p.x != nullptr;
-    uint8_t *ws = p.workspace;
-    const bool fuse = floats && p.m <= kMxFuseRows;
-    const int shape = tile_shape(p.m, p.n);
-    // where scales are packed, the activations are quantised in the same launch
-    const bool packs_floats = floats && p.m > kMxRowsMax && !scales_in_place(shape, p.w_scale, p.ws_s, p.k, format);
-    if (floats && !fuse && !packs_floats && p.k > 0) {
-        uint8_t *scales = ws + code_bytes(p.m, p.k, format);
-        if (int e = launch_mx_quantize_rows(p.x, p.x_dtype, p.x_s, p.m, p.k, ws, scales, format, stream))
-            return e;
-        p.a = ws;
-        p.a_scale = scales;
-        p.a_s = mx4 ? p.k / 2 : p.k;
-        p.as_s = p.k / 32;
-    }
-    if (floats && !fuse)
-        ws += code_bytes(p.m, p.k, format) + round256(static_cast<int64_t>(p.m) * (p.k / 32));
     if (p.m <= kMxRowsMax) {
+        const bool fuse = floats && p.m <= kMxFuseRows;
+        if (floats && !fuse && p.k > 0) {
+            uint8_t *scales = p.workspace + code_bytes(p.m, p.k, format);
+            if (int e = launch_mx_quantize_rows(p.x, p.x_dtype, p.x_s, p.m, p.k, p.workspace, scales, format, stream))
+                return e;
+            p.a = p.workspace;
+            p.a_scale = scales;
+            p.a_s = mx4 ? p.k / 2 : p.k;
+            p.as_s = p.k / 32;
+        }
         const void *fn = by_out(out_dtype, [&](auto o) {
             using OT = decltype(o);
             return mx4 ? stream_fn<OT, SSU_FORMAT_MXFP4>(fuse, p.x_dtype) : stream_fn<OT, SSU_FORMAT_MXFP8>(fuse, p.x_dtype);
@@ -950,42 +985,53 @@ int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *s
         return run(fn, (p.n + kStreamRows - 1) / kStreamRows, kStreamWaves * 64, args, stream);
     }
 
+    const int shape = tile_shape(p.m, p.n);
     TileParams t = {};
-    t.packed = packs_floats || !scales_in_place(shape, p.a_scale, p.as_s, p.k, format) ||
-               !scales_in_place(shape, p.w_scale, p.ws_s, p.k, format);
-    t.ktiles = static_cast<int32_t>(t.packed ? ktiles_of(p.k, format) : p.k / ktile_depth(format));
+    t.ktiles = static_cast<int32_t>(shape == 0 ? ktiles_of(p.k, format) : padded_scales(p.k) * 32 / ktile_depth(format));
     t.a_scales = p.a_scale;
     t.w_scales = p.w_scale;
-    if (t.packed && t.ktiles > 0) {
-        PackParams q = {};
-        if (packs_floats) {
-            q.x = p.x;
-            q.x_s = p.x_s;
-            q.codes = p.workspace;
-            p.a = p.workspace;
-            p.a_s = mx4 ? p.k / 2 : p.k;
-        } else {
-            q.a_scale = p.a_scale;
-            q.as_s = p.as_s;
-        }
-        q.a_packed = ws;
-        q.w_packed = reinterpret_cast<uint32_t *>(ws) + packed_room(p.m, t.ktiles);
+    // one launch before the product for what has to be quantised or laid out
+    PackParams q = {};
+    q.m = p.m, q.n = p.n, q.k = p.k;
+    q.ktiles = shape == 0 ? t.ktiles : 0;
+    uint8_t *ws = p.workspace;
+    int64_t a_work = 0, w_work = 0;
+    if (floats) {
+        q.x = p.x;
+        q.x_s = p.x_s;
+        q.codes = ws;
+        p.a = ws;
+        p.a_s = mx4 ? p.k / 2 : p.k;
+        ws += code_bytes(p.m, p.k, format);
+        a_work = static_cast<int64_t>(p.m) * (shape == 0 ? t.ktiles * (ktile_depth(format) / 8) : padded_scales(p.k) * 4);
+    } else if (shape == 0 || !scales_in_place(p.a_scale, p.as_s, p.k)) {
+        q.a_scale = p.a_scale;
+        q.as_s = p.as_s;
+        a_work = shape == 0 ? packed_words(p.m, t.ktiles) : p.m * padded_scales(p.k) / 4;
+    }
+    if (a_work > 0) {
+        q.a_out = ws;
+        t.a_scales = ws;
+        p.as_s = padded_scales(p.k);
+    }
+    if (shape == 0 || !scales_in_place(p.w_scale, p.ws_s, p.k)) {
         q.w_scale = p.w_scale;
         q.ws_s = p.ws_s;
-        q.m = p.m, q.n = p.n, q.k = p.k, q.ktiles = t.ktiles;
-        const int64_t a_work = packs_floats ? static_cast<int64_t>(p.m) * t.ktiles * (ktile_depth(format) / 8) : packed_words(p.m, t.ktiles);
-        const int64_t w_work = packed_words(p.n, t.ktiles);
+        q.w_out = ws + (shape == 0 ? 4 * packed_room(p.m, t.ktiles) : p.m * padded_scales(p.k));
+        w_work = shape == 0 ? packed_words(p.n, t.ktiles) : p.n * padded_scales(p.k) / 4;
+        t.w_scales = q.w_out;
+        p.ws_s = padded_scales(p.k);
+    }
+    if (a_work + w_work > 0) {
         const auto groups = [](int64_t work) { return static_cast<int>(std::min<int64_t>((work + kQuantThreads - 1) / kQuantThreads, 32768)); };
         q.a_groups = groups(a_work);
-        const void *fn = !packs_floats          ? pack_fn<void>(format)
+        const void *fn = !floats                ? pack_fn<void>(format)
                          : p.x_dtype == SSU_F32 ? pack_fn<float>(format)
                          : p.x_dtype == SSU_F16 ? pack_fn<_Float16>(format)
                                                 : pack_fn<__bf16>(format);
         void *args[] = {&q};
         if (int e = run(fn, q.a_groups + groups(w_work), kQuantThreads, args, stream))
             return e;
-        t.a_scales = q.a_packed;
-        t.w_scales = reinterpret_cast<const uint8_t *>(q.w_packed);
     }
     t.p = p;
     t.mtiles = (p.m + kTileShapes[shape].tm - 1) / kTileShapes[shape].tm;
