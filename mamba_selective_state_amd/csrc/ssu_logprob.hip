@@ -105,35 +105,33 @@ __device__ __forceinline__ RowView<T> row_view(const LogprobParams &p, int64_t r
     return v;
 }
 
-// The given token's logit, -inf if it is not allowed.
+// The given token's logit (-inf if it is not allowed) and how many allowed logits equal it at
+// lower indices of its access: the scan takes of that access only the logits above it. Eight lanes
+// fetch the access's logits together.
 template <typename T>
-__device__ __forceinline__ float token_logit(const RowView<T> &v) {
-    if (!v.inside)
-        return -__builtin_inff();
-    const bool listed = !v.mask || (v.mask[v.token / 8] >> (v.token % 8)) & 1;
-    const float x = widen(v.x[v.token]);
-    return listed ? x : -__builtin_inff();
+__device__ __forceinline__ void token_logit(const RowView<T> &v, int vocab, int lane, float *mine, int *equal) {
+    const int token = v.inside ? static_cast<int>(v.token) : 0;
+    const int at = token / kVec * kVec + lane;
+    const bool mine_lane = lane < kVec && at < vocab && v.inside;
+    float x = -__builtin_inff();
+    if (mine_lane) {
+        x = widen(v.x[at]);
+        if (v.mask && !((v.mask[at / 8] >> (at % 8)) & 1))
+            x = -__builtin_inff();
+    }
+    *mine = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), token % kVec));
+    *equal = __popcll(__ballot(mine_lane && at < token && x == *mine));
 }
 
-// What the scan did not count: in the access that holds the token it took the logits
-// above the token's only; here come the equal ones at lower indices.
-template <typename T>
-__device__ __forceinline__ int equal_before(const RowView<T> &v, float mine) {
-    int n = 0;
-    for (int64_t i = v.token / kVec * kVec; i < v.token; i++)
-        n += (!v.mask || (v.mask[i / 8] >> (i % 8)) & 1) && widen(v.x[i]) == mine;
-    return n;
-}
-
-// Writes a row's results (one thread; `mine`: the token's logit, `logs`: log s).
-template <typename T>
-__device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, const RowView<T> &v, const Sums &r, float mine,
+// Writes a row's results (one thread; `mine`: the token's logit, `equal`: see token_logit, `logs`:
+// log s).
+__device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, const Sums &r, float mine, int equal, float inv,
                                           bool bad, float logs) {
     const bool have = mine > -__builtin_inff();
     const float nan = __builtin_nanf("");
-    p.logprob[row] = bad ? nan : have ? (mine - r.m) * v.inv - logs : -__builtin_inff();
+    p.logprob[row] = bad ? nan : have ? (mine - r.m) * inv - logs : -__builtin_inff();
     p.entropy[row] = bad ? nan : r.s > 0.0f ? fmaxf(logs - r.t / r.s * 0.693147180559945309f, 0.0f) : 0.0f;
-    p.rank[row] = bad || !have ? -1 : r.before + equal_before(v, mine);
+    p.rank[row] = bad || !have ? -1 : r.before + equal;
 }
 
 __device__ __forceinline__ void write_alternative(const LogprobParams &p, int64_t row, int place, uint64_t key, const Sums &r,
@@ -295,7 +293,9 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
         fetch_round(t, raw, bits);
     else if (t < end)
         fetch_one(t, raw, bits);
-    const float mine = token_logit(v);
+    float mine;
+    int equal;
+    token_logit(v, p.vocab, lane, &mine, &equal);
     const bool counted = mine > -__builtin_inff();
     const int token = counted ? static_cast<int>(v.token) : 0;
     // logits above it stand before the token: at lower indices the equal ones too
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
         const bool bad = v.bad || bad_sum;
         const float logs = __builtin_amdgcn_logf(r.s) * 0.693147180559945309f;
         if (threadIdx.x == 0)
-            write_row(p, row, v, r, mine, bad, logs);
+            write_row(p, row, r, mine, equal, v.inv, bad, logs);
         if constexpr (TOP)
             place(merged_n, [&](int at, uint64_t key) { write_alternative(p, row, at, key, r, v.inv, bad, logs); });
         return;
@@ -493,6 +493,14 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
             total = mine_part;
     }
     if constexpr (TOP) {
+        // every thread's keys, on their way while the floor is found
+        constexpr int kMost = kMostSegments * SSU_TOP_MAX / kLogprobThreads;
+        uint64_t keys[kMost];
+#pragma unroll
+        for (int i = 0; i < kMost; i++) {
+            const int at = i * kLogprobThreads + threadIdx.x;
+            keys[i] = at < sp.segments * p.top ? get(sp.keys + base * p.top + at) : 0;
+        }
         // a segment whose first key is not among the `top` first keys has no alternative, so
         // at most top * top keys are left (with fewer segments than that: all of theirs)
         if (wave == 1) {
@@ -508,18 +516,17 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
                 floor = here ? head : 0;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < sp.segments * p.top; i += kLogprobThreads) {
-            const uint64_t key = get(sp.keys + base * p.top + i);
-            if (key != 0 && key >= floor)
-                merged[atomicAdd(&merged_n, 1)] = key;
-        }
+#pragma unroll
+        for (int i = 0; i < kMost; i++)
+            if (keys[i] != 0 && keys[i] >= floor)
+                merged[atomicAdd(&merged_n, 1)] = keys[i];
     }
     __syncthreads();
     r = total;
     const bool bad = v.bad || r.s != r.s;
     const float logs = __builtin_amdgcn_logf(r.s) * 0.693147180559945309f;
     if (threadIdx.x == 0)
-        write_row(p, row, v, r, mine, bad, logs);
+        write_row(p, row, r, mine, equal, v.inv, bad, logs);
     if constexpr (TOP)
         place(merged_n, [&](int at, uint64_t key) { write_alternative(p, row, at, key, r, v.inv, bad, logs); });
 }
