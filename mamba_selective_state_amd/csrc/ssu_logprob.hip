@@ -145,53 +145,109 @@ __device__ __forceinline__ void write_alternative(const LogprobParams &p, int64_
 
 // The first tokens of what a wave has seen, in order, one per lane: lane i holds the i-th
 // (lanes from `top` on hold what was pushed out). A logit enters only if it stands before the
-// `top`-th, so after the first few accesses hardly any does.
+// `top`-th, so after the first access hardly any does.
 struct Candidates {
-    uint32_t word, index;              // this lane's token: order_word of its logit (0: none), index
-    uint32_t floor_word, floor_index;  // the top-th token, or a bound that it is not behind; uniform
-    float gate;                        // logits below it do not enter
+    uint64_t key;    // this lane's token; 0: none
+    uint64_t floor;  // keys above it enter: the top-th token's, or a bound below it; uniform
+    float gate;      // logits below it do not enter
 
-    __device__ __forceinline__ void insert(uint32_t w, uint32_t i, int top, int lane) {
-        const uint64_t behind = __ballot(w > word || (w == word && i < index));
+    // After `key` has changed.
+    __device__ __forceinline__ void raise(int top) {
+        const uint64_t k = (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(key >> 32), top - 1)) << 32) |
+                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(key), top - 1));
+        if (k != 0) {
+            floor = k;
+            // an equal logit at a lower index of the same access may still enter
+            gate = fmaxf(gate, key_value(k));
+        }
+    }
+    __device__ __forceinline__ void insert(uint64_t k, int top, int lane) {
+        const uint64_t behind = __ballot(k > key);
         if (behind == 0)
             return;
         const int at = __builtin_ctzll(behind);  // lanes are in order: all from here on move up
-        const uint32_t pw = __builtin_amdgcn_update_dpp(0, static_cast<int>(word), 0x138, 0xF, 0xF, false);   // wave_shr:1
-        const uint32_t pi = __builtin_amdgcn_update_dpp(0, static_cast<int>(index), 0x138, 0xF, 0xF, false);
-        word = lane > at ? pw : lane == at ? w : word;
-        index = lane > at ? pi : lane == at ? i : index;
-        const uint32_t fw = __builtin_amdgcn_readlane(word, top - 1);
-        if (fw != 0) {
-            floor_word = fw;
-            floor_index = __builtin_amdgcn_readlane(index, top - 1);
-            // an equal logit at a lower index of the same access may still enter
-            gate = fmaxf(gate, word_value(fw));
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(key >> 32), 0x138, 0xF, 0xF, false);  // wave_shr:1
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(key), 0x138, 0xF, 0xF, false);
+        const uint64_t left = (static_cast<uint64_t>(hi) << 32) | lo;
+        key = lane > at ? left : lane == at ? k : key;
+        raise(top);
+    }
+    // The first access's logits, while nothing has entered: those at or above the gate are put in
+    // order together, through `list` (kList keys of LDS). False, and nothing done, where they are
+    // too many.
+    static constexpr int kList = 256;
+    __device__ __forceinline__ bool first(const float x[kVec], uint32_t at, int top, int lane, uint64_t *list) {
+        constexpr int kMost = kList / 2;
+        int n = 0;
+        uint64_t pass[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; i++) {
+            pass[i] = __ballot(x[i] >= gate && x[i] < __builtin_inff());
+            n += __popcll(pass[i]);
         }
+        if (n > kMost)
+            return false;
+        int to = 0;
+#pragma unroll
+        for (int i = 0; i < kVec; i++) {
+            const int mine = to + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(pass[i] >> 32),
+                                                            __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(pass[i]), 0));
+            if ((pass[i] >> lane) & 1)
+                list[mine] = order_key(order_word(x[i]), at + i);
+            to += __popcll(pass[i]);
+        }
+        // up to the next multiple of eight, keys that stand behind all
+        if (lane < 8 && n + lane < kMost)
+            list[n + lane] = 0;
+        list[kMost + lane] = 0;
+        __builtin_amdgcn_wave_barrier();
+        const uint64_t a = list[lane], b = list[64 + lane];
+        int ra = 0, rb = 0;
+        for (int j = 0; j < n; j += 8)
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                const uint64_t o = list[j + q];
+                ra += o > a;
+                rb += o > b;
+            }
+        __builtin_amdgcn_wave_barrier();
+        if (lane < n && ra < kWaveLanes)
+            list[kMost + ra] = a;
+        if (64 + lane < n && rb < kWaveLanes)
+            list[kMost + rb] = b;
+        __builtin_amdgcn_wave_barrier();
+        key = list[kMost + lane];
+        raise(top);
+        return true;
     }
     // An access's logits (destroyed), the lane's first index `at`: the lanes' largest ones are
     // offered and taken out until none is left that could enter.
     __device__ __forceinline__ void offer(float x[kVec], uint32_t at, int top, int lane) {
         while (true) {
-            float best = x[0];
+            float best = x[0], second = -__builtin_inff();
             uint32_t i = 0;
 #pragma unroll
             for (int j = 1; j < kVec; j++) {
                 const bool larger = x[j] > best;
+                second = fmaxf(second, larger ? best : x[j]);
                 best = larger ? x[j] : best;
                 i = larger ? j : i;
             }
-            const uint32_t w = order_word(best);
-            auto before_floor = [&] { return w > floor_word || (w == floor_word && at + i < floor_index); };
-            const bool pass = best >= gate && best < __builtin_inff() && before_floor();
+            const uint64_t k = order_key(order_word(best), at + i);
+            const bool pass = best >= gate && best < __builtin_inff() && k > floor;
             uint64_t todo = __ballot(pass);
             if (todo == 0)
                 return;
             while (todo) {
                 const int from = __builtin_ctzll(todo);
-                insert(__builtin_amdgcn_readlane(w, from), __builtin_amdgcn_readlane(at + i, from), top, lane);
+                insert((static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(k >> 32), from)) << 32) |
+                           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(k), from)),
+                       top, lane);
                 todo &= todo - 1;
-                todo &= __ballot(before_floor());
+                todo &= __ballot(k > floor);
             }
+            if (__ballot(second >= gate) == 0)
+                return;
 #pragma unroll
             for (int j = 0; j < kVec; j++)
                 x[j] = pass && i == static_cast<uint32_t>(j) ? -__builtin_inff() : x[j];
@@ -209,7 +265,7 @@ struct Candidates {
                 b = t;
         }
         if (b > 0x007FFFFFu) {  // above -inf's word
-            floor_word = b;     // with the index that stands behind every other
+            floor = static_cast<uint64_t>(b) << 32;  // behind every key of that value
             gate = word_value(b);
         }
     }
@@ -226,7 +282,7 @@ struct Split {
 constexpr int kMostSegments = 64;
 // Rows below which a row is split: enough workgroups for two on every compute unit.
 constexpr int kSplitBelow = 512;
-constexpr int kMergeCand = SSU_TOP_MAX * SSU_TOP_MAX;  // keys that a join of segments looks at, at most
+constexpr int kMergeCand = kMostSegments * SSU_TOP_MAX;  // keys of a row's segments, at most
 
 template <typename T, bool MASK, bool TOP>
 __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const LogprobParams p, const Split sp) {
@@ -250,7 +306,8 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
     typedef T Raw __attribute__((ext_vector_type(kVec), aligned(sizeof(T))));
     Sums w = {kLowest, 0.0f, 0.0f, 0};
     float limit = kLowest;
-    Candidates c = {0, 0, 0, 0xFFFFFFFFu, kLowest};
+    Candidates c = {0, 0, kLowest};
+    int done = -1;  // the access whose logits have been offered before the scan
 
     // whole tile `t`: its logits, and which of them the mask allows
     auto fetch = [&](int t, Raw *raw, uint32_t *bits) {
@@ -346,21 +403,21 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
         w.t += q;
         w.before += before;
         if constexpr (TOP) {
-            if (__ballot(top >= c.gate)) {
+            if (t != done && __ballot(top >= c.gate)) {
                 c.offer(x, at, p.top, lane);
-                if (c.floor_word != 0) {
-                    const float floor = word_value(c.floor_word);
+                const uint32_t word = static_cast<uint32_t>(c.floor >> 32);
+                if (word != 0) {
+                    const float value = word_value(word);
                     if (lane == 0)
-                        __hip_atomic_store(&floors[wave], floor, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                        __hip_atomic_store(&floors[wave], value, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
                     // accesses come in the order of their indices: what only equals a token of
-                    // this wave stays behind it from here on
-                    if (c.floor_index != 0xFFFFFFFFu)
-                        c.gate = fmaxf(c.gate, next_above(floor));
+                    // this wave stays behind it from here on (a bound's key has no index)
+                    if (static_cast<uint32_t>(c.floor) != 0)
+                        c.gate = fmaxf(c.gate, next_above(value));
                 }
             }
         }
     };
-
     // the other waves' floors hold for this one too
     auto read_floors = [&] {
         if constexpr (TOP) {
@@ -380,6 +437,13 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
             best = fmaxf(best, largest(x));
         }
         c.bound(best, p.top);
+        float x[kVec];
+        values(raw[0], bits[0], std::false_type(), x);
+        if (c.first(x, t * kTile + lane * kVec, p.top, lane, merged + wave * Candidates::kList)) {
+            done = t;
+            if (c.floor != 0 && lane == 0)
+                __hip_atomic_store(&floors[wave], word_value(static_cast<uint32_t>(c.floor >> 32)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
     }
     while (round) {
         read_floors();
@@ -433,8 +497,8 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
             out(i, static_cast<uint64_t>(0));
     };
     if constexpr (TOP) {
-        if (lane < p.top && c.word != 0)
-            merged[atomicAdd(&merged_n, 1)] = order_key(c.word, c.index);
+        if (lane < p.top && c.key != 0)
+            merged[atomicAdd(&merged_n, 1)] = c.key;
         __syncthreads();
     }
     const bool bad_sum = r.s != r.s;
@@ -501,19 +565,18 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
             const int at = i * kLogprobThreads + threadIdx.x;
             keys[i] = at < sp.segments * p.top ? get(sp.keys + base * p.top + at) : 0;
         }
-        // a segment whose first key is not among the `top` first keys has no alternative, so
-        // at most top * top keys are left (with fewer segments than that: all of theirs)
+        // the top-th of 64 of them, each segment's first ones, is behind no alternative
         if (wave == 1) {
-            const uint64_t head = lane < sp.segments ? get(sp.keys + (base + lane) * p.top) : 0;
+            const int each = min(p.top, kWaveLanes / sp.segments);
+            const uint64_t k = lane < each * sp.segments ? get(sp.keys + (base + lane / each) * p.top + lane % each) : 0;
             int at = 0;
-            for (int j = 0; j < sp.segments; j++) {
-                const uint64_t o = (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(head >> 32), j)) << 32) |
-                                   static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(head), j));
-                at += o > head || (o == head && j < lane);
+            for (int j = 0; j < kWaveLanes; j++) {
+                const uint64_t o = (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(k >> 32), j)) << 32) |
+                                   static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(k), j));
+                at += o > k || (o == k && j < lane);
             }
-            const uint64_t here = __ballot(at == p.top - 1 && lane < sp.segments);
-            if (lane == (here ? __builtin_ctzll(here) : 0))
-                floor = here ? head : 0;
+            if (at == p.top - 1)
+                floor = k;  // 0 where there are fewer
         }
         __syncthreads();
 #pragma unroll
