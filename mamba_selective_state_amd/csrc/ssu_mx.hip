@@ -493,7 +493,7 @@ __device__ __forceinline__ void finish_tile(const MxParams &p, f32x16 (&acc)[FM]
                 if (m + k * kRows < p.m) {
                     OT *at = dst + k * kRows * p.out_s;
                     if (n + kVec <= p.n)
-                        *reinterpret_cast<VecU *>(at) = v;
+                        __builtin_nontemporal_store(static_cast<VecU>(v), reinterpret_cast<VecU *>(at));
                     else
 #pragma unroll
                         for (int e = 0; e < kVec - 1; e++)
