@@ -197,6 +197,25 @@ def test_strides(m):
         assert (out[:, :3] == 5).all() and (out[:, n + 3:] == 5).all()
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("m,n,k", [(4347, 4001, 96), (4001, 4347, 608), (4354, 3841, 64)])
+def test_last_round_of_tiles(m, n, k, fmt):
+    """A few tiles more than whole rounds of them, below and on the right: float activations that
+    are codes again, a bias in the outputs' type, strided outputs between guards."""
+    g = torch.Generator().manual_seed(m + n + k)
+    a, sa = acts(m, k, fmt, g)
+    x = R.decode(a, sa, fmt).float()
+    w, sw = weights(n, k, g)
+    bias = torch.randint(-8, 9, (n,), generator=g).float()
+    ref = R.decode(a, sa, fmt).cuda() @ R.decode(w, sw, "mxfp4").cuda().t() + bias.double().cuda()
+    say("[gpu] mx_linear, last round", fmt, m, n, k)
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.full((m, n + 5), 5.0, dtype=dt, device="cuda")
+        ssu.mx_linear(x.cuda(), w.cuda(), sw.cuda(), bias=bias.cuda().to(dt), activation=fmt, out=out[:, 2:n + 2])
+        assert torch.equal(out[:, 2:n + 2], ref.float().to(dt)), dt
+        assert (out[:, :2] == 5).all() and (out[:, n + 2:] == 5).all()
+
+
 def test_leading_dimensions_and_empty():
     g = torch.Generator().manual_seed(0)
     w, sw = (t.cuda() for t in weights(64, 128, g))
