@@ -29,15 +29,7 @@ __device__ __forceinline__ void store8(T *dst, const float v[8]) {
     *reinterpret_cast<Vec *>(dst) = r;
 }
 
-// The first `n` (up to 8) of them, zeros after.
-template <typename T>
-__device__ __forceinline__ void load8(const T *src, int n, float v[8]) {
-    if (n >= 8)
-        return load8(src, v);
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-        v[i] = i < n ? widen(src[i]) : 0.0f;
-}
+// The first `n` (up to 8) of them.
 template <typename T>
 __device__ __forceinline__ void store8(T *dst, int n, const float v[8]) {
     if (n >= 8)
@@ -46,6 +38,14 @@ __device__ __forceinline__ void store8(T *dst, int n, const float v[8]) {
     for (int i = 0; i < 8; i++)
         if (i < n)
             dst[i] = narrow<T>(v[i]);
+}
+
+// Between a wave's LDS writes and its other lanes' reads of them (or the reverse): the hardware keeps
+// a wave's LDS accesses in order, and the fences make the compiler do so across lanes.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Sum over the wave, the same in every lane; all lanes must be active.

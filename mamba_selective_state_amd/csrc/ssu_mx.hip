@@ -161,9 +161,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void mx_stream_kernel(const MxPa
                 if (l % 4 == 0)
                     qscales[wave][m][l / 4] = static_cast<uint8_t>(sc);
             }
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            wave_lds_fence();
         }
         const int m = min(r, p.m - 1);
         const uint8_t *a = kFuse ? nullptr : p.a + m * p.a_s;
@@ -196,8 +194,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void mx_stream_kernel(const MxPa
                                                                    FORMAT == SSU_FORMAT_MXFP8 ? kE4M3 : kE2M1, 0, wsv[s], 0, as);
         }
         if constexpr (kFuse) {
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            wave_lds_fence();
         }
     }
     sums[wave][l] = acc;
@@ -481,9 +478,7 @@ __device__ __forceinline__ void finish_tile(const MxParams &p, f32x16 (&acc)[FM]
                         v[e] = narrow<OT>(sum[e]);
                     *reinterpret_cast<Vec4 *>(slab + r * kRow + j * 32 + 8 * q + 4 * h) = v;
                 }
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            wave_lds_fence();
             const int m = m0 + (wm * FM + i) * 32 + l / kLanes;
             const OT *src = slab + l / kLanes * kRow + l % kLanes * kVec;
             OT *dst = static_cast<OT *>(p.out) + m * p.out_s + n;
@@ -501,9 +496,7 @@ __device__ __forceinline__ void finish_tile(const MxParams &p, f32x16 (&acc)[FM]
                                 at[e] = v[e];
                 }
             }
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            wave_lds_fence();
         });
     }
 }
@@ -657,6 +650,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_ring_kernel(const TilePa
     constexpr int kRuns = kRoundK / 512, kScaleRow = 16 * kRuns;
     constexpr int kScaleKiB = (TM + TN) * kScaleRow / 1024;
     constexpr int kScaleLoads = kScaleKiB > kWaves ? kScaleKiB / kWaves : 1;
+    static_assert(kRuns <= 2, "one bit of the row permutes them");
     static_assert(kScaleKiB % kWaves == 0 || kWaves % kScaleKiB == 0, "every wave fetches as many");
     static_assert(SUB == 1 || kSteps == 1, "images of several K tiles are for one step per tile");
     // arrays of their own: the compiler tells fills of one from reads of another
@@ -688,7 +682,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_ring_kernel(const TilePa
         }
         in_order();
     };
-    auto permuted = [](int row, int run) { return kRuns == 4 ? run ^ ((row >> 2) & 3) : kRuns == 2 ? run ^ ((row >> 3) & 1) : run; };
+    auto permuted = [](int row, int run) { return kRuns == 2 ? run ^ ((row >> 3) & 1) : run; };
     const uint8_t *scale[kScaleLoads];
     int scale_at[kScaleLoads];
 #pragma unroll
@@ -897,7 +891,7 @@ struct TileShape {
     int tm, tn;
 };
 constexpr TileShape kTileShapes[5] = {{256, 256}, {128, 128}, {64, 64}, {64, 64}, {128, 128}};
-constexpr int kTailShape = 4;
+constexpr int kDeepShape = 3, kTailShape = 4;
 constexpr int kTileThreads = 256;
 
 template <typename OT, int FORMAT>
@@ -909,17 +903,26 @@ const void *tile_fn(int shape) {
     case 2: return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 1>);
     case kTailShape: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 128, 128, 2, 2, 1>);
     }
-    return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 2>);
+    if constexpr (FORMAT == SSU_FORMAT_MXFP8)  // kDeepShape
+        return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 2>);
+    return nullptr;
 }
 
-// The largest tile that leaves every compute unit one; of the smallest, the form with images of
-// two K tiles if no unit gets a second workgroup, else the one with images of one, of which two
-// workgroups fit a unit.
-int tile_shape(int64_t m, int64_t n) {
-    for (int s = 0; s < 3; s++)
-        if (((m + kTileShapes[s].tm - 1) / kTileShapes[s].tm) * ((n + kTileShapes[s].tn - 1) / kTileShapes[s].tn) >= (s < 2 ? 256 : 257))
+// The largest tile of which there are more than 128: otherwise there are at most two of the next
+// smaller one for each compute unit, and they are done sooner. k 4096, in us:
+//   256 and 128: 2048 x 4096 (128 of the large) 42.4 and 38.0, 2048 x 5120 (160) 39.4 and 46.8,
+//     2048 x 8192 (256) 44.9 and 60.3; MXFP8 57.4 and 49.7, 55.7 and 64.9, 61.9 and 83.9
+//   128 and 64: 1024 x 2048 (128) 19.7 and 17.8, 1024 x 2560 (160) 19.6 and 22.9,
+//     1024 x 4096 (256) 21.0 and 27.7; MXFP8 25.2 and 24.0, 25.4 and 29.5, 26.5 and 38.8
+// Of the smallest, MXFP8 takes images of two K tiles if no unit gets a second workgroup: 64 x 2048
+// 14.1 instead of 15.1, but 64 x 16384 and twice the rows 25.5 instead of 20.4. MXFP4's K tiles are as
+// deep by themselves (11.4 with two of them, 10.8 without).
+int tile_shape(int64_t m, int64_t n, int format) {
+    const auto tiles = [&](int s) { return ((m + kTileShapes[s].tm - 1) / kTileShapes[s].tm) * ((n + kTileShapes[s].tn - 1) / kTileShapes[s].tn); };
+    for (int s = 0; s < 2; s++)
+        if (tiles(s) > 128)
             return s;
-    return 3;
+    return format == SSU_FORMAT_MXFP8 && tiles(2) <= 256 ? kDeepShape : 2;
 }
 
 // Where the large tiles end and a second launch of smaller ones takes over: large tiles that would be
@@ -933,6 +936,8 @@ struct Cut {
 constexpr int kTailMost = 96;
 Cut tail_cut(int64_t m, int64_t n) {
     const int64_t mt = (m + 255) / 256, nt = (n + 255) / 256, full = mt * nt / 256 * 256;
+    if (full == 0)
+        return {m, n};
     const int64_t rows = full / nt, cols = full / mt;  // whole rows, or columns, of tiles in the full rounds
     const int64_t below = (mt - rows) * nt, right = (nt - cols) * mt;
     if (std::min(below, right) > kTailMost)
@@ -978,7 +983,7 @@ int64_t mx_linear_workspace(int64_t m, int64_t n, int64_t k, int format, bool fl
     const int64_t codes = floats && m > kMxFuseRows ? code_bytes(m, k, format) : 0;
     if (m <= kMxRowsMax)
         return codes > 0 ? codes + m * (k / 32) : 0;
-    if (tile_shape(m, n) == 0)
+    if (tile_shape(m, n, format) == 0)
         return codes + 4 * (packed_room(m, ktiles_of(k, format)) + packed_room(n, ktiles_of(k, format)));
     return codes + (m + n) * padded_scales(k);
 }
@@ -1006,7 +1011,7 @@ int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *s
         return run(fn, (p.n + kStreamRows - 1) / kStreamRows, kStreamWaves * 64, args, stream);
     }
 
-    const int shape = tile_shape(p.m, p.n);
+    const int shape = tile_shape(p.m, p.n, format);
     TileParams t = {};
     t.ktiles = static_cast<int32_t>(shape == 0 ? ktiles_of(p.k, format) : padded_scales(p.k) * 32 / ktile_depth(format));
     t.a_scales = p.a_scale;
