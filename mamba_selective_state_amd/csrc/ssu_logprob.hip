@@ -200,7 +200,7 @@ struct Candidates {
         if (lane < 8 && n + lane < kMost)
             list[n + lane] = 0;
         list[kMost + lane] = 0;
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_fence();
         const uint64_t a = list[lane], b = list[64 + lane];
         int ra = 0, rb = 0;
         for (int j = 0; j < n; j += 8)
@@ -210,12 +210,12 @@ struct Candidates {
                 ra += o > a;
                 rb += o > b;
             }
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_fence();
         if (lane < n && ra < kWaveLanes)
             list[kMost + ra] = a;
         if (64 + lane < n && rb < kWaveLanes)
             list[kMost + rb] = b;
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_fence();
         key = list[kMost + lane];
         raise(top);
         return true;
@@ -280,8 +280,13 @@ struct Split {
 };
 
 constexpr int kMostSegments = 64;
-// Rows below which a row is split: enough workgroups for two on every compute unit.
-constexpr int kSplitBelow = 512;
+// Fewer rows than compute units are split, into two workgroups for each. f32, vocabulary 131072, no
+// alternatives and 20, in us: 1 row split 6.3 and 12.3, whole 16.5 and 42.7; 64 rows 10.0 and 23.8,
+// 17.5 and 45.5; 200 rows 22.0 and 42.9, 21.1 and 47.5; 400 rows 38.9 and 60.9, 32.8 and 57.5. One
+// workgroup for each instead of two: 64 rows 10.3 and 27.3, four 12.5 and 23.1.
+constexpr int kSplitBelow = 256, kSplitTo = 512;
+constexpr int kTicketBytes = 2048;  // of the workspace, at its start
+static_assert(4 * kSplitBelow <= kTicketBytes, "a ticket for each row that is split");
 constexpr int kMergeCand = kMostSegments * SSU_TOP_MAX;  // keys of a row's segments, at most
 
 template <typename T, bool MASK, bool TOP>
@@ -528,6 +533,7 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
     }
     if constexpr (TOP)
         place(merged_n, [&](int at, uint64_t key) { put(sp.keys + (base + segment) * p.top + at, key); });
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's stores are complete
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -605,7 +611,7 @@ const void *logprob_fn(bool mask, bool top) {
 // Segments of a row and tiles per segment.
 void split(int64_t rows, int64_t vocab, int32_t *segments, int32_t *per) {
     const int64_t tiles = (vocab + kTile - 1) / kTile;
-    int64_t s = rows < kSplitBelow ? (kSplitBelow + rows - 1) / rows : 1;
+    int64_t s = rows < kSplitBelow ? (kSplitTo + rows - 1) / rows : 1;
     // a segment has a tile for each wave
     s = std::min<int64_t>({s, kMostSegments, std::max<int64_t>(1, tiles / kLogprobWaves)});
     *per = static_cast<int32_t>(std::max<int64_t>(1, (tiles + s - 1) / s));
@@ -619,7 +625,7 @@ void split(int64_t rows, int64_t vocab, int32_t *segments, int32_t *per) {
 int64_t logprobs_workspace(int64_t rows, int64_t vocab, int64_t top) {
     int32_t s, per;
     split(rows, vocab, &s, &per);
-    return s == 1 ? 0 : 4 * kSplitBelow + rows * s * static_cast<int64_t>(sizeof(Sums) + 8 * top);
+    return s == 1 ? 0 : kTicketBytes + rows * s * static_cast<int64_t>(sizeof(Sums) + 8 * top);
 }
 
 int launch_logprobs(const LogprobParams &p, int dtype, void *stream) {
@@ -627,7 +633,7 @@ int launch_logprobs(const LogprobParams &p, int dtype, void *stream) {
     split(p.rows, p.vocab, &sp.segments, &sp.tiles);
     if (sp.segments > 1) {
         sp.tickets = reinterpret_cast<uint32_t *>(p.workspace);
-        sp.sums = reinterpret_cast<Sums *>(p.workspace + 4 * kSplitBelow);
+        sp.sums = reinterpret_cast<Sums *>(p.workspace + kTicketBytes);
         sp.keys = reinterpret_cast<uint64_t *>(sp.sums + p.rows * sp.segments);
     }
     if (p.rows * sp.segments > INT32_MAX)
