@@ -241,16 +241,20 @@ struct NormShape {
     int lanes, nv;  // nv 0: the long kernel
 };
 
-// Lanes per part. Many parts: the fewest lanes that keep a part in registers (no barrier
-// for up to 2048 elements). Few parts: the time of one part is the time of the call, so up to two
-// runs for each of 256 lanes, then as many lanes as a workgroup has.
+// Lanes per part. Many elements: the fewest lanes that keep a part in registers (no barrier
+// for up to 2048). Few: the time of one part is the time of the call, so one run per lane up to
+// 2048 elements, two for up to 4096, then as many lanes as a workgroup has. Kernel times in us, bf16
+// with a residual:
+//   256 x 2048: 64 lanes 4.27, 256 lanes 2.65; 1024 x 2048: 5.17, 4.04; 4096 x 2048: 10.8, 12.3
+//   256 x 8192: 256 lanes 5.16, 1024 lanes 4.33; 1024 x 8192: 10.8, 13.3
+//   65536 x 128: 16 lanes 13.0, 64 lanes 23.7; 65536 x 512: 64 lanes 40, 256 lanes 57
 NormShape shape_for(int64_t parts, int part) {
     if (part < 8)
         return {kWaveLanes, 0};
     const int runs = (part + 7) / 8;
     constexpr NormShape kShapes[] = {{16, 1},  {64, 1},  {64, 2},   {64, 4},   {256, 1},
                                      {256, 2}, {256, 4}, {1024, 1}, {1024, 2}, {1024, 4}};
-    const bool many = parts >= 1024;
+    const bool many = parts * part >= (1 << 22);
     for (const NormShape &s : kShapes)
         if (runs <= s.lanes * s.nv && (many || s.nv == 1 || s.lanes * s.nv == 512 || s.lanes == 1024))
             return s;
