@@ -6,7 +6,13 @@
 //   log p[token] = (x_token - m) / temperature - log s,  entropy = log s - t ln 2 / s.
 // m is one value per wave, raised (and the sums scaled) only when a logit passes it by
 // more than 2^16 times in probability: any reference within that is as good as the
-// largest logit, and the common vector costs no rescaling.
+// largest logit, and the common vector costs no rescaling. All sums are f32, eight logits at a
+// time, then a lane's, a wave's, a workgroup's.
+//
+// The logits' bytes bound it: 2048 x 65536 bf16 (268 MB) take 46 us without alternatives (5.8 TB/s). With
+// them a wave looks at an access twice only if a logit reaches its gate; 1024 x 131072 bf16
+// with 8 take 64 us, with 20 84. A row is one workgroup's (four waves that take turns at
+// its accesses, four in flight each), or several workgroups' if there are few rows (see kSplitBelow).
 #include <algorithm>
 
 #include "ssu_layer_device.h"

@@ -93,7 +93,14 @@ __device__ __forceinline__ void store_out4(const MxParams &p, int m, int n, f32x
 // ---------------------------------------------------------------- few rows
 //
 // The weights' bytes bound it. A workgroup takes 16 outputs of up to 16 rows; its waves split
-// k and join their sums in LDS.
+// k and join their sums in LDS (by the waves' order, so that results repeat). 16 outputs, the
+// least of an instruction, give the most workgroups: 18560 x 4096 weights, one bf16 row quantised to
+// MXFP8 on the way, take 8.7 us (40.4 MB, 4.6 TB/s).
+//
+// kMxRowsMax: with 16 rows 18560 x 4096 MXFP8 takes 20.9 us here and 21.7 in the tiled kernels, with 32 34.6
+// and 23.4; 4096 x 8192 MXFP4 10.2 and 14.9, 13.4 and 15.8. 16 is also the instruction's other side.
+// kMxFuseRows: every workgroup quantises all rows for itself: 12.4 us with 4 rows, where a
+// launch of its own takes 15.8 for 5; the work grows with the rows, and the LDS for them.
 
 constexpr int kStreamWaves = 8;
 constexpr int kStreamRows = 16;  // weight rows per workgroup
@@ -501,6 +508,13 @@ __device__ __forceinline__ void finish_tile(const MxParams &p, f32x16 (&acc)[FM]
     }
 }
 
+// The matrix instructions bound it, and the 64 KB per K tile that come from the L2: 8192 x 18560 x 4096 MXFP4
+// runs at 3400 TF in all (366 us with the 20 of the quantisation), its loop at 4500 of the 6800 TF that registers alone
+// reach (5200 with zero codes, which draw less power). A tile's first fetches and its stores, 16 us a
+// round, are not covered by another workgroup: the sums take all accumulators of a compute unit, and four
+// images or more outputs per wave brought nothing. The stores of whole runs go past the
+// caches, which keep activations and weights (408 us without).
+//
 // TM x TN outputs per workgroup; the waves are WM x WN over the tile and WK over the
 // steps of a K tile (those join their sums in LDS at the end). Codes go straight
 // from memory to two LDS images: while one K tile is multiplied the next arrives. Each
@@ -631,6 +645,9 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
     finish_tile<OT, FM, FN, WM, WN, WK, kStage>(p, acc, lds0, lds1, m0, n0, l, wave);
 }
 
+// 256 x 4096 x 8192 MXFP4: 14.6 us (24 MB at 1.6 TB/s from HBM, but every workgroup reads
+// 0.8 MB from the L2; its fetches' way, 32 K tiles one after another, bounds it).
+//
 // The smaller tiles: too little work per K tile to hide a fetch behind one of them, so four images
 // of SUB K tiles take turns. A wave waits for the fetches that the next products need and no
 // more: only fetches count in vmcnt here, every image issues the same number of them, and they

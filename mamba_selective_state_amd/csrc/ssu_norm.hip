@@ -1,7 +1,11 @@
 // Gated, residual-adding RMS norm (ssu_add_rms_norm): per part of a row,
 //   u = x * silu(gate) + residual,  y = u * rsqrt(mean u^2 + eps) * weight.
 // The bytes bound it: every input is read once, u stays in registers between the sum
-// and the outputs, and the MX codes are made where y is.
+// and the outputs, and the MX codes are made where y is. 16384 x 8192 bf16 with a gate, 8 groups, to MXFP8: 133 us
+// (675 MB, 5.1 TB/s, a plain copy's rate); with a residual instead, to bf16, 187 us (5.7 TB/s). 256 x 4096
+// with a residual to MXFP8: 4.5 us, most of it the way there and back of one access and a barrier.
+// u and the sum are f32; the residual is rounded to its type when it is stored, y is made of the
+// unrounded u.
 #include <algorithm>
 
 #include "ssu_layer_device.h"
