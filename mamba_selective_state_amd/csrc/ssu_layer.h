@@ -29,7 +29,7 @@ int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t 
 // Product with MXFP4 weights. Strides: codes and scales in bytes, out in
 // elements. Up to kMxRowsMax rows run in the streaming kernel, which reads
 // scales where they are (and quantises up to kMxFuseRows rows by itself); more rows run
-// in the tiled kernels, which take codes and scales packed in a workspace.
+// in the tiled kernels, whose quantised codes and laid out scales are in a workspace.
 constexpr int kMxRowsMax = 16;
 constexpr int kMxFuseRows = 4;
 struct MxParams {

@@ -515,18 +515,17 @@ __device__ __forceinline__ void finish_tile(const MxParams &p, f32x16 (&acc)[FM]
 // images or more outputs per wave brought nothing. The stores of whole runs go past the
 // caches, which keep activations and weights (408 us without).
 //
-// TM x TN outputs per workgroup; the waves are WM x WN over the tile and WK over the
-// steps of a K tile (those join their sums in LDS at the end). Codes go straight
+// TM x TN outputs per workgroup; the waves are WM x WN over the tile. Codes go straight
 // from memory to two LDS images: while one K tile is multiplied the next arrives. Each
 // step's operands are read during the step before, the next tile's first ones
 // during this one's last step, behind the only barrier of a tile; the image that
 // the tile leaves is filled from there on.
-template <typename OT, int FORMAT, int TM, int TN, int WM, int WN, int WK>
-__global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TileParams t) {
+template <typename OT, int FORMAT, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(const TileParams t) {
     using KT = KTile<FORMAT>;
-    constexpr int kWaves = WM * WN * WK;
+    constexpr int kWaves = WM * WN;
     constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
-    constexpr int kSteps = KT::kSteps / WK;  // of this wave per K tile
+    constexpr int kSteps = KT::kSteps;
     constexpr int kABytes = TM * KT::kARow, kStage = kABytes + TN * KT::kWRow;
     // two arrays, so that the compiler can tell a fill of one from a read of the other
     __shared__ alignas(16) uint8_t lds0[kStage];
@@ -534,7 +533,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
     const MxParams &p = t.p;
     const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int r = l % 32, h = l / 32;
-    const int wm = wave % WM, wn = wave / WM % WN, wk = wave / (WM * WN);
+    const int wm = wave % WM, wn = wave / WM;
     int mt, nt;
     tile_at(blockIdx.x, t.mtiles, t.ntiles, &mt, &nt);
     const int m0 = mt * TM, n0 = nt * TN;
@@ -561,9 +560,8 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
         std::conditional_t<FORMAT == SSU_FORMAT_MXFP8, i32x8, i32x4> a[FM];
         i32x4 w[FN];
     };
-    auto read = [&](const uint8_t *src, int j) {
+    auto read = [&](const uint8_t *src, int s) {
         Frags f;
-        const int s = wk + WK * j;
 #pragma unroll
         for (int i = 0; i < FM; i++) {
             const int row = (wm * FM + i) * 32 + r;
@@ -581,7 +579,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
     };
     f32x16 acc[FM][FN] = {};
     auto multiply = [&](const Frags &f, auto jc) {
-        constexpr int kByte = decltype(jc)::value * WK;
+        constexpr int kByte = decltype(jc)::value;
 #pragma unroll
         for (int i = 0; i < FM; i++)
 #pragma unroll
@@ -601,10 +599,10 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
         auto tile = [&](uint8_t *here, uint8_t *there, int kt) {
 #pragma unroll
             for (int i = 0; i < FM; i++)
-                asc[i] = WK > 1 ? asc_next[i] >> (8 * wk) : asc_next[i];
+                asc[i] = asc_next[i];
 #pragma unroll
             for (int i = 0; i < FN; i++)
-                wsc[i] = WK > 1 ? wsc_next[i] >> (8 * wk) : wsc_next[i];
+                wsc[i] = wsc_next[i];
             load_scales(min(kt + 1, t.ktiles - 1));
             for_passes<0, kSteps>([&](auto jc) {
                 constexpr int j = decltype(jc)::value;
@@ -642,7 +640,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void mx_tile_kernel(const TilePa
         fills_barrier();
     }
 
-    finish_tile<OT, FM, FN, WM, WN, WK, kStage>(p, acc, lds0, lds1, m0, n0, l, wave);
+    finish_tile<OT, FM, FN, WM, WN, 1, kStage>(p, acc, lds0, lds1, m0, n0, l, wave);
 }
 
 // 256 x 4096 x 8192 MXFP4: 14.6 us (24 MB at 1.6 TB/s from HBM, but every workgroup reads
@@ -915,10 +913,10 @@ template <typename OT, int FORMAT>
 const void *tile_fn(int shape) {
     constexpr int kWk = KTile<FORMAT>::kSteps;
     switch (shape) {
-    case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 256, 256, 2, 2, 1>);
+    case 0: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 256, 256, 2, 2>);
     case 1: return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 128, 128, 2, 2, 1, 1>);
     case 2: return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 1>);
-    case kTailShape: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 128, 128, 2, 2, 1>);
+    case kTailShape: return reinterpret_cast<const void *>(&mx_tile_kernel<OT, FORMAT, 128, 128, 2, 2>);
     }
     if constexpr (FORMAT == SSU_FORMAT_MXFP8)  // kDeepShape
         return reinterpret_cast<const void *>(&mx_ring_kernel<OT, FORMAT, 64, 64, 1, 4 / kWk, kWk, 2>);
