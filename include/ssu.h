@@ -549,10 +549,12 @@ SSU_API ssu_status_t ssu_mx_linear(const ssu_mx_linear_args_t *args, void *works
  *   top_tokens i32, top_logprobs f32 [rows, top], contiguous, top <=
  *                SSU_TOP_MAX; both or neither
  * `workspace`: DEVICE memory of at least ssu_token_logprobs_workspace_bytes, 256-
- * byte aligned (NULL where that is 0), whose first 2048 bytes are zero before its first use and
- * which nothing else writes between calls (a call leaves them zero); two calls
- * that overlap must not share one. */
+ * byte aligned (NULL where that is 0), whose first SSU_LOGPROB_ZEROED_BYTES are zero before its
+ * first use and which nothing else writes between calls (a call leaves them zero); two calls
+ * that overlap must not share one. A captured graph needs one that is its own, stays
+ * allocated as long as it, and was zeroed before its first replay. */
 #define SSU_TOP_MAX 32
+#define SSU_LOGPROB_ZEROED_BYTES 2048
 typedef struct {
     ssu_tensor_t logits, tokens, mask, temperature;
     ssu_tensor_t logprob, entropy, rank, top_tokens, top_logprobs;

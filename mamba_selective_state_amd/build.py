@@ -42,12 +42,14 @@ def torch_command(obj):
     """g++ command that compiles TORCH_SRC to `obj`, and the libraries to link it with."""
     import torch
     root = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     inc = [os.path.join(root, "include"),
            os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"]]
-    flags = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
+           sysconfig.get_paths()["include"], os.path.join(rocm, "include")]
+    flags = ["-O2", "-D__HIP_PLATFORM_AMD__", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
              "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
-    libs = ["-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+    libs = ["-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+            "-L" + os.path.join(rocm, "lib"), "-lamdhip64"]
     return ["g++", *flags, *["-I" + i for i in inc], "-c", "-o", obj, TORCH_SRC], libs
 
 

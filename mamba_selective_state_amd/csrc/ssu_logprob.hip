@@ -291,7 +291,7 @@ constexpr int kMostSegments = 64;
 // 17.5 and 45.5; 200 rows 22.0 and 42.9, 21.1 and 47.5; 400 rows 38.9 and 60.9, 32.8 and 57.5. One
 // workgroup for each instead of two: 64 rows 10.3 and 27.3, four 12.5 and 23.1.
 constexpr int kSplitBelow = 256, kSplitTo = 512;
-constexpr int kTicketBytes = 2048;  // of the workspace, at its start
+constexpr int kTicketBytes = SSU_LOGPROB_ZEROED_BYTES;  // of the workspace, at its start
 static_assert(4 * kSplitBelow <= kTicketBytes, "a ticket for each row that is split");
 constexpr int kMergeCand = kMostSegments * SSU_TOP_MAX;  // keys of a row's segments, at most
 

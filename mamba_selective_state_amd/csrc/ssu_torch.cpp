@@ -8,6 +8,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
+#include <hip/hip_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
@@ -118,12 +119,25 @@ at::Tensor make(const at::Tensor &like, at::IntArrayRef shape, at::ScalarType dt
     return at::empty(shape, like.options().dtype(dtype));
 }
 
-// The cached workspace of an operator on a device's stream, grown to at least `bytes`.
-// One per stream: calls on one stream are ordered, so they can share it; it is
-// allocated on that stream, so the caching allocator hands a grown one's
-// predecessor out again only behind the kernels that used it.
+// Whether what is enqueued on the stream now goes into a graph.
+bool capturing(uintptr_t stream) {
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(reinterpret_cast<hipStream_t>(stream), &status) != hipSuccess)
+        (void)hipGetLastError();  // the launch reports what is wrong with the stream
+    return status != hipStreamCaptureStatusNone;
+}
+
+// Scratch memory of one call, from torch's allocator and on the call's stream: given back when the call
+// has been enqueued, it is handed out again only behind the call's kernels. While a graph is
+// captured it is the graph's own memory, which stays with the graph.
+at::Tensor scratch(const at::Tensor &like, int64_t bytes) {
+    return bytes > 0 ? at::empty({bytes}, like.options().dtype(at::kByte)) : at::Tensor();
+}
+
+// The workspaces of token_logprobs, whose first bytes are zero between calls: one per device and
+// stream, on which calls are ordered, grown to what a call needs. No graph uses them: a graph would
+// go on writing to one that has been replaced, or while another graph that was captured on the same stream runs.
 struct Workspace {
-    int op;
     int8_t device;
     uintptr_t stream;
     at::Tensor memory;
@@ -131,24 +145,25 @@ struct Workspace {
 // never destroyed: the interpreter may end after torch's allocator
 std::vector<Workspace> &workspaces = *new std::vector<Workspace>();
 
-void *workspace(int op, const at::Tensor &like, uintptr_t stream, int64_t bytes, bool zeroed, int64_t *have) {
-    *have = 0;
+at::Tensor logprob_workspace(const at::Tensor &like, uintptr_t stream, int64_t bytes) {
     if (bytes == 0)
-        return nullptr;
+        return at::Tensor();
+    if (capturing(stream)) {  // the call's own, zeroed by every replay
+        at::Tensor own = scratch(like, bytes);
+        own.narrow(0, 0, SSU_LOGPROB_ZEROED_BYTES).zero_();
+        return own;
+    }
     Workspace *w = nullptr;
     for (Workspace &c : workspaces)
-        if (c.op == op && c.device == like.get_device() && c.stream == stream)
+        if (c.device == like.get_device() && c.stream == stream)
             w = &c;
     if (!w) {
-        workspaces.push_back({op, static_cast<int8_t>(like.get_device()), stream, at::Tensor()});
+        workspaces.push_back({static_cast<int8_t>(like.get_device()), stream, at::Tensor()});
         w = &workspaces.back();
     }
-    if (!w->memory.defined() || w->memory.numel() < bytes) {
-        const auto options = like.options().dtype(at::kByte);
-        w->memory = zeroed ? at::zeros({bytes}, options) : at::empty({bytes}, options);
-    }
-    *have = w->memory.numel();
-    return w->memory.data_ptr();
+    if (!w->memory.defined() || w->memory.numel() < bytes)
+        w->memory = at::zeros({bytes}, like.options().dtype(at::kByte));
+    return w->memory;
 }
 
 int64_t as_int(PyObject *o) {
@@ -266,9 +281,10 @@ PyObject *mx_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         describe_rows(*out, dev, "out", &args.out);
         const uintptr_t stream = as_stream(a[8]);
-        int64_t have;
-        void *ws_ptr = workspace(0, x, stream, ssu_mx_linear_workspace_bytes(&args), false, &have);
-        check(ssu_mx_linear(&args, ws_ptr, have, reinterpret_cast<void *>(stream)), "ssu_mx_linear");
+        const at::Tensor ws_mem = scratch(x, ssu_mx_linear_workspace_bytes(&args));
+        check(ssu_mx_linear(&args, ws_mem.defined() ? ws_mem.data_ptr() : nullptr, ws_mem.defined() ? ws_mem.numel() : 0,
+                            reinterpret_cast<void *>(stream)),
+              "ssu_mx_linear");
         return given(a[6], made);
     });
 }
@@ -302,10 +318,10 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n) {
         for (int i = 0; i < (top ? 5 : 3); i++)
             describe(made[i], dev, at[i]);
         const uintptr_t stream = as_stream(a[5]);
-        int64_t have;
-        // its tickets start at zero and every call leaves them there
-        void *ws = workspace(1, logits, stream, ssu_token_logprobs_workspace_bytes(&args), true, &have);
-        check(ssu_token_logprobs(&args, ws, have, reinterpret_cast<void *>(stream)), "ssu_token_logprobs");
+        const at::Tensor ws = logprob_workspace(logits, stream, ssu_token_logprobs_workspace_bytes(&args));
+        check(ssu_token_logprobs(&args, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0,
+                                 reinterpret_cast<void *>(stream)),
+              "ssu_token_logprobs");
         PyObject *r = PyTuple_New(5);
         if (!r)
             throw PythonError();
