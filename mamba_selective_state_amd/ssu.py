@@ -609,7 +609,13 @@ def ssd_workspace(device, stream, nbytes):
     `nbytes` (a call of an already seen size allocates nothing). One per
     stream: calls on one stream are ordered, so they can share it; a grown
     workspace is allocated on that stream, so the caching allocator hands
-    the old one's memory out again only behind the kernels that used it."""
+    the old one's memory out again only behind the kernels that used it.
+    While a graph is captured the call gets one of its own, which stays with
+    the graph: a graph would go on writing to a workspace that has been
+    replaced, or share it with another graph that runs on another stream."""
+    with torch.cuda.device(device):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     key = (device, stream)
     ws = _ssd_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:

@@ -1,4 +1,4 @@
-"""Workspaces of mx_linear and token_logprobs: a captured graph owns what it writes to, whatever else is
+"""Workspaces of mx_linear, token_logprobs and ssd_combined_fwd_varlen: a captured graph owns what it writes to, whatever else is
 captured, called or allocated on its stream, and an eager call leaves nothing behind.
 
 Every answer is compared bit for bit with that of an eager call on the default stream: the
@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import mamba_selective_state_amd as ssu
+import workloads as W
 
 pytestmark = pytest.mark.gpu
 
@@ -58,7 +59,30 @@ class Logprobs:
         self.logits.copy_((3 * torch.randn(self.logits.shape, generator=torch.Generator().manual_seed(seed))).bfloat16())
 
 
-OPS = pytest.mark.parametrize("Op", [Linear, Logprobs])
+class Ssd:
+    """A prefill of three sequences: every chunk's state goes through the workspace."""
+
+    def __init__(self, seed, lengths=(300, 17, 129)):
+        c = W.ssd(seed=seed, lengths=lengths, heads=8, dim=64, dstate=128, groups=2, chunk_size=128, io="f32",
+                  state_dtype="f32")
+        self.t = {k: torch.from_numpy(c[k]).cuda() for k in ("x", "dt", "A", "B", "C", "D", "dt_bias")}
+        for k in ("x", "B", "C"):
+            self.t[k] = self.t[k].bfloat16()
+        self.t.update({k: torch.as_tensor(c[k]).cuda() for k in ("cu_seqlens", "cu_chunk_seqlens", "last_chunk_indices", "seq_idx")})
+        self.t.update(chunk_size=c["chunk_size"], dt_softplus=True, state_dtype=torch.float32)
+
+    def call(self):
+        y = torch.empty_like(self.t["x"])
+        return y, ssu.ssd_combined_fwd_varlen(out=y, **self.t)
+
+    def larger(self):
+        return Ssd(99, (3000, 500)).call()
+
+    def change(self, seed):
+        self.t["x"].copy_(torch.randn(self.t["x"].shape, generator=torch.Generator().manual_seed(seed)).bfloat16())
+
+
+OPS = pytest.mark.parametrize("Op", [Linear, Logprobs, Ssd])
 
 
 def expect(op):
