@@ -455,7 +455,11 @@ SSU_API ssu_status_t ssu_ssd_prefill_noalloc(const ssu_ssd_args_t *args, void *s
  * update -> gated RMS norm -> output projection, and its last layer's logits
  * become log probabilities of the drafted tokens. The entry points below
  * follow the conventions above: caller-owned device memory, no allocation,
- * asynchronous on `stream`, nothing device-resident read on the host. */
+ * asynchronous on `stream`, nothing device-resident read on the host.
+ * Widths and inner sizes, the product's rows and outputs and the vocabulary are at most 2^31 -
+ * 65537. A call is one launch of at most 2^32 - 1 work items, and one that needs more is refused: from
+ * 2^24 rows of logits on, 2^27 outputs of a product of up to 16 rows, 2^26 parts of fewer than eight
+ * elements of a norm, and at 2^31 elements of it or more in wider parts. */
 
 /* Number formats of an operator's 8- or 4-bit operand. MXFP8 and MXFP4 as
  * above (E4M3 / E2M1 elements, an E8M0 scale byte per 32 consecutive values

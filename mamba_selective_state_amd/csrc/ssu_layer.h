@@ -9,6 +9,9 @@
 
 namespace ssu {
 
+// What the launch functions return, besides HIP's codes: more work items than the 2^32 - 1 of one launch.
+constexpr int kTooManyWorkItems = -1;
+
 // RMS norm. Strides are in elements; a "part" is one group of one row.
 struct NormParams {
     const void *x, *weight, *residual, *gate;  // residual, gate may be null

@@ -22,10 +22,16 @@ ssu_status_t fail(ssu_status_t st, const char *fmt, ...) {
 }
 
 ssu_status_t done(int hip) {
+    if (hip == ssu::kTooManyWorkItems)
+        return fail(SSU_ERR_NOT_IMPLEMENTED, "more rows or outputs than one launch takes");
     if (hip != 0)
         return fail(SSU_ERR_HIP, "kernel launch failed: %s", ssu::hip_error_string(hip));
     return ssu::report_error(SSU_OK, "");
 }
+
+// Rows, columns and inner sizes. The kernels count in 32 bits within a row and round sizes up to
+// whole accesses, tiles and rounds of tiles, a few KiB at most.
+constexpr int64_t kMostSize = INT32_MAX - 65536;
 
 bool is_float(int d) { return d == SSU_F32 || d == SSU_F16 || d == SSU_BF16; }
 bool is_index(int d) { return d == SSU_I32 || d == SSU_I64; }
@@ -119,7 +125,7 @@ ssu_status_t ssu_add_rms_norm(const ssu_norm_args_t *a, void *stream) {
     if (!is_float(x.dtype))
         return fail(SSU_ERR_VALUE, "x must be f32, f16 or bf16");
     const int64_t rows = x.size[0], dim = x.size[1];
-    if (rows < 0 || dim < 0 || dim > INT32_MAX)
+    if (rows < 0 || dim < 0 || dim > kMostSize)
         return fail(SSU_ERR_VALUE, "x has a size out of range");
     ssu::NormParams p = {};
     if (ssu_status_t st = matrix("x", x, rows, dim, false, &p.x_s))
@@ -197,7 +203,7 @@ ssu_status_t ssu_mx_quantize(const ssu_tensor_t *src, const ssu_tensor_t *codes,
     const int64_t rows = src->size[0], k = src->size[1];
     if (k % 32 != 0)
         return fail(SSU_ERR_VALUE, "k must be a multiple of 32");
-    if (k > INT32_MAX)
+    if (k > kMostSize)
         return fail(SSU_ERR_NOT_IMPLEMENTED, "k too large");
     int64_t s;
     if (ssu_status_t st = matrix("src", *src, rows, k, false, &s))
@@ -225,7 +231,7 @@ ssu_status_t ssu_mx_linear(const ssu_mx_linear_args_t *a, void *workspace, int64
     if (!present(a->x) || a->x.ndim != 2 || !present(a->w) || a->w.ndim != 2 || !present(a->out) || a->out.ndim != 2)
         return fail(SSU_ERR_VALUE, "x, w and out must be 2-D");
     const int64_t m = a->x.size[0], n = a->w.size[0], k = a->w.size[1] * 2;
-    if (m < 0 || n < 0 || m > INT32_MAX || n > INT32_MAX || k > INT32_MAX)
+    if (m < 0 || n < 0 || m > kMostSize || n > kMostSize || k > kMostSize)
         return fail(SSU_ERR_VALUE, "x or w has a size out of range");
     if (k % 32 != 0)
         return fail(SSU_ERR_VALUE, "k must be a multiple of 32 (w is [n, k / 2] code pairs)");
@@ -289,7 +295,7 @@ ssu_status_t ssu_token_logprobs(const ssu_logprob_args_t *a, void *workspace, in
     if (!present(x) || x.ndim != 2 || !is_float(x.dtype))
         return fail(SSU_ERR_VALUE, "logits must be [rows, vocab], f32, f16 or bf16");
     const int64_t rows = x.size[0], vocab = x.size[1];
-    if (rows < 0 || vocab < 0 || rows > INT32_MAX || vocab > INT32_MAX - 65536)
+    if (rows < 0 || vocab < 0 || rows > INT32_MAX || vocab > kMostSize)
         return fail(SSU_ERR_VALUE, "logits has a size out of range");
     ssu::LogprobParams p = {};
     if (ssu_status_t st = matrix("logits", x, rows, vocab, false, &p.logits_s))

@@ -2,11 +2,20 @@
 // elements at a time, and eight fp32 values to their MX codes.
 #pragma once
 
+#include <hip/hip_runtime.h>
+
 #include "ssu_device.h"
 #include "ssu_layer.h"
 
 namespace ssu {
 namespace {
+
+inline int launch_groups(const void *fn, int64_t groups, int threads, void **args, void *stream) {
+    if (groups > static_cast<int64_t>(UINT32_MAX) / threads)
+        return kTooManyWorkItems;
+    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(groups)), dim3(static_cast<unsigned>(threads)), args, 0,
+                                            static_cast<hipStream_t>(stream)));
+}
 
 // Eight consecutive elements at any element-aligned address: gfx950's global
 // loads take unaligned addresses, so one 16-byte (f32: two) access serves

@@ -642,16 +642,13 @@ int launch_logprobs(const LogprobParams &p, int dtype, void *stream) {
         sp.sums = reinterpret_cast<Sums *>(p.workspace + kTicketBytes);
         sp.keys = reinterpret_cast<uint64_t *>(sp.sums + p.rows * sp.segments);
     }
-    if (p.rows * sp.segments > INT32_MAX)
-        return static_cast<int>(hipErrorInvalidValue);
     const bool mask = p.mask != nullptr, top = p.top > 0;
     const void *fn = dtype == SSU_F32   ? logprob_fn<float>(mask, top)
                      : dtype == SSU_F16 ? logprob_fn<_Float16>(mask, top)
                                         : logprob_fn<__bf16>(mask, top);
     LogprobParams pc = p;
     void *args[] = {&pc, &sp};
-    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(p.rows * sp.segments)), dim3(kLogprobThreads), args, 0,
-                                            static_cast<hipStream_t>(stream)));
+    return launch_groups(fn, p.rows * sp.segments, kLogprobThreads, args, stream);
 }
 
 }  // namespace ssu

@@ -973,13 +973,6 @@ const void *by_out(int out_dtype, F &&f) {
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 int64_t code_bytes(int64_t m, int64_t k, int format) { return round256(format == SSU_FORMAT_MXFP4 ? m * k / 2 : m * k); }
 
-int run(const void *fn, int64_t grid, int block, void **args, void *stream) {
-    if (grid > INT32_MAX)
-        return static_cast<int>(hipErrorInvalidValue);
-    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(block), args, 0,
-                                            static_cast<hipStream_t>(stream)));
-}
-
 }  // namespace
 
 int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t rows, int64_t k, uint8_t *codes,
@@ -991,7 +984,7 @@ int launch_mx_quantize_rows(const void *src, int dtype, int64_t stride, int64_t 
     blocks = blocks > 65536 ? 65536 : blocks;
     int32_t k32 = static_cast<int32_t>(k);
     void *args[] = {&src, &stride, &rows, &k32, &codes, &scales};
-    return run(fn, blocks, kQuantThreads, args, stream);
+    return launch_groups(fn, blocks, kQuantThreads, args, stream);
 }
 
 int64_t mx_linear_workspace(int64_t m, int64_t n, int64_t k, int format, bool floats) {
@@ -1023,7 +1016,7 @@ int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *s
             return mx4 ? stream_fn<OT, SSU_FORMAT_MXFP4>(fuse, p.x_dtype) : stream_fn<OT, SSU_FORMAT_MXFP8>(fuse, p.x_dtype);
         });
         void *args[] = {&p};
-        return run(fn, (p.n + kStreamRows - 1) / kStreamRows, kStreamWaves * 64, args, stream);
+        return launch_groups(fn, (p.n + kStreamRows - 1) / kStreamRows, kStreamWaves * 64, args, stream);
     }
 
     const int shape = tile_shape(p.m, p.n, format);
@@ -1071,7 +1064,7 @@ int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *s
                          : p.x_dtype == SSU_F16 ? pack_fn<_Float16>(format)
                                                 : pack_fn<__bf16>(format);
         void *args[] = {&q};
-        if (int e = run(fn, q.a_groups + groups(w_work), kQuantThreads, args, stream))
+        if (int e = launch_groups(fn, q.a_groups + groups(w_work), kQuantThreads, args, stream))
             return e;
     }
     t.p = p;
@@ -1083,7 +1076,7 @@ int launch_mx_linear(const MxParams &args_in, int format, int out_dtype, void *s
             return mx4 ? tile_fn<OT, SSU_FORMAT_MXFP4>(shape) : tile_fn<OT, SSU_FORMAT_MXFP8>(shape);
         });
         void *args[] = {&t};
-        return run(fn, static_cast<int64_t>(t.mtiles) * t.ntiles, kTileThreads, args, stream);
+        return launch_groups(fn, static_cast<int64_t>(t.mtiles) * t.ntiles, kTileThreads, args, stream);
     };
     if (shape != 0)
         return launch(shape);

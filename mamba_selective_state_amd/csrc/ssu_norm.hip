@@ -300,8 +300,7 @@ int launch_norm(const NormParams &p, int dtype, int format, void *stream) {
     const int per = s.nv && s.lanes < kNormThreads ? kNormThreads / s.lanes : 1;
     NormParams pc = p;
     void *args[] = {&pc};
-    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>((p.parts + per - 1) / per)), dim3(s.lanes * per), args,
-                                            0, static_cast<hipStream_t>(stream)));
+    return launch_groups(fn, (p.parts + per - 1) / per, s.lanes * per, args, stream);
 }
 
 }  // namespace ssu
