@@ -1,13 +1,14 @@
 // Log probabilities of given tokens with entropy, rank and the top
 // alternatives (ssu_token_logprobs), in one pass over the logits.
 //
-// With k = log2(e) / temperature and a reference m near the largest logit,
+// With k = log2(e) / temperature and the largest logit m,
 //   s = sum 2^((x - m) k),  t = sum 2^((x - m) k) (x - m) k   (over allowed tokens)
 //   log p[token] = (x_token - m) / temperature - log s,  entropy = log s - t ln 2 / s.
-// m is one value per wave, raised (and the sums scaled) only when a logit passes it by
-// more than 2^16 times in probability: any reference within that is as good as the
-// largest logit, and the common vector costs no rescaling. All sums are f32, eight logits at a
-// time, then a lane's, a wave's, a workgroup's.
+// m is one value per wave, raised (and the sums scaled) when a logit passes it: of n accesses in no
+// order about ln n do. The largest logit's own term is then 1 exactly. A reference further below costs
+// digits: with one up to 2^16 times in probability below, the log probability of a token that holds nearly
+// all was the difference of two numbers near 11, off by up to 2e-6 instead of 1e-7. All sums are
+// f32, eight logits at a time, then a lane's, a wave's, a workgroup's.
 //
 // The logits' bytes bound it: 2048 x 65536 bf16 (268 MB) take 46 us without alternatives (5.8 TB/s). With
 // them a wave looks at an access twice only if a logit reaches its gate; 1024 x 131072 bf16
@@ -49,11 +50,11 @@ __device__ __forceinline__ float next_below(float v) {
 }
 __device__ __forceinline__ float next_above(float v) { return -next_below(-v); }
 
+// Over the wave, the same in every lane; all lanes must be active.
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 1; d < kWaveLanes; d *= 2)
-        v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    const int m = __float_as_int(group_max<16>(v));
+    return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(m, 0)), __int_as_float(__builtin_amdgcn_readlane(m, 16))),
+                 fmaxf(__int_as_float(__builtin_amdgcn_readlane(m, 32)), __int_as_float(__builtin_amdgcn_readlane(m, 48))));
 }
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -316,7 +317,6 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
     const int first = segment * sp.tiles, end = min(tiles, first + sp.tiles);
     typedef T Raw __attribute__((ext_vector_type(kVec), aligned(sizeof(T))));
     Sums w = {kLowest, 0.0f, 0.0f, 0};
-    float limit = kLowest;
     Candidates c = {0, 0, kLowest};
     int done = -1;  // the access whose logits have been offered before the scan
 
@@ -389,13 +389,12 @@ __global__ __launch_bounds__(kLogprobThreads, 4) void logprob_kernel(const Logpr
         values(raw, bits, all, x);
         const int at = t * kTile + lane * kVec;
         const float top = largest(x);
-        if (__ballot(top > limit)) {
+        if (__ballot(top > w.m)) {
             const float m = fmaxf(w.m, wave_max(top));
             const float delta = (w.m - m) * v.k, f = __builtin_amdgcn_exp2f(delta);
             w.t = f > 0.0f ? f * (w.t + delta * w.s) : 0.0f * w.t;
             w.s *= f;
             w.m = m;
-            limit = m + 16.0f / v.k;
         }
         float low = mine_high;
         if (at + kVec <= token)
