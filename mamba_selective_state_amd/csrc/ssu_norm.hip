@@ -15,19 +15,43 @@ namespace {
 
 constexpr int kNormThreads = 256;
 
-// z * sigmoid(z) to within 2 ulps: the codes of an MX output go by y's last bits, and the plain
+constexpr float kLog2eHi = 1.44269504088896341f, kLog2eLo = 1.925963033500011e-8f, kLn2 = 0.693147180559945309f;
+
+// z * sigmoid(z) to within 2 ulps for z >= -87: the codes of an MX output go by y's last bits, and the plain
 // exp2(z log2 e) loses |z| / 2 of them. log2 e is taken in two parts, the reciprocal is
-// refined once. Below -87 the result is under 1e-36 and taken as at -87.
+// refined once. A NaN stays.
 __device__ __forceinline__ float silu_exact(float z) {
-    constexpr float kHi = 1.44269504088896341f, kLo = 1.925963033500011e-8f;
-    z = z < -87.0f ? -87.0f : z;  // a NaN stays
-    const float c = fminf(z, 87.0f);
-    const float hi = -c * kHi;
-    const float lo = fmaf(-c, kHi, -hi) - c * kLo;
+    const float c = __builtin_amdgcn_fmed3f(z, -87.0f, 87.0f);
+    const float hi = -c * kLog2eHi;
+    const float lo = fmaf(-c, kLog2eHi, -hi) - c * kLog2eLo;
     const float e = __builtin_amdgcn_exp2f(hi);
-    const float d = 1.0f + fmaf(e * lo, 0.693147180559945309f, e);
+    const float d = 1.0f + fmaf(e * lo, kLn2, e);
     const float r = __builtin_amdgcn_rcpf(d);
     return z * fmaf(fmaf(-d, r, 1.0f), r, r);
+}
+// The same below -87, where 1 + e^-z overflows: z e^z, with 2^96 in the exponential and out of z, so that
+// only the product leaves the range of normal numbers. -inf times 0 is a NaN, as in the formula.
+__device__ __forceinline__ float silu_far(float z) {
+#pragma clang fp contract(off)  // lo is what the rounded hi leaves: 96 must be added to that hi
+    const float c = fmaxf(z, -300.0f);
+    const float hi = c * kLog2eHi;
+    const float lo = fmaf(c, kLog2eHi, -hi) + c * kLog2eLo;
+    const float e = __builtin_amdgcn_exp2f(hi + 96.0f);
+    return z * 0x1p-96f * fmaf(e * lo, kLn2, e);
+}
+// v times silu(z), eight at a time: one look for all of them at whether a gate lies that far out.
+__device__ __forceinline__ void apply_gate(float v[8], const float z[8]) {
+    float least = z[0];
+#pragma unroll
+    for (int j = 1; j < 8; j++)
+        least = fminf(least, z[j]);
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        float s = silu_exact(z[j]);
+        if (least < -87.0f)
+            s = z[j] < -87.0f ? silu_far(z[j]) : s;
+        v[j] *= s;
+    }
 }
 
 // Eight elements of a row as loaded: all of them, or the first n and zeros after.
@@ -135,10 +159,13 @@ __global__ __launch_bounds__(LANES < kNormThreads ? kNormThreads : LANES) void n
 #pragma unroll
         for (int j = 0; j < 8; j++)
             u[v][j] = widen(x[v].v[j]);
-        if (p.gate)
+        if (p.gate) {
+            float gate[8];
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                u[v][j] *= silu_exact(widen(z[v].v[j]));
+                gate[j] = widen(z[v].v[j]);
+            apply_gate(u[v], gate);
+        }
         if (p.residual)
 #pragma unroll
             for (int j = 0; j < 8; j++)
@@ -196,9 +223,11 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const NormParam
             u[j] = widen(x.v[j]);
         if (p.gate) {
             x.load(static_cast<const T *>(p.gate) + row * p.gate_s + first + i, n);
+            float gate[8];
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                u[j] *= silu_exact(widen(x.v[j]));
+                gate[j] = widen(x.v[j]);
+            apply_gate(u, gate);
         }
         if (p.residual) {
             Raw8Or32<T> r;
