@@ -8,6 +8,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
+#include <c10/core/DeviceGuard.h>
 #include <hip/hip_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -215,6 +216,7 @@ PyObject *add_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int format = static_cast<int>(as_int(a[6]));
         const at::Tensor *out = tensor(a[7]), *scales = tensor(a[8]), *residual_out = tensor(a[9]);
         const at::Device dev = x.device();
+        const c10::DeviceGuard guard(dev);  // the default stream's handle is the current GPU's
         ssu_norm_args_t args = {};
         describe_rows(x, dev, "x", &args.x);
         describe(weight, dev, &args.weight);
@@ -264,6 +266,7 @@ PyObject *mx_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor &x = required(a[0], "x"), &w = required(a[2], "weight"), &ws = required(a[3], "weight_scale");
         const at::Tensor *x_scale = tensor(a[1]), *bias = tensor(a[4]), *out = tensor(a[6]);
         const at::Device dev = x.device();
+        const c10::DeviceGuard guard(dev);  // the default stream's handle is the current GPU's
         ssu_mx_linear_args_t args = {};
         describe_rows(x, dev, "x", &args.x);
         describe(w, dev, &args.w);
@@ -296,6 +299,7 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor *mask = tensor(a[2]), *temperature = tensor(a[3]);
         const int64_t top = as_int(a[4]);
         const at::Device dev = logits.device();
+        const c10::DeviceGuard guard(dev);
         if (top < 0)
             raise(PyExc_ValueError, "top must not be negative");
         ssu_logprob_args_t args = {};

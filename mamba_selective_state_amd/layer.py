@@ -179,9 +179,10 @@ def mx_quantize(x, out_format="mxfp4", codes=None, scales=None):
     if scales is None:
         scales = torch.empty(ss, dtype=torch.uint8, device=x.device)
     dev = x.device
-    ssu_mx_quantize(tensor_desc(_rows(x, "x"), dev), tensor_desc(_rows(codes, "codes"), dev),
-                    tensor_desc(_rows(scales, "scales"), dev), fmt,
-                    _stream_of(x))
+    args = (tensor_desc(_rows(x, "x"), dev), tensor_desc(_rows(codes, "codes"), dev),
+            tensor_desc(_rows(scales, "scales"), dev), fmt, _stream_of(x))
+    with torch.cuda.device(dev):  # the default stream's handle is the current GPU's
+        ssu_mx_quantize(*args)
     return codes, scales
 
 
