@@ -6,7 +6,8 @@ ssu_mx_linear, ssu_token_logprobs. High level: add_rms_norm, mx_quantize,
 mx_linear and token_logprobs, which take torch tensors and allocate what they
 return; the marshalling of the three that a decode step calls is in C++
 (csrc/ssu_torch.cpp), since their kernels take no longer than it takes in
-Python. Without that module, as without the library, the import fails.
+Python. That module, which is bound to the torch it was built with, is loaded by
+the first call of one of them; without it the call raises ImportError.
 """
 import collections
 import ctypes
@@ -14,7 +15,6 @@ import ctypes
 import torch
 
 from .ssu import OK, SsuError, SsuTensor, _lib, _raise, tensor_desc
-from . import _ssu_torch as _native
 
 FORMAT_SAME, FORMAT_MXFP4, FORMAT_MXFP8 = 0, 4, 8
 TOP_MAX = 32  # SSU_TOP_MAX
@@ -54,14 +54,26 @@ _lib.ssu_token_logprobs.argtypes = [ctypes.POINTER(SsuLogprobArgs), ctypes.c_voi
 _lib.ssu_token_logprobs.restype = ctypes.c_int
 
 
-_native.set_error_type(SsuError)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_module = None
+
+
+def _native():
+    global _module
+    if _module is None:
+        try:
+            from . import _ssu_torch
+        except ImportError as e:
+            raise ImportError("_ssu_torch.so is missing or was built for another torch: build the "
+                              "package again (%s)" % e) from e
+        _ssu_torch.set_error_type(SsuError)
+        _module = _ssu_torch
+    return _module
 
 
 def _stream_of(t):
     """The handle of the current stream of a tensor's GPU (0 for a tensor that has none: the
     operators refuse it)."""
-    return _raw_stream(t.get_device()) if t.is_cuda else 0
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
 
 
 def _stream(stream):
@@ -160,8 +172,8 @@ def add_rms_norm(x, weight, residual=None, gate=None, groups=1, eps=1e-5, out_fo
     dtype. Outputs are allocated unless given; residual_out may be residual
     and out may be x. u is not rounded before the norm."""
     fmt = FORMAT_SAME if out_format is None else _format(out_format)
-    y, scales, u = _native.add_rms_norm(x, weight, residual, gate, groups, eps, fmt, out,
-                                        out_scales, residual_out, _stream_of(x))
+    y, scales, u = _native().add_rms_norm(x, weight, residual, gate, groups, eps, fmt, out,
+                                          out_scales, residual_out, _stream_of(x))
     if scales is not None:
         y = (y, scales)
     return y if residual is None else (y, u)
@@ -216,7 +228,7 @@ def mx_linear(x, weight, weight_scale, bias=None, activation="mxfp8", out=None, 
     like = x if x_scale is None else None  # of the result's dtype; None: bfloat16
     if out is None and out_dtype is not None and out_dtype != (x.dtype if like is x else torch.bfloat16):
         out = torch.empty(x.shape[:-1] + weight.shape[:1], dtype=out_dtype, device=x.device)
-    return _native.mx_linear(x, x_scale, weight, weight_scale, bias, fmt, out, like, _stream_of(x))
+    return _native().mx_linear(x, x_scale, weight, weight_scale, bias, fmt, out, like, _stream_of(x))
 
 
 TokenLogprobs = collections.namedtuple(
@@ -247,5 +259,5 @@ def token_logprobs(logits, tokens, top=0, mask=None, temperature=None):
     alternatives are -1 and -inf. Returns a TokenLogprobs of float32 logprob and
     entropy, int32 rank, and int32 top_tokens and float32 top_logprobs
     [rows, top] (None without top)."""
-    return TokenLogprobs(*_native.token_logprobs(logits, tokens, mask, temperature, top,
-                                                 _stream_of(logits)))
+    return TokenLogprobs(*_native().token_logprobs(logits, tokens, mask, temperature, top,
+                                                   _stream_of(logits)))
