@@ -87,7 +87,9 @@ def build(out=LIB, extra=(), ceiling=True):
             list(pool.map(compile_one, range(len(srcs) + module)))
         link(out, objs[:len(SOURCES)])
         if module:
-            link(TORCH_LIB, [torch_obj, *torch_libs, out, "-Wl,-rpath,$ORIGIN"], ["g++"])
+            # by its bare name: a path would be looked up as it is, past the rpath
+            link(TORCH_LIB, [torch_obj, *torch_libs, "-L" + os.path.dirname(out),
+                             "-l:" + os.path.basename(out), "-Wl,-rpath,$ORIGIN"], ["g++"])
         if ceiling:
             link(CEILING_LIB, objs[len(SOURCES):])
     finally:

@@ -1,4 +1,4 @@
-"""The package in another folder: without _ssu_torch.so."""
+"""The package in another folder: without _ssu_torch.so, and with its own libraries."""
 import os
 import shutil
 import subprocess
@@ -44,3 +44,17 @@ for f in (lambda: ssu.add_rms_norm(x, x[0]), lambda: ssu.mx_linear(x, x, x), lam
         print("refused")
 """)
     assert out[0].startswith(str(tmp_path)) and out[1:] == ["refused"] * 3
+
+
+def test_copied_package_uses_its_own_library(tmp_path):
+    dst = copy_package(tmp_path)
+    out = run(tmp_path, """
+import torch
+import mamba_selective_state_amd as ssu
+try:
+    ssu.add_rms_norm(torch.zeros(2, 64), torch.zeros(64))
+except ValueError:
+    pass
+print(*sorted({l.split()[-1] for l in open("/proc/self/maps") if "ssu" in l and ".so" in l}))
+""")
+    assert out == [os.path.join(dst, n) for n in ("_ssu_torch.so", "libssu.so")]
