@@ -186,6 +186,16 @@ uintptr_t as_stream(PyObject *o) {
     return static_cast<uintptr_t>(v);
 }
 
+// torch.OutOfMemoryError, by which callers tell it from other errors.
+void set_out_of_memory(const char *what) {
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type)
+        PyErr_SetString(type, what);  // otherwise the import's own error stands
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
+}
+
 // No C++ exception leaves the module.
 template <typename F>
 PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F &&f) {
@@ -194,6 +204,10 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F &&f) {
             raise(PyExc_TypeError, "wrong number of arguments");
         return f();
     } catch (const PythonError &) {
+    } catch (const c10::OutOfMemoryError &e) {
+        set_out_of_memory(e.what_without_backtrace());
+    } catch (const c10::Error &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {

@@ -108,3 +108,14 @@ def test_quantized_bytes():
     low, high = got & 15, got >> 4
     low, high = (torch.where(h == zero[0], zero[1], h) for h in (low, high))
     assert torch.equal(low | (high << 4), R.encode_e2m1(q)) and torch.equal(scales.cpu(), byte)
+
+
+def test_out_of_memory_is_torch_s():
+    """An output that no GPU holds (the product's 360 GB): torch's own error, and the next call works."""
+    x = torch.zeros(600_000, 32, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(300_000, 16, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(300_000, 1, dtype=torch.uint8, device="cuda")
+    print("[gpu] abi: more memory than there is", flush=True)
+    with pytest.raises(torch.OutOfMemoryError):
+        ssu.mx_linear(x, w, s)
+    assert ssu.mx_linear(x[:40], w[:64], s[:64]).shape == (40, 64)
