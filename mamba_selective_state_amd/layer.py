@@ -216,8 +216,8 @@ def mx_linear(x, weight, weight_scale, bias=None, activation="mxfp8", out=None, 
     x is a float tensor [..., k], quantised in the call to `activation`
     ("mxfp8" or "mxfp4"), or a pair (codes, scales) from add_rms_norm or mx_quantize
     (its format is taken from its width). The result [..., n] has out_dtype
-    (default: x's dtype, bfloat16 for a pair); sums are kept in float32 and
-    rounded once."""
+    (default: x's dtype, bfloat16 for a pair; `out`'s, if that is given); sums are kept in
+    float32 and rounded once."""
     x_scale = None
     if isinstance(x, (tuple, list)):
         x, x_scale = x
@@ -226,7 +226,10 @@ def mx_linear(x, weight, weight_scale, bias=None, activation="mxfp8", out=None, 
     else:
         fmt = _format(activation)
     like = x if x_scale is None else None  # of the result's dtype; None: bfloat16
-    if out is None and out_dtype is not None and out_dtype != (x.dtype if like is x else torch.bfloat16):
+    if out is not None:
+        if out_dtype is not None and out_dtype != out.dtype:
+            raise ValueError("out_dtype is %s, out has %s" % (out_dtype, out.dtype))
+    elif out_dtype is not None and out_dtype != (x.dtype if like is x else torch.bfloat16):
         out = torch.empty(x.shape[:-1] + weight.shape[:1], dtype=out_dtype, device=x.device)
     return _native().mx_linear(x, x_scale, weight, weight_scale, bias, fmt, out, like, _stream_of(x))
 
