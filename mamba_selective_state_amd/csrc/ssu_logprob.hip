@@ -10,9 +10,9 @@
 // all was the difference of two numbers near 11, off by up to 2e-6 instead of 1e-7. All sums are
 // f32, eight logits at a time, then a lane's, a wave's, a workgroup's.
 //
-// The logits' bytes bound it: 2048 x 65536 bf16 (268 MB) take 46 us without alternatives (5.8 TB/s). With
-// them a wave looks at an access twice only if a logit reaches its gate; 1024 x 131072 bf16
-// with 8 take 64 us, with 20 84. A row is one workgroup's (four waves that take turns at
+// The logits' bytes bound it: 1024 x 131072 bf16 (268 MB, from HBM) take 55 us without alternatives (4.9
+// TB/s). With them a wave looks at an access twice only if a logit reaches its gate: with 8 the
+// same rows take 67 us, with 20 84. A row is one workgroup's (four waves that take turns at
 // its accesses, four in flight each), or several workgroups' if there are few rows (see kSplitBelow).
 #include <algorithm>
 

@@ -98,7 +98,8 @@ __device__ __forceinline__ void store_out4(const MxParams &p, int m, int n, f32x
 // MXFP8 on the way, take 8.7 us (40.4 MB, 4.6 TB/s).
 //
 // kMxRowsMax: with 16 rows 18560 x 4096 MXFP8 takes 20.9 us here and 21.7 in the tiled kernels, with 32 34.6
-// and 23.4; 4096 x 8192 MXFP4 10.2 and 14.9, 13.4 and 15.8. 16 is also the instruction's other side.
+// and 23.4; 4096 x 8192 MXFP4 10.2 and 14.9, 13.4 and 15.8: there 32 rows too would be faster here, which a rule by rows
+// alone gives away. 16 is also the instruction's other side.
 // kMxFuseRows: every workgroup quantises all rows for itself: 12.4 us with 4 rows, where a
 // launch of its own takes 15.8 for 5; the work grows with the rows, and the LDS for them.
 
@@ -509,11 +510,13 @@ __device__ __forceinline__ void finish_tile(const MxParams &p, f32x16 (&acc)[FM]
 }
 
 // The matrix instructions bound it, and the 64 KB per K tile that come from the L2: 8192 x 18560 x 4096 MXFP4
-// runs at 3400 TF in all (366 us with the 20 of the quantisation), its loop at 4500 of the 6800 TF that registers alone
-// reach (5200 with zero codes, which draw less power). A tile's first fetches and its stores, 16 us a
-// round, are not covered by another workgroup: the sums take all accumulators of a compute unit, and four
-// images or more outputs per wave brought nothing. The stores of whole runs go past the
-// caches, which keep activations and weights (408 us without).
+// runs at 3300 TF in all (375 us with the 20 of the quantisation; 367 to 387 from run to run). By the
+// kernel's times with 8192 x 18432 (nine rounds of tiles) from k = 1024 to 8192, 139 to 600 us, the loop
+// runs at 4700 TF (MXFP8, 175 to 888 us: 3000), where registers alone reach 6800 (5200 with zero codes, which draw less
+// power), and 8 us a round do not depend on k (12 with 8192 x 8192, four rounds): a tile's first fetches and its
+// stores, which no other workgroup covers. A wave has all 512 registers of its lanes, half of them sums,
+// so a compute unit holds one workgroup. Four images or more outputs per wave brought nothing. The stores of whole
+// runs go past the caches, which keep activations and weights (408 us without, 388 with them then).
 //
 // TM x TN outputs per workgroup; the waves are WM x WN over the tile. Codes go straight
 // from memory to two LDS images: while one K tile is multiplied the next arrives. Each

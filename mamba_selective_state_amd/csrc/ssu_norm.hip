@@ -1,9 +1,9 @@
 // Gated, residual-adding RMS norm (ssu_add_rms_norm): per part of a row,
 //   u = x * silu(gate) + residual,  y = u * rsqrt(mean u^2 + eps) * weight.
 // The bytes bound it: every input is read once, u stays in registers between the sum
-// and the outputs, and the MX codes are made where y is. 16384 x 8192 bf16 with a gate, 8 groups, to MXFP8: 133 us
-// (675 MB, 5.1 TB/s, a plain copy's rate); with a residual instead, to bf16, 187 us (5.7 TB/s). 256 x 4096
-// with a residual to MXFP8: 4.5 us, most of it the way there and back of one access and a barrier.
+// and the outputs, and the MX codes are made where y is. 16384 x 8192 bf16 with a gate, 8 groups, to MXFP8: 134 us
+// (675 MB, 5.0 TB/s, a plain copy's rate); with a residual instead, to bf16, 190 us (5.6 TB/s). 256 x 4096
+// with a residual to MXFP8: 4.8 us, most of it the way there and back of one access and a barrier.
 // u and the sum are f32; the residual is rounded to its type when it is stored, y is made of the
 // unrounded u.
 #include <algorithm>
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(LANES < kNormThreads ? kNormThreads : LANES) void n
 }
 
 // Parts that no workgroup's registers hold: the inputs are read again for the outputs (2048
-// rows of 65536 bf16 with a residual: 278 us, 3.9 TB/s counting each byte once). Parts of
+// rows of 65536 bf16 with a residual: 284 us, 3.8 TB/s counting each byte once). Parts of
 // fewer than eight elements: one wave each.
 constexpr int kLongThreads = 1024;
 template <typename T, int FORMAT>
@@ -280,6 +280,8 @@ struct NormShape {
 // with a residual:
 //   256 x 2048: 64 lanes 4.27, 256 lanes 2.65; 1024 x 2048: 5.17, 4.04; 4096 x 2048: 10.8, 12.3
 //   256 x 8192: 256 lanes 5.16, 1024 lanes 4.33; 1024 x 8192: 10.8, 13.3
+//   256 x 4096: 256 lanes 4.70, 1024 lanes 4.24; 900 x 4096: 9.3, 10.9; 900 x 2561: 6.7, 8.3 (so for
+//     up to 4096 the two cross between 256 and 900 rows, where the rule takes 256 lanes throughout)
 //   65536 x 128: 16 lanes 13.0, 64 lanes 23.7; 65536 x 512: 64 lanes 40, 256 lanes 57
 NormShape shape_for(int64_t parts, int part) {
     if (part < 8)
