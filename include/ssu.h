@@ -568,6 +568,75 @@ SSU_API int64_t ssu_token_logprobs_workspace_bytes(const ssu_logprob_args_t *arg
 SSU_API ssu_status_t ssu_token_logprobs(const ssu_logprob_args_t *args, void *workspace,
                                         int64_t workspace_bytes, void *stream);
 
+/* Low-rank adapters of many requests beside a shared projection: to every row of y,
+ *   y[r] += scale[i] * (x[r] a[i]^T) b[i]^T,   i = adapter[r]
+ * A row whose adapter is none of [0, adapters) (-1, say) keeps its bytes. What one adapter's weights hold reaches no
+ * row of another.
+ *   x        as ssu_mx_linear takes it: f32 / f16 / bf16 [rows, k], last stride 1; or u8 codes of
+ *            x_format ([rows, k] or [rows, k / 2]) with x_scale u8 [rows, k / 32], last strides 1
+ *   a        [adapters, rank, k], last stride 1, x's dtype (bf16 where x is codes)
+ *   b        [adapters, n, rank], last stride 1, a's dtype
+ *   adapter  [rows] i32 / i64, in any order
+ *   scale    [adapters] f32, or absent (1)
+ *   y        [rows, n], a's dtype, last stride 1: read and written; overlaps nothing else
+ *   x_format SSU_FORMAT_SAME, or the codes' SSU_FORMAT_MXFP8 / SSU_FORMAT_MXFP4 (k a multiple of 32)
+ * rank is at most SSU_LORA_RANK_MAX, adapters at most SSU_LORA_ADAPTERS_MAX. Both products are summed in f32; x a^T reaches
+ * the second one as f32, or as two summands of the 16-bit type (16 bits of it in bf16, 22 in f16, or what is above
+ * 2^-24 of the row's largest); y is rounded once.
+ * `workspace`: as for ssu_mx_linear. Two or three kernels. */
+#define SSU_LORA_RANK_MAX 128
+#define SSU_LORA_ADAPTERS_MAX 4096
+typedef struct {
+    ssu_tensor_t x, x_scale, a, b, adapter, scale, y;
+    int32_t x_format; /* ssu_format_t */
+} ssu_lora_args_t;
+
+SSU_API int64_t ssu_add_lora_workspace_bytes(const ssu_lora_args_t *args);
+SSU_API ssu_status_t ssu_add_lora(const ssu_lora_args_t *args, void *workspace, int64_t workspace_bytes,
+                                  void *stream);
+
+/* ---- Beam search over a batch of requests, `beams` sequences each.
+ *
+ * The choice of continuations. Token v after beam i scores
+ *   scores[b, i] + logits[b, i, v] - log sum over the allowed tokens of e^logits[b, i, .]
+ * (allowed: mask bit set, logit above -inf); a finished beam has one continuation, end_token at scores[b, i], whatever its
+ * logits hold; a beam at -inf has none. Of each request's continuations the first `keep` are given: larger scores first, equal
+ * ones by beam, then by token; a beam's own order is that of its logits. Where there are fewer: -inf, -1, -1. A NaN or +inf
+ * among a request's scores, or among the allowed logits of a beam that is neither finished nor at -inf,
+ * makes all its out_scores NaN, its parents and tokens -1. Log sums, and the scores by which beams are compared, are held in
+ * 64 bits over sums in f32.
+ *   logits      [batch * beams, vocab], f32 / f16 / bf16, last stride 1
+ *   scores      [batch, beams] f32
+ *   finished    [batch, beams] u8 (0 or not), or absent
+ *   mask        as for ssu_token_logprobs, a row for each of the logits'
+ *   out_scores  [batch, keep] f32, contiguous; out_parents (beams), out_tokens [batch, keep] i32, contiguous
+ *   end_token   in [0, vocab) where finished is given
+ * beams is at most SSU_BEAMS_MAX, keep at most SSU_TOP_MAX. `workspace`: as for ssu_mx_linear. Two kernels. */
+#define SSU_BEAMS_MAX 64
+typedef struct {
+    ssu_tensor_t logits, scores, finished, mask;
+    ssu_tensor_t out_scores, out_parents, out_tokens;
+    int32_t end_token;
+} ssu_beam_args_t;
+
+SSU_API int64_t ssu_beam_select_workspace_bytes(const ssu_beam_args_t *args);
+SSU_API ssu_status_t ssu_beam_select(const ssu_beam_args_t *args, void *workspace, int64_t workspace_bytes,
+                                     void *stream);
+
+/* The sequences' states after it. Beam j of request b goes on from its beam parents[b, j]: the first such j of a parent
+ * keeps that parent's slot, every further one gets the slot of a beam that has none, in the order of both, and in every pool
+ * the parent's slot is copied there. A j whose parent is none of [0, beams) (-1, say) gets such a slot too, with nothing
+ * copied. out_slots[b, j] is beam j's slot from now on; together they are the request's slots as before.
+ *   pools      `count` tensors [slots, ...] of any dtype of ssu_dtype_t, a slot's elements contiguous; no two overlap
+ *   slots      [batch, beams] i32 / i64: the beams' slots, each slot once. A copy from or to one that a
+ *              pool does not have (a pad id, say) is left out.
+ *   parents    [batch, beams] i32 / i64
+ *   out_slots  [batch, beams] i32 / i64, rows contiguous; overlaps neither slots nor parents
+ * Slots of 2^31 - 1 and above, or below 0, come back as -1. beams is at most SSU_BEAMS_MAX. One kernel for up to 64 pools. */
+SSU_API ssu_status_t ssu_reorder_states(const ssu_tensor_t *pools, int32_t count, const ssu_tensor_t *slots,
+                                        const ssu_tensor_t *parents, const ssu_tensor_t *out_slots,
+                                        void *stream);
+
 /* Message of the last failing call on this thread ("" if none). The pointer
  * stays valid until the next call on the same thread. */
 SSU_API const char *ssu_last_error(void);

@@ -16,11 +16,14 @@ from .ssu import (LIBRARY_PATH, SsuArgs, SsuConvShiftArgs, SsuError, SsuReplayAr
                   replay_spec_selective_state_update, selective_state_update, ssu_abi_version,
                   ssu_batch_memcpy, ssu_conv_state_shift, ssu_last_error, ssu_plan,
                   ssu_replay_spec_update, ssu_replay_update, ssu_update)
-from .layer import (SsuLogprobArgs, SsuMxLinearArgs, SsuNormArgs, TokenLogprobs, add_rms_norm,
-                    make_logprob_args, make_mx_linear_args, make_norm_args, mx_linear, mx_quantize,
+from .layer import (SsuLogprobArgs, SsuLoraArgs, SsuMxLinearArgs, SsuNormArgs, TokenLogprobs, add_lora,
+                    add_rms_norm, make_logprob_args, make_lora_args, make_mx_linear_args, make_norm_args,
+                    mx_linear, mx_quantize, ssu_add_lora, ssu_add_lora_workspace_bytes,
                     ssu_add_rms_norm, ssu_mx_linear, ssu_mx_linear_workspace_bytes,
                     ssu_mx_quantize, ssu_token_logprobs, ssu_token_logprobs_workspace_bytes,
                     token_logprobs)
+from .search import (BeamSelection, SsuBeamArgs, beam_select, make_beam_args, reorder_states,
+                     ssu_beam_select, ssu_beam_select_workspace_bytes, ssu_reorder_states)
 
 __all__ = ["selective_state_update", "prewarm_selective_state_update",
            "replay_selective_state_update", "replay_spec_selective_state_update", "ssu_update",
@@ -38,4 +41,6 @@ __all__ = ["selective_state_update", "prewarm_selective_state_update",
            "ssu_add_rms_norm", "ssu_mx_quantize", "ssu_mx_linear", "ssu_mx_linear_workspace_bytes",
            "ssu_token_logprobs", "ssu_token_logprobs_workspace_bytes", "SsuNormArgs",
            "SsuMxLinearArgs", "SsuLogprobArgs", "make_norm_args", "make_mx_linear_args",
-           "make_logprob_args"]
+           "make_logprob_args", "add_lora", "ssu_add_lora", "ssu_add_lora_workspace_bytes", "SsuLoraArgs",
+           "make_lora_args", "beam_select", "reorder_states", "BeamSelection", "ssu_beam_select",
+           "ssu_beam_select_workspace_bytes", "ssu_reorder_states", "SsuBeamArgs", "make_beam_args"]

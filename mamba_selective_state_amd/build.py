@@ -12,7 +12,8 @@ SOURCES = [os.path.join(CSRC, "ssu_kernels.hip"), os.path.join(CSRC, "ssu_replay
            os.path.join(CSRC, "ssu_copy.hip"),
            os.path.join(CSRC, "ssu_ssd.hip"), os.path.join(CSRC, "ssu_noalloc.hip"),
            os.path.join(CSRC, "ssu_norm.hip"), os.path.join(CSRC, "ssu_mx.hip"),
-           os.path.join(CSRC, "ssu_logprob.hip"),
+           os.path.join(CSRC, "ssu_logprob.hip"), os.path.join(CSRC, "ssu_lora.hip"),
+           os.path.join(CSRC, "ssu_beam.hip"), os.path.join(CSRC, "ssu_reorder.hip"),
            os.path.join(CSRC, "ssu_api.cpp"), os.path.join(CSRC, "ssu_layer_api.cpp")]
 # Streaming-ceiling kernels for the benchmark (a separate library, not part
 # of libssu's interface).
@@ -24,6 +25,7 @@ TORCH_SRC = os.path.join(CSRC, "ssu_torch.cpp")
 TORCH_LIB = os.path.join(HERE, "_ssu_torch.so")
 HEADERS = [os.path.join(CSRC, "ssu_internal.h"), os.path.join(CSRC, "ssu_device.h"),
            os.path.join(CSRC, "ssu_layer.h"), os.path.join(CSRC, "ssu_layer_device.h"),
+           os.path.join(CSRC, "ssu_logits_device.h"),
            os.path.join(os.path.dirname(HERE), "include", "ssu.h")]
 
 # Packed-fp32 instructions are switched off for all device code; hipcc -O3

@@ -1,6 +1,6 @@
 // Internal interface between the host entry points of the layer operators
 // (ssu_layer_api.cpp) and their gfx950 kernels (ssu_norm.hip, ssu_mx.hip,
-// ssu_logprob.hip).
+// ssu_logprob.hip, ssu_lora.hip, ssu_beam.hip, ssu_reorder.hip).
 #pragma once
 
 #include <stdint.h>
@@ -65,5 +65,55 @@ struct LogprobParams {
 // Workspace bytes (0 where a row is not split).
 int64_t logprobs_workspace(int64_t rows, int64_t vocab, int64_t top);
 int launch_logprobs(const LogprobParams &p, int dtype, void *stream);
+
+// Low-rank adapters. Strides in elements (x's and its scales' in bytes for codes).
+struct LoraParams {
+    const void *x, *a, *b, *ids;
+    const uint8_t *x_scale;  // of codes
+    const float *scale;      // may be null
+    void *y;
+    int64_t x_s, xs_s, a_l, a_r, b_l, b_n, ids_s, scale_s, y_s;
+    int32_t rows, k, n, rank, adapters, ids_i64;
+    int32_t slices, slice;  // of k; set by the launch
+    uint8_t *workspace;
+};
+int64_t lora_workspace(int64_t rows, int64_t adapters, int64_t k, int64_t rank);
+int launch_add_lora(const LoraParams &p, int dtype, int format, void *stream);
+
+// Beam search: choice of continuations. Strides in elements.
+struct BeamParams {
+    const void *logits;
+    const float *scores;
+    const uint8_t *finished;  // may be null
+    const int32_t *mask;      // may be null
+    float *out_scores;
+    int32_t *out_parents, *out_tokens;
+    int64_t logits_s, scores_b, scores_s, finished_b, finished_s, mask_s;
+    int64_t batch;
+    int32_t beams, vocab, keep, end_token;
+    uint8_t *workspace;
+};
+int64_t beam_workspace(int64_t rows, int64_t vocab, int64_t keep);
+int launch_beam_select(const BeamParams &p, int dtype, void *stream);
+
+// Beam search: states after the choice. Strides of slots, parents and out in elements, of a
+// pool in bytes.
+constexpr int kReorderPools = 64;  // of one launch
+struct ReorderPool {
+    uint8_t *base;
+    int64_t stride, bytes;  // of a slot
+    int64_t slots;
+};
+struct ReorderParams {
+    const void *slots, *parents;
+    void *out;
+    int64_t slots_b, slots_s, parents_b, parents_s, out_b;
+    int64_t batch, piece;  // bytes of a slot that a workgroup copies; set by the launch
+    int32_t beams, count;
+    int32_t slots_i64, parents_i64, out_i64;
+    int32_t first_piece[kReorderPools + 1];  // set by the launch
+    ReorderPool pool[kReorderPools];
+};
+int launch_reorder(const ReorderParams &p, void *stream);
 
 }  // namespace ssu

@@ -1,5 +1,5 @@
-// Host entry points of the layer operators (norm, MX product, token log
-// probabilities): argument validation and launches, with the conventions of
+// Host entry points of the layer operators (norm, MX product, low-rank adapters, token log
+// probabilities) and of beam search: argument validation and launches, with the conventions of
 // ssu_api.cpp -- only shapes, strides, dtypes and alignment are looked at.
 #include <math.h>
 #include <stdarg.h>
@@ -35,7 +35,7 @@ constexpr int64_t kMostSize = INT32_MAX - 65536;
 
 bool is_float(int d) { return d == SSU_F32 || d == SSU_F16 || d == SSU_BF16; }
 bool is_index(int d) { return d == SSU_I32 || d == SSU_I64; }
-int64_t elem_bytes(int d) { return d == SSU_F32 || d == SSU_I32 ? 4 : d == SSU_U8 ? 1 : d == SSU_I64 ? 8 : 2; }
+int64_t elem_bytes(int d) { return d == SSU_F32 || d == SSU_I32 ? 4 : d == SSU_U8 ? 1 : d == SSU_I64 || d == SSU_F64 ? 8 : 2; }
 bool present(const ssu_tensor_t &t) { return t.data != nullptr; }
 bool aligned(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
 
@@ -90,6 +90,47 @@ ssu_status_t mx_output(const ssu_tensor_t &codes, const ssu_tensor_t &scales, co
     if (!aligned(codes.data, 8))
         return fail(SSU_ERR_VALUE, "%s must be 8-byte aligned", codes_name);
     return SSU_OK;
+}
+
+// [a, b] with any strides that are not negative, b's being 0 where it has one element.
+ssu_status_t table(const char *name, const ssu_tensor_t &t, int64_t a, int64_t b, int64_t *sa, int64_t *sb) {
+    if (!present(t))
+        return fail(SSU_ERR_VALUE, "%s is required", name);
+    if (t.ndim != 2 || t.size[0] != a || t.size[1] != b)
+        return fail(SSU_ERR_VALUE, "%s must be [%lld, %lld]", name, (long long)a, (long long)b);
+    if ((a > 1 && t.stride[0] < 0) || (b > 1 && t.stride[1] < 0))
+        return fail(SSU_ERR_VALUE, "%s has a negative stride", name);
+    if (!aligned(t.data, elem_bytes(t.dtype)))
+        return fail(SSU_ERR_VALUE, "%s is not aligned to its element size", name);
+    *sa = a > 1 ? t.stride[0] : 0;
+    *sb = b > 1 ? t.stride[1] : 0;
+    return SSU_OK;
+}
+
+// An adapter's matrices, [adapters, rows, cols].
+ssu_status_t matrices(const char *name, const ssu_tensor_t &t, int64_t count, int64_t rows, int64_t cols, int64_t *s0, int64_t *s1) {
+    if (t.size[0] != count || t.size[1] != rows || t.size[2] != cols)
+        return fail(SSU_ERR_VALUE, "%s must be [%lld, %lld, %lld]", name, (long long)count, (long long)rows, (long long)cols);
+    if (cols > 1 && t.stride[2] != 1)
+        return fail(SSU_ERR_VALUE, "%s needs last stride 1", name);
+    if ((count > 1 && t.stride[0] < 0) || (rows > 1 && t.stride[1] < 0))
+        return fail(SSU_ERR_VALUE, "%s has a negative stride", name);
+    if (!aligned(t.data, elem_bytes(t.dtype)))
+        return fail(SSU_ERR_VALUE, "%s is not aligned to its element size", name);
+    *s0 = count > 1 ? t.stride[0] : 0;
+    *s1 = rows > 1 ? t.stride[1] : 0;
+    return SSU_OK;
+}
+
+// Whether the bytes of two [a, b] tables of non-negative strides can overlap.
+bool overlap(const ssu_tensor_t &x, const ssu_tensor_t &y) {
+    auto end = [](const ssu_tensor_t &t) {
+        int64_t last = 0;
+        for (int i = 0; i < t.ndim; i++)
+            last += t.size[i] > 1 ? (t.size[i] - 1) * t.stride[i] : 0;
+        return reinterpret_cast<uintptr_t>(t.data) + static_cast<uintptr_t>((last + 1) * elem_bytes(t.dtype));
+    };
+    return reinterpret_cast<uintptr_t>(x.data) < end(y) && reinterpret_cast<uintptr_t>(y.data) < end(x);
 }
 
 bool mx_format(int f) { return f == SSU_FORMAT_MXFP4 || f == SSU_FORMAT_MXFP8; }
@@ -363,6 +404,231 @@ ssu_status_t ssu_token_logprobs(const ssu_logprob_args_t *a, void *workspace, in
         return fail(SSU_ERR_VALUE, "workspace must be 256-byte aligned and hold %lld bytes", (long long)need);
     p.workspace = static_cast<uint8_t *>(workspace);
     return done(ssu::launch_logprobs(p, x.dtype, stream));
+}
+
+int64_t ssu_add_lora_workspace_bytes(const ssu_lora_args_t *a) {
+    if (!a || a->a.ndim != 3 || a->y.ndim != 2 || a->y.size[0] <= 0 || a->y.size[0] > kMostSize || a->a.size[0] <= 0 || a->a.size[1] <= 0 ||
+        a->a.size[1] > SSU_LORA_RANK_MAX || a->a.size[2] < 0 || a->a.size[2] > kMostSize)
+        return 0;
+    return ssu::lora_workspace(a->y.size[0], a->a.size[0], a->a.size[2], a->a.size[1]);
+}
+
+ssu_status_t ssu_add_lora(const ssu_lora_args_t *a, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!a)
+        return fail(SSU_ERR_VALUE, "ssu_add_lora: args is NULL");
+    if (a->x_format != SSU_FORMAT_SAME && !mx_format(a->x_format))
+        return fail(SSU_ERR_NOT_IMPLEMENTED, "x_format must be SAME, MXFP8 or MXFP4");
+    if (!present(a->y) || a->y.ndim != 2 || !present(a->a) || a->a.ndim != 3 || !present(a->b) || a->b.ndim != 3)
+        return fail(SSU_ERR_VALUE, "y must be 2-D, a and b 3-D");
+    const int64_t rows = a->y.size[0], n = a->y.size[1], adapters = a->a.size[0], rank = a->a.size[1], k = a->a.size[2];
+    if (rows < 0 || n < 0 || k < 0 || rows > kMostSize || n > kMostSize || k > kMostSize)
+        return fail(SSU_ERR_VALUE, "y or a has a size out of range");
+    if (rank < 0 || rank > SSU_LORA_RANK_MAX)
+        return fail(SSU_ERR_NOT_IMPLEMENTED, "rank must be at most %d", SSU_LORA_RANK_MAX);
+    if (adapters < 0 || adapters > SSU_LORA_ADAPTERS_MAX)
+        return fail(SSU_ERR_NOT_IMPLEMENTED, "at most %d adapters", SSU_LORA_ADAPTERS_MAX);
+    const int dtype = a->a.dtype;
+    if (!is_float(dtype) || a->b.dtype != dtype || a->y.dtype != dtype)
+        return fail(SSU_ERR_VALUE, "a, b and y must have one dtype: f32, f16 or bf16");
+    ssu::LoraParams p = {};
+    if (a->x_format == SSU_FORMAT_SAME) {
+        if (a->x.dtype != dtype)
+            return fail(SSU_ERR_VALUE, "x must have a's dtype");
+        if (present(a->x_scale))
+            return fail(SSU_ERR_VALUE, "x_scale belongs to the MX formats");
+        if (ssu_status_t st = matrix("x", a->x, rows, k, false, &p.x_s))
+            return st;
+    } else {
+        if (dtype != SSU_BF16)
+            return fail(SSU_ERR_VALUE, "x of codes needs a, b and y in bf16");
+        if (k % 32 != 0)
+            return fail(SSU_ERR_VALUE, "x of codes needs k to be a multiple of 32");
+        if (a->x.dtype != SSU_U8 || !present(a->x_scale) || a->x_scale.dtype != SSU_U8)
+            return fail(SSU_ERR_VALUE, "x of codes and x_scale must be u8");
+        if (ssu_status_t st = matrix("x", a->x, rows, a->x_format == SSU_FORMAT_MXFP4 ? k / 2 : k, false, &p.x_s))
+            return st;
+        if (ssu_status_t st = matrix("x_scale", a->x_scale, rows, k / 32, false, &p.xs_s))
+            return st;
+    }
+    if (ssu_status_t st = matrices("a", a->a, adapters, rank, k, &p.a_l, &p.a_r))
+        return st;
+    if (ssu_status_t st = matrices("b", a->b, adapters, n, rank, &p.b_l, &p.b_n))
+        return st;
+    if (!is_index(a->adapter.dtype))
+        return fail(SSU_ERR_VALUE, "adapter must be i32 or i64");
+    if (ssu_status_t st = vector("adapter", a->adapter, rows, false, &p.ids_s))
+        return st;
+    if (present(a->scale)) {
+        if (a->scale.dtype != SSU_F32)
+            return fail(SSU_ERR_VALUE, "scale must be f32");
+        if (ssu_status_t st = vector("scale", a->scale, adapters, false, &p.scale_s))
+            return st;
+    }
+    if (ssu_status_t st = matrix("y", a->y, rows, n, true, &p.y_s))
+        return st;
+    if (rows == 0 || n == 0 || k == 0 || rank == 0 || adapters == 0)
+        return done(0);
+    const int64_t need = ssu_add_lora_workspace_bytes(a);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(SSU_ERR_VALUE, "workspace must be 256-byte aligned and hold %lld bytes", (long long)need);
+    p.workspace = static_cast<uint8_t *>(workspace);
+    p.x = a->x.data;
+    p.x_scale = static_cast<const uint8_t *>(a->x_scale.data);
+    p.a = a->a.data;
+    p.b = a->b.data;
+    p.ids = a->adapter.data;
+    p.ids_i64 = a->adapter.dtype == SSU_I64;
+    p.scale = static_cast<const float *>(a->scale.data);
+    p.y = const_cast<void *>(a->y.data);
+    p.rows = static_cast<int32_t>(rows);
+    p.k = static_cast<int32_t>(k);
+    p.n = static_cast<int32_t>(n);
+    p.rank = static_cast<int32_t>(rank);
+    p.adapters = static_cast<int32_t>(adapters);
+    return done(ssu::launch_add_lora(p, dtype, a->x_format, stream));
+}
+
+int64_t ssu_beam_select_workspace_bytes(const ssu_beam_args_t *a) {
+    if (!a || a->logits.ndim != 2 || a->logits.size[0] <= 0 || a->logits.size[0] > INT32_MAX || a->logits.size[1] < 0 ||
+        a->out_tokens.ndim != 2 || a->out_tokens.size[1] <= 0 || a->out_tokens.size[1] > SSU_TOP_MAX)
+        return 0;
+    return ssu::beam_workspace(a->logits.size[0], a->logits.size[1], a->out_tokens.size[1]);
+}
+
+ssu_status_t ssu_beam_select(const ssu_beam_args_t *a, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!a)
+        return fail(SSU_ERR_VALUE, "ssu_beam_select: args is NULL");
+    const ssu_tensor_t &x = a->logits;
+    if (!present(x) || x.ndim != 2 || !is_float(x.dtype))
+        return fail(SSU_ERR_VALUE, "logits must be [batch * beams, vocab], f32, f16 or bf16");
+    if (!present(a->scores) || a->scores.ndim != 2 || a->scores.dtype != SSU_F32)
+        return fail(SSU_ERR_VALUE, "scores must be [batch, beams], f32");
+    const int64_t batch = a->scores.size[0], beams = a->scores.size[1], vocab = x.size[1];
+    if (beams < 1 || beams > SSU_BEAMS_MAX)
+        return fail(SSU_ERR_NOT_IMPLEMENTED, "beams must be 1 to %d", SSU_BEAMS_MAX);
+    if (batch < 0 || batch > INT32_MAX / beams || vocab < 0 || vocab > kMostSize)
+        return fail(SSU_ERR_VALUE, "scores or logits has a size out of range");
+    ssu::BeamParams p = {};
+    if (ssu_status_t st = matrix("logits", x, batch * beams, vocab, false, &p.logits_s))
+        return st;
+    if (ssu_status_t st = table("scores", a->scores, batch, beams, &p.scores_b, &p.scores_s))
+        return st;
+    if (present(a->finished)) {
+        if (a->finished.dtype != SSU_U8)
+            return fail(SSU_ERR_VALUE, "finished must be u8");
+        if (ssu_status_t st = table("finished", a->finished, batch, beams, &p.finished_b, &p.finished_s))
+            return st;
+        if (a->end_token < 0 || a->end_token >= vocab)
+            return fail(SSU_ERR_VALUE, "end_token must lie in the vocabulary");
+    }
+    if (present(a->mask)) {
+        if (a->mask.dtype != SSU_I32)
+            return fail(SSU_ERR_VALUE, "mask must be i32 words of 32 bits");
+        if (ssu_status_t st = matrix("mask", a->mask, batch * beams, (vocab + 31) / 32, false, &p.mask_s))
+            return st;
+    }
+    if (!present(a->out_tokens) || a->out_tokens.ndim != 2)
+        return fail(SSU_ERR_VALUE, "out_tokens must be [batch, keep]");
+    const int64_t keep = a->out_tokens.size[1];
+    if (keep < 0 || keep > SSU_TOP_MAX)
+        return fail(SSU_ERR_NOT_IMPLEMENTED, "keep must be at most %d", SSU_TOP_MAX);
+    if (a->out_scores.dtype != SSU_F32 || a->out_parents.dtype != SSU_I32 || a->out_tokens.dtype != SSU_I32)
+        return fail(SSU_ERR_VALUE, "out_scores must be f32, out_parents and out_tokens i32");
+    const struct {
+        const char *name;
+        const ssu_tensor_t &t;
+    } outs[] = {{"out_scores", a->out_scores}, {"out_parents", a->out_parents}, {"out_tokens", a->out_tokens}};
+    for (const auto &o : outs) {
+        int64_t s;
+        if (ssu_status_t st = matrix(o.name, o.t, batch, keep, true, &s))
+            return st;
+        if (s != keep)
+            return fail(SSU_ERR_VALUE, "%s must be contiguous", o.name);
+    }
+    if (batch == 0 || keep == 0)
+        return done(0);
+    const int64_t need = ssu_beam_select_workspace_bytes(a);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(SSU_ERR_VALUE, "workspace must be 256-byte aligned and hold %lld bytes", (long long)need);
+    p.workspace = static_cast<uint8_t *>(workspace);
+    p.logits = x.data;
+    p.scores = static_cast<const float *>(a->scores.data);
+    p.finished = static_cast<const uint8_t *>(a->finished.data);
+    p.mask = static_cast<const int32_t *>(a->mask.data);
+    p.out_scores = static_cast<float *>(const_cast<void *>(a->out_scores.data));
+    p.out_parents = static_cast<int32_t *>(const_cast<void *>(a->out_parents.data));
+    p.out_tokens = static_cast<int32_t *>(const_cast<void *>(a->out_tokens.data));
+    p.batch = batch;
+    p.beams = static_cast<int32_t>(beams);
+    p.vocab = static_cast<int32_t>(vocab);
+    p.keep = static_cast<int32_t>(keep);
+    p.end_token = a->end_token;
+    return done(ssu::launch_beam_select(p, x.dtype, stream));
+}
+
+ssu_status_t ssu_reorder_states(const ssu_tensor_t *pools, int32_t count, const ssu_tensor_t *slots, const ssu_tensor_t *parents,
+                                const ssu_tensor_t *out_slots, void *stream) {
+    if (!slots || !parents || !out_slots || count < 0 || (count > 0 && !pools))
+        return fail(SSU_ERR_VALUE, "ssu_reorder_states: a tensor is NULL");
+    if (!present(*slots) || slots->ndim != 2)
+        return fail(SSU_ERR_VALUE, "slots must be [batch, beams]");
+    const int64_t batch = slots->size[0], beams = slots->size[1];
+    if (beams < 1 || beams > SSU_BEAMS_MAX)
+        return fail(SSU_ERR_NOT_IMPLEMENTED, "beams must be 1 to %d", SSU_BEAMS_MAX);
+    if (batch < 0 || batch > INT32_MAX / beams)
+        return fail(SSU_ERR_VALUE, "slots has a size out of range");
+    if (!is_index(slots->dtype) || !is_index(parents->dtype) || !is_index(out_slots->dtype))
+        return fail(SSU_ERR_VALUE, "slots, parents and out_slots must be i32 or i64");
+    ssu::ReorderParams p = {};
+    if (ssu_status_t st = table("slots", *slots, batch, beams, &p.slots_b, &p.slots_s))
+        return st;
+    if (ssu_status_t st = table("parents", *parents, batch, beams, &p.parents_b, &p.parents_s))
+        return st;
+    if (ssu_status_t st = matrix("out_slots", *out_slots, batch, beams, true, &p.out_b))
+        return st;
+    if (batch > 0 && (overlap(*out_slots, *slots) || overlap(*out_slots, *parents)))
+        return fail(SSU_ERR_VALUE, "out_slots overlaps slots or parents");
+    p.slots = slots->data;
+    p.parents = parents->data;
+    p.out = const_cast<void *>(out_slots->data);
+    p.slots_i64 = slots->dtype == SSU_I64;
+    p.parents_i64 = parents->dtype == SSU_I64;
+    p.out_i64 = out_slots->dtype == SSU_I64;
+    p.batch = batch;
+    p.beams = static_cast<int32_t>(beams);
+    auto describe = [&](int32_t i, ssu::ReorderPool *to) {
+        const ssu_tensor_t &t = pools[i];
+        if (!present(t) || t.ndim < 1 || t.ndim > 4 || t.dtype < SSU_F32 || t.dtype > SSU_U8)
+            return fail(SSU_ERR_VALUE, "pool %d must be [slots, ...]", i);
+        int64_t elements = 1;
+        for (int d = 1; d < t.ndim; d++)
+            elements *= t.size[d];
+        int64_t inner = 1;
+        for (int d = t.ndim - 1; d > 0 && elements > 0; d--) {
+            if (t.size[d] > 1 && t.stride[d] != inner)
+                return fail(SSU_ERR_VALUE, "pool %d: a slot's elements must be contiguous", i);
+            inner *= t.size[d];
+        }
+        if (t.size[0] > 1 && t.stride[0] < elements)
+            return fail(SSU_ERR_VALUE, "pool %d has overlapping slots", i);
+        const int64_t b = elem_bytes(t.dtype);
+        *to = {static_cast<uint8_t *>(const_cast<void *>(t.data)), t.stride[0] * b, elements * b, t.size[0]};
+        return SSU_OK;
+    };
+    for (int32_t i = 0; i < count; i++)  // all are looked at before anything is enqueued
+        if (ssu_status_t st = describe(i, &p.pool[0]))
+            return st;
+    if (batch == 0)
+        return done(0);
+    for (int32_t at = 0; at == 0 || at < count; at += ssu::kReorderPools) {
+        p.count = count - at < ssu::kReorderPools ? count - at : ssu::kReorderPools;
+        for (int32_t i = 0; i < p.count; i++)
+            if (ssu_status_t st = describe(at + i, &p.pool[i]))
+                return st;
+        if (const int hip = ssu::launch_reorder(p, stream))
+            return done(hip);
+    }
+    return done(0);
 }
 
 }  // extern "C"

@@ -10,10 +10,10 @@
 namespace ssu {
 namespace {
 
-inline int launch_groups(const void *fn, int64_t groups, int threads, void **args, void *stream) {
+inline int launch_groups(const void *fn, int64_t groups, int threads, void **args, void *stream, unsigned lds_bytes = 0) {
     if (groups > static_cast<int64_t>(UINT32_MAX) / threads)
         return kTooManyWorkItems;
-    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(groups)), dim3(static_cast<unsigned>(threads)), args, 0,
+    return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(groups)), dim3(static_cast<unsigned>(threads)), args, lds_bytes,
                                             static_cast<hipStream_t>(stream)));
 }
 

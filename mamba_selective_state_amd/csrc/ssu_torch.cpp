@@ -349,6 +349,136 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// (y, x, x_scale, a, b, adapter, scale, format, stream) -> y
+PyObject *add_lora(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 9, [&] {
+        const at::Tensor &y = required(a[0], "y"), &x = required(a[1], "x"), &la = required(a[3], "lora_a"), &lb = required(a[4], "lora_b"),
+                         &adapter = required(a[5], "adapter");
+        const at::Tensor *x_scale = tensor(a[2]), *scale = tensor(a[6]);
+        const at::Device dev = y.device();
+        const c10::DeviceGuard guard(dev);  // the default stream's handle is the current GPU's
+        ssu_lora_args_t args = {};
+        describe_rows(y, dev, "y", &args.y);
+        describe_rows(x, dev, "x", &args.x);
+        if (x_scale)
+            describe_rows(*x_scale, dev, "x_scale", &args.x_scale);
+        describe(la, dev, &args.a);
+        describe(lb, dev, &args.b);
+        describe(adapter, dev, &args.adapter);
+        if (scale)
+            describe(*scale, dev, &args.scale);
+        args.x_format = static_cast<int32_t>(as_int(a[7]));
+        const uintptr_t stream = as_stream(a[8]);
+        const at::Tensor ws = scratch(y, ssu_add_lora_workspace_bytes(&args));
+        check(ssu_add_lora(&args, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, reinterpret_cast<void *>(stream)),
+              "ssu_add_lora");
+        return Py_NewRef(a[0]);
+    });
+}
+
+// (logits, scores, keep, finished, end_token, mask, stream) -> (scores, parents, tokens)
+PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 7, [&] {
+        const at::Tensor &logits = required(a[0], "logits"), &scores = required(a[1], "scores");
+        const at::Tensor *finished = tensor(a[3]), *mask = tensor(a[5]);
+        const int64_t keep = as_int(a[2]), end_token = as_int(a[4]);
+        const at::Device dev = logits.device();
+        const c10::DeviceGuard guard(dev);
+        if (keep < 0)
+            raise(PyExc_ValueError, "keep must not be negative");
+        if (end_token < INT32_MIN || end_token > INT32_MAX)
+            raise(PyExc_ValueError, "end_token must lie in the vocabulary");
+        ssu_beam_args_t args = {};
+        describe_rows(logits, dev, "logits", &args.logits);
+        describe(scores, dev, &args.scores);
+        if (finished) {
+            if (finished->scalar_type() == at::kBool)  // a byte each, 0 or 1
+                describe(finished->view(at::kByte), dev, &args.finished);
+            else
+                describe(*finished, dev, &args.finished);
+        }
+        if (mask) {
+            describe_rows(*mask, dev, "mask", &args.mask);
+            if (args.mask.size[0] == 1 && args.logits.size[0] != 1)  // one mask for all rows
+                args.mask.size[0] = args.logits.size[0], args.mask.stride[0] = 0;
+        }
+        args.end_token = static_cast<int32_t>(end_token);
+        const int64_t batch = scores.dim() ? scores.size(0) : 0;
+        const at::Tensor made[3] = {make(logits, {batch, keep}, at::kFloat), make(logits, {batch, keep}, at::kInt),
+                                    make(logits, {batch, keep}, at::kInt)};
+        ssu_tensor_t *at[3] = {&args.out_scores, &args.out_parents, &args.out_tokens};
+        for (int i = 0; i < 3; i++)
+            describe(made[i], dev, at[i]);
+        const uintptr_t stream = as_stream(a[6]);
+        const at::Tensor ws = scratch(logits, ssu_beam_select_workspace_bytes(&args));
+        check(ssu_beam_select(&args, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0,
+                              reinterpret_cast<void *>(stream)),
+              "ssu_beam_select");
+        PyObject *r = PyTuple_New(3);
+        if (!r)
+            throw PythonError();
+        for (int i = 0; i < 3; i++)
+            PyTuple_SET_ITEM(r, i, wrap(made[i]));
+        return r;
+    });
+}
+
+// A pool [slots, ...] of any type as the bytes of its slots.
+void describe_pool(const at::Tensor &t, const at::Device &dev, ssu_tensor_t *d) {
+    if (!t.is_cuda() || t.device() != dev)
+        raise(PyExc_ValueError, "every tensor must live on the first one's GPU");
+    if (t.dim() == 0)
+        raise(PyExc_ValueError, "a pool must be [slots, ...]");
+    int64_t elements = 1;
+    for (int64_t i = t.dim() - 1; i > 0; i--) {
+        if (t.size(i) > 1 && t.stride(i) != elements && t.numel() > 0)
+            raise(PyExc_ValueError, "a pool's slots must be contiguous");
+        elements *= t.size(i);
+    }
+    const int64_t bytes = static_cast<int64_t>(t.element_size());
+    d->data = t.data_ptr() ? t.data_ptr() : reinterpret_cast<void *>(16);
+    d->dtype = SSU_U8;
+    d->ndim = 2;
+    d->size[0] = t.size(0);
+    d->size[1] = elements * bytes;
+    d->stride[0] = t.stride(0) * bytes;
+    d->stride[1] = 1;
+}
+
+// (pools, slots, parents, out_slots, stream) -> out_slots
+PyObject *reorder_states(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 5, [&] {
+        const at::Tensor &slots = required(a[1], "slots"), &parents = required(a[2], "parents");
+        const at::Tensor *out = tensor(a[3]);
+        const at::Device dev = slots.device();
+        const c10::DeviceGuard guard(dev);
+        std::vector<ssu_tensor_t> pools;
+        if (THPVariable_Check(a[0])) {
+            pools.emplace_back();
+            describe_pool(required(a[0], "pools"), dev, &pools.back());
+        } else {
+            if (!PyList_Check(a[0]) && !PyTuple_Check(a[0]))
+                raise(PyExc_TypeError, "pools must be a torch.Tensor, or a list or tuple of them");
+            const Py_ssize_t count = PySequence_Fast_GET_SIZE(a[0]);
+            pools.resize(static_cast<size_t>(count));
+            for (Py_ssize_t i = 0; i < count; i++)
+                describe_pool(required(PySequence_Fast_GET_ITEM(a[0], i), "a pool"), dev, &pools[static_cast<size_t>(i)]);
+        }
+        ssu_tensor_t s = {}, p = {}, o = {};
+        describe(slots, dev, &s);
+        describe(parents, dev, &p);
+        at::Tensor made;
+        if (!out) {
+            made = make(slots, slots.sizes(), slots.scalar_type());
+            out = &made;
+        }
+        describe(*out, dev, &o);
+        check(ssu_reorder_states(pools.data(), static_cast<int32_t>(pools.size()), &s, &p, &o, reinterpret_cast<void *>(as_stream(a[4]))),
+              "ssu_reorder_states");
+        return given(a[3], made);
+    });
+}
+
 PyObject *set_error_type(PyObject *, PyObject *type) {
     Py_XDECREF(g_error_type);
     g_error_type = Py_NewRef(type);
@@ -364,6 +494,9 @@ PyMethodDef methods[] = {
     {"add_rms_norm", fast<add_rms_norm>(), METH_FASTCALL, nullptr},
     {"mx_linear", fast<mx_linear>(), METH_FASTCALL, nullptr},
     {"token_logprobs", fast<token_logprobs>(), METH_FASTCALL, nullptr},
+    {"add_lora", fast<add_lora>(), METH_FASTCALL, nullptr},
+    {"beam_select", fast<beam_select>(), METH_FASTCALL, nullptr},
+    {"reorder_states", fast<reorder_states>(), METH_FASTCALL, nullptr},
     {"set_error_type", set_error_type, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -2,9 +2,9 @@
 around the state update"): argument marshalling only, like ssu.py.
 
 Low level, same names as the C ABI: ssu_add_rms_norm, ssu_mx_quantize,
-ssu_mx_linear, ssu_token_logprobs. High level: add_rms_norm, mx_quantize,
-mx_linear and token_logprobs, which take torch tensors and allocate what they
-return; the marshalling of the three that a decode step calls is in C++
+ssu_mx_linear, ssu_add_lora, ssu_token_logprobs. High level: add_rms_norm, mx_quantize,
+mx_linear, add_lora and token_logprobs, which take torch tensors and allocate what they
+return; the marshalling of the four that a decode step calls is in C++
 (csrc/ssu_torch.cpp), since their kernels take no longer than it takes in
 Python. That module, which is bound to the torch it was built with, is loaded by
 the first call of one of them; without it the call raises ImportError.
@@ -18,6 +18,8 @@ from .ssu import OK, SsuError, SsuTensor, _lib, _raise, tensor_desc
 
 FORMAT_SAME, FORMAT_MXFP4, FORMAT_MXFP8 = 0, 4, 8
 TOP_MAX = 32  # SSU_TOP_MAX
+LORA_RANK_MAX = 128  # SSU_LORA_RANK_MAX
+LORA_ADAPTERS_MAX = 4096  # SSU_LORA_ADAPTERS_MAX
 _FORMATS = {"mxfp4": FORMAT_MXFP4, "mxfp8": FORMAT_MXFP8}
 
 
@@ -29,6 +31,11 @@ class SsuNormArgs(ctypes.Structure):
 
 class SsuMxLinearArgs(ctypes.Structure):
     _fields_ = [(n, SsuTensor) for n in ("x", "x_scale", "w", "w_scale", "bias", "out")] + [
+        ("x_format", ctypes.c_int32)]
+
+
+class SsuLoraArgs(ctypes.Structure):
+    _fields_ = [(n, SsuTensor) for n in ("x", "x_scale", "a", "b", "adapter", "scale", "y")] + [
         ("x_format", ctypes.c_int32)]
 
 
@@ -47,6 +54,11 @@ _lib.ssu_mx_linear_workspace_bytes.restype = ctypes.c_int64
 _lib.ssu_mx_linear.argtypes = [ctypes.POINTER(SsuMxLinearArgs), ctypes.c_void_p, ctypes.c_int64,
                                ctypes.c_void_p]
 _lib.ssu_mx_linear.restype = ctypes.c_int
+_lib.ssu_add_lora_workspace_bytes.argtypes = [ctypes.POINTER(SsuLoraArgs)]
+_lib.ssu_add_lora_workspace_bytes.restype = ctypes.c_int64
+_lib.ssu_add_lora.argtypes = [ctypes.POINTER(SsuLoraArgs), ctypes.c_void_p, ctypes.c_int64,
+                              ctypes.c_void_p]
+_lib.ssu_add_lora.restype = ctypes.c_int
 _lib.ssu_token_logprobs_workspace_bytes.argtypes = [ctypes.POINTER(SsuLogprobArgs)]
 _lib.ssu_token_logprobs_workspace_bytes.restype = ctypes.c_int64
 _lib.ssu_token_logprobs.argtypes = [ctypes.POINTER(SsuLogprobArgs), ctypes.c_void_p, ctypes.c_int64,
@@ -105,6 +117,17 @@ def ssu_mx_linear(args, workspace=None, workspace_bytes=0, stream=None):
     st = _lib.ssu_mx_linear(ctypes.byref(args), workspace, workspace_bytes, _stream(stream))
     if st != OK:
         _raise(st, "ssu_mx_linear")
+
+
+def ssu_add_lora_workspace_bytes(args):
+    return _lib.ssu_add_lora_workspace_bytes(ctypes.byref(args))
+
+
+def ssu_add_lora(args, workspace=None, workspace_bytes=0, stream=None):
+    """Enqueue an addition of low-rank adapters (include/ssu.h ssu_add_lora)."""
+    st = _lib.ssu_add_lora(ctypes.byref(args), workspace, workspace_bytes, _stream(stream))
+    if st != OK:
+        _raise(st, "ssu_add_lora")
 
 
 def ssu_token_logprobs_workspace_bytes(args):
@@ -232,6 +255,33 @@ def mx_linear(x, weight, weight_scale, bias=None, activation="mxfp8", out=None, 
     elif out_dtype is not None and out_dtype != (x.dtype if like is x else torch.bfloat16):
         out = torch.empty(x.shape[:-1] + weight.shape[:1], dtype=out_dtype, device=x.device)
     return _native().mx_linear(x, x_scale, weight, weight_scale, bias, fmt, out, like, _stream_of(x))
+
+
+def make_lora_args(y, x, lora_a, lora_b, adapter, scale=None, x_scale=None, x_format=FORMAT_SAME):
+    """SsuLoraArgs of 2-D x and y."""
+    a = SsuLoraArgs()
+    for name, t in (("x", x), ("x_scale", x_scale), ("a", lora_a), ("b", lora_b), ("adapter", adapter),
+                    ("scale", scale), ("y", y)):
+        if t is not None:
+            setattr(a, name, tensor_desc(t, y.device))
+    a.x_format = x_format
+    return a
+
+
+def add_lora(y, x, lora_a, lora_b, adapter, scale=None):
+    """Adds to every row of y [..., n], the result of a projection of x that all rows share, its request's low-rank
+    adapter: y[r] += scale[i] (x[r] lora_a[i]^T) lora_b[i]^T with i = adapter[r]. Returns y.
+
+    x [..., k] is what the projection took: floats of y's dtype, or (y in bfloat16) a pair (codes, scales) from
+    add_rms_norm or mx_quantize. lora_a [adapters, rank, k] and lora_b [adapters, n, rank] have y's dtype (float32,
+    float16 or bfloat16); rank is at most 128, smaller ones are padded with zeros by the caller or kept in groups of their own.
+    adapter: int32 or int64, one per row, in any order; a row whose number is none of [0, adapters), such as -1, keeps
+    its values. scale: float32 [adapters]. Sums are kept in float32, and y is rounded once more."""
+    x_scale, fmt = None, FORMAT_SAME
+    if isinstance(x, (tuple, list)):
+        x, x_scale = x
+        fmt = FORMAT_MXFP4 if x.shape[-1] * 2 == lora_a.shape[-1] else FORMAT_MXFP8
+    return _native().add_lora(y, x, x_scale, lora_a, lora_b, adapter, scale, fmt, _stream_of(y))
 
 
 TokenLogprobs = collections.namedtuple(

@@ -97,7 +97,10 @@ EXPORTS = ("ssu_plan", "ssu_update", "ssu_replay_update", "ssu_replay_spec_updat
            "ssu_ssd_prefill_noalloc", "ssu_ssd_plan", "ssu_last_error", "ssu_abi_version",
            # bound in layer.py
            "ssu_add_rms_norm", "ssu_mx_quantize", "ssu_mx_linear", "ssu_mx_linear_workspace_bytes",
-           "ssu_token_logprobs", "ssu_token_logprobs_workspace_bytes")
+           "ssu_token_logprobs", "ssu_token_logprobs_workspace_bytes",
+           "ssu_add_lora", "ssu_add_lora_workspace_bytes",
+           # bound in search.py
+           "ssu_beam_select", "ssu_beam_select_workspace_bytes", "ssu_reorder_states")
 SSD_SCRATCH_BYTES = 64 << 20  # SSU_SSD_SCRATCH_BYTES
 
 
