@@ -17,7 +17,6 @@ namespace {
 constexpr int kBeamThreads = 256;
 constexpr int kBeamWaves = kBeamThreads / kWaveLanes;
 constexpr int kTile = kVec * kWaveLanes;  // logits per wave and access
-constexpr int kInFlight = 4;              // accesses in flight per wave
 constexpr float kLog2e = 1.44269504088896341f;
 
 // Largest logit and the sum over it of a share of a row.
@@ -43,32 +42,30 @@ __device__ __forceinline__ bool beam_reads(float score, bool ended) {
     return !ended && score > -__builtin_inff() && score < __builtin_inff();
 }
 
+// One pass over a share of a row. Beside the wave's sum a lane keeps where its best access (eight logits) is, and the largest
+// logits of that and of the second best. At least `keep` logits are not below T, the `keep`-th of the best accesses of the
+// workgroup's 64 groups of four lanes; so after the pass only accesses that reach T are looked at again: a lane's best
+// one, and its others only where the second best reaches T too. Of 16 kept about one lane in three workgroups does.
 template <typename T, bool MASK>
 __global__ __launch_bounds__(kBeamThreads, 4) void beam_scan_kernel(const BeamParams p, const BeamSplit sp) {
+    constexpr int kInFlight = 16 / sizeof(T);  // accesses of a wave: 8 KiB
+    constexpr int kRoom = 512;  // logits that reach T; where there are more, by equal ones, each wave finds its first ones
     __shared__ Share wave_shares[kBeamWaves];
-    __shared__ uint64_t lists[kBeamWaves * Candidates::kList];
+    __shared__ uint32_t heads[kWaveLanes];
+    __shared__ uint64_t list[kRoom];
     __shared__ int listed;
-    __shared__ float floors[kBeamWaves];  // what a wave's `keep`-th token is at least
     const int lane = threadIdx.x % kWaveLanes, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
     const int64_t row = blockIdx.x / sp.segments;
     const int segment = static_cast<int>(blockIdx.x % sp.segments);
     const int64_t request = row / p.beams;
     const int beam = static_cast<int>(row % p.beams);
-    if (!beam_reads(beam_score(p, request, beam), beam_ended(p, request, beam)))
-        return;
-    if (lane == 0)
-        floors[wave] = kLowest;
-    if (threadIdx.x == 0)
-        listed = 0;
-    __syncthreads();
+    const float score = beam_score(p, request, beam);
+    const bool ended = beam_ended(p, request, beam);
     const T *x_row = static_cast<const T *>(p.logits) + row * p.logits_s;
     const uint8_t *mask = MASK ? reinterpret_cast<const uint8_t *>(p.mask + row * p.mask_s) : nullptr;
     const int whole = p.vocab / kTile, tiles = (p.vocab + kTile - 1) / kTile;
     const int first = segment * sp.tiles, end = min(tiles, first + sp.tiles);
     typedef T Raw __attribute__((ext_vector_type(kVec), aligned(sizeof(T))));
-    Share w = {kLowest, 0.0f};
-    Candidates c = {0, 0, kLowest};
-    int done = -1;  // the access whose logits have been offered before the scan
 
     // whole access `t`: its logits, and which of them the mask allows
     auto fetch = [&](int t, Raw *raw, uint32_t *bits) {
@@ -97,113 +94,118 @@ __global__ __launch_bounds__(kBeamThreads, 4) void beam_scan_kernel(const BeamPa
                 x[i] = (bits >> i) & 1 ? x[i] : -__builtin_inff();
         }
     };
-    auto largest = [&](const float x[kVec]) {
-        float a = fmaxf(x[0], x[1]);
-#pragma unroll
-        for (int i = 2; i < kVec; i++)
-            a = fmaxf(a, x[i]);
-        return a;
-    };
+    Share w = {kLowest, 0.0f};  // m: of the wave
+    float m1 = kLowest, m2 = kLowest;
+    int best_at = first + wave;
     auto take = [&](int t, const Raw &raw, uint32_t bits, auto all) {
         float x[kVec];
         values(raw, bits, all, x);
-        const float top = largest(x);
+        float top = fmaxf(x[0], x[1]);
+#pragma unroll
+        for (int i = 2; i < kVec; i++)
+            top = fmaxf(top, x[i]);
         if (__ballot(top > w.m)) {
             const float m = fmaxf(w.m, wave_max(top));
             w.s *= __builtin_amdgcn_exp2f((w.m - m) * kLog2e);
             w.m = m;
         }
+        best_at = top > m1 ? t : best_at;
+        m2 = __builtin_amdgcn_fmed3f(m1, m2, top);
+        m1 = fmaxf(m1, top);
         float s = 0.0f;  // of this access: long chains of additions would lose digits
 #pragma unroll
         for (int i = 0; i < kVec; i++)
             s += __builtin_amdgcn_exp2f((x[i] - w.m) * kLog2e);
         w.s += s;
-        if (t != done && __ballot(top >= c.gate)) {
-            c.offer(x, t * kTile + lane * kVec, p.keep, lane);
-            const uint32_t word = static_cast<uint32_t>(c.floor >> 32);
-            if (word != 0) {
-                const float value = word_value(word);
-                if (lane == 0)
-                    __hip_atomic_store(&floors[wave], value, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                // accesses come in the order of their indices: what only equals a token of
-                // this wave stays behind it from here on (a bound's key has no index)
-                if (static_cast<uint32_t>(c.floor) != 0)
-                    c.gate = fmaxf(c.gate, next_above(value));
-            }
-        }
-    };
-    // the other waves' floors hold for this one too
-    auto read_floors = [&] {
-#pragma unroll
-        for (int i = 0; i < kBeamWaves; i++)
-            c.gate = fmaxf(c.gate, __hip_atomic_load(&floors[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
     };
     const int whole_end = min(end, whole);
     int t = first + wave;
-    bool round = t + (kInFlight - 1) * kBeamWaves < whole_end;
     Raw raw[kInFlight];
     uint32_t bits[kInFlight];
-    auto fetch_round = [&](int from) {
+    auto fetch_round = [&] {
 #pragma unroll
         for (int u = 0; u < kInFlight; u++)
-            fetch(from + u * kBeamWaves, &raw[u], &bits[u]);
+            fetch(t + u * kBeamWaves, &raw[u], &bits[u]);
     };
-    auto fetch_one = [&](int from) {
-        if (from < whole)
-            fetch(from, &raw[0], &bits[0]);
-        else
-            fetch_part(from, &raw[0], &bits[0]);
-    };
+    bool round = t + (kInFlight - 1) * kBeamWaves < whole_end;
     if (round)
-        fetch_round(t);
-    else if (t < end)
-        fetch_one(t);
-    if (t < end) {
-        float best = -__builtin_inff();
-#pragma unroll
-        for (int u = 0; u < kInFlight; u++) {
-            if (u > 0 && !round)
-                break;
-            float x[kVec];
-            values(raw[u], bits[u], std::false_type(), x);
-            best = fmaxf(best, largest(x));
-        }
-        c.bound(best, p.keep);
-        float x[kVec];
-        values(raw[0], bits[0], std::false_type(), x);
-        if (c.first(x, t * kTile + lane * kVec, p.keep, lane, lists + wave * Candidates::kList)) {
-            done = t;
-            if (c.floor != 0 && lane == 0)
-                __hip_atomic_store(&floors[wave], word_value(static_cast<uint32_t>(c.floor >> 32)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        }
-    }
+        fetch_round();
+    if (!beam_reads(score, ended))
+        return;
     while (round) {
-        read_floors();
 #pragma unroll
         for (int u = 0; u < kInFlight; u++)
             take(t + u * kBeamWaves, raw[u], bits[u], std::bool_constant<!MASK>());
         t += kInFlight * kBeamWaves;
         round = t + (kInFlight - 1) * kBeamWaves < whole_end;
         if (round)
-            fetch_round(t);
-        else if (t < end)
-            fetch_one(t);
+            fetch_round();
     }
-    while (t < end) {
-        read_floors();
+    for (; t < end; t += kBeamWaves) {
+        fetch_part(t, &raw[0], &bits[0]);
         take(t, raw[0], bits[0], std::false_type());
-        t += kBeamWaves;
-        if (t < end)
-            fetch_one(t);
     }
 
-    // the workgroup's sum and list
+    // T, and the workgroup's sum
     w.s = wave_sum(w.s);
     if (lane == 0)
         wave_shares[wave] = w;
+    const float four = group_max<4>(m1);
+    if (lane % 4 == 0)
+        heads[wave * 16 + lane / 4] = order_word(four);
+    if (threadIdx.x == 0)
+        listed = 0;
     __syncthreads();
-    if (lane < p.keep && c.key != 0)
-        lists[atomicAdd(&listed, 1)] = c.key;
+    // the `keep`-th largest but for its last ten bits, which are 0, found bit by bit
+    const uint32_t head = heads[lane];
+    uint32_t lowest = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 10; bit--) {
+        const uint32_t t = lowest | (1u << bit);
+        if (__popcll(__ballot(head >= t)) >= p.keep)
+            lowest = t;
+    }
+    const float bound = fmaxf(word_value(lowest), kLowest);
+    // the lane's logits of an access that reach T, to the list
+    auto append = [&](int t, const Raw &raw, uint32_t bits) {
+        float x[kVec];
+        values(raw, bits, std::false_type(), x);
+        uint32_t pass = 0;
+#pragma unroll
+        for (int i = 0; i < kVec; i++)
+            pass |= x[i] >= bound && x[i] < __builtin_inff() ? 1u << i : 0;
+        if (pass == 0)
+            return;
+        int to = atomicAdd(&listed, static_cast<int>(__popc(pass)));
+#pragma unroll
+        for (int i = 0; i < kVec; i++)
+            if ((pass >> i) & 1) {
+                if (to < kRoom)
+                    list[to] = order_key(order_word(x[i]), t * kTile + lane * kVec + i);
+                to++;
+            }
+    };
+    if (m1 >= bound && m1 > kLowest) {
+        fetch_part(best_at, &raw[0], &bits[0]);
+        append(best_at, raw[0], bits[0]);
+    }
+    const bool more = m2 >= bound && m2 > kLowest;
+    if (__ballot(more)) {
+        t = first + wave;
+        for (; t + (kInFlight - 1) * kBeamWaves < whole_end; t += kInFlight * kBeamWaves)
+            if (more) {
+                fetch_round();
+#pragma unroll
+                for (int u = 0; u < kInFlight; u++)
+                    if (t + u * kBeamWaves != best_at)
+                        append(t + u * kBeamWaves, raw[u], bits[u]);
+            }
+        for (; t < end; t += kBeamWaves)
+            if (more && t != best_at) {
+                fetch_part(t, &raw[0], &bits[0]);
+                append(t, raw[0], bits[0]);
+            }
+    }
     __syncthreads();
     const int64_t share = row * sp.segments + segment;
     if (threadIdx.x == 0) {
@@ -216,86 +218,145 @@ __global__ __launch_bounds__(kBeamThreads, 4) void beam_scan_kernel(const BeamPa
             r.s += wave_shares[i].s * __builtin_amdgcn_exp2f((wave_shares[i].m - r.m) * kLog2e);
         sp.shares[share] = r;
     }
-    const int n = listed;
+    int n = listed;
+    if (n > kRoom) {
+        __syncthreads();
+        if (threadIdx.x == 0)
+            listed = 0;
+        __syncthreads();
+        Candidates c = {0, static_cast<uint64_t>(order_word(bound)) << 32, bound};
+        for (t = first + wave; t < end; t += kBeamWaves) {
+            fetch_part(t, &raw[0], &bits[0]);
+            float x[kVec];
+            values(raw[0], bits[0], std::false_type(), x);
+            c.offer(x, t * kTile + lane * kVec, p.keep, lane);
+        }
+        if (lane < p.keep && c.key != 0)
+            list[atomicAdd(&listed, 1)] = c.key;
+        __syncthreads();
+        n = listed;
+    }
     for (int i = threadIdx.x; i < n; i += kBeamThreads) {
-        const uint64_t key = lists[i];
+        const uint64_t key = list[i];
         int at = 0;
-        for (int j = 0; j < n; j++)
-            at += lists[j] > key;
+        int j = 0;
+        for (; j + 8 <= n; j += 8)
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+                at += list[j + q] > key;
+        for (; j < n; j++)
+            at += list[j] > key;
         if (at < p.keep)
             sp.keys[share * p.keep + at] = key;
     }
-    for (int i = n + static_cast<int>(threadIdx.x); i < p.keep; i += kBeamThreads)
-        sp.keys[share * p.keep + i] = 0;
+    if (static_cast<int>(threadIdx.x) >= n && static_cast<int>(threadIdx.x) < p.keep)
+        sp.keys[share * p.keep + threadIdx.x] = 0;
 }
 
 // ---------------------------------------------------------------- the join
 
-// A continuation; beams in the order of their numbers, a beam's tokens in that of their keys.
-struct Continuation {
-    double c;
-    uint64_t key;  // its logit's (1: an ended beam's only one; 0: none)
-    int32_t beam;
-};
-__device__ __forceinline__ bool before(const Continuation &a, const Continuation &b) {
-    return a.c > b.c || (a.c == b.c && (a.beam < b.beam || (a.beam == b.beam && a.key > b.key)));
-}
-
 constexpr int kMostSegments = 64;
-// Fewer rows than compute units are split, into two workgroups for each.
-constexpr int kSplitBelow = 256, kSplitTo = 512;
-// Lists of a request: with its rows alone below kSplitBelow it has kSplitTo + 1 for each beam at most, and a sample of them
-// less than `keep` more.
-constexpr int kMostSample = kSplitTo + SSU_BEAMS_MAX + SSU_TOP_MAX;
+constexpr int kMostLists = 512;  // of a request
+// Its sample: one of each list, and less than `keep` more where they are few; or about 64.
+constexpr int kMostSample = kMostLists + SSU_TOP_MAX;
 // The sample's `keep`-th stands behind the heads of at most `keep` lists, or of all if there are fewer.
 constexpr int kMostChosen = SSU_TOP_MAX * SSU_TOP_MAX;
 
+// A continuation's place in the order, as whole numbers: larger scores first; equal ones by beam, a beam's by their
+// logits, equal logits by their places in the beam's lists, which are in the order of the tokens.
+struct Place {
+    uint64_t score;  // 0: none
+    uint64_t rest;
+};
+__device__ __forceinline__ bool before(const Place &a, const Place &b) {
+    return a.score > b.score || (a.score == b.score && a.rest > b.rest);
+}
+__device__ __forceinline__ uint64_t score_word(double c) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(c + 0.0));  // -0 and 0 are equal
+    return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double word_score(uint64_t w) {
+    return __longlong_as_double(static_cast<long long>(w >> 63 ? w & 0x7FFFFFFFFFFFFFFFull : ~w));
+}
+constexpr int kListBits = 11, kWordBits = 32;
+static_assert(kMostSegments * SSU_TOP_MAX <= 1 << kListBits, "places in a beam's lists");
+__device__ __forceinline__ uint64_t rest_word(int beam, uint32_t word, int at) {
+    return (static_cast<uint64_t>(SSU_BEAMS_MAX - 1 - beam) << (kWordBits + kListBits)) | (static_cast<uint64_t>(word) << kListBits) |
+           static_cast<uint64_t>((1 << kListBits) - 1 - at);
+}
+__device__ __forceinline__ int rest_beam(uint64_t rest) { return SSU_BEAMS_MAX - 1 - static_cast<int>(rest >> (kWordBits + kListBits)); }
+
+// How many of places[0 .. n) stand before `mine`.
+__device__ __forceinline__ int number_before(const Place *places, int n, const Place &mine) {
+    int at = 0, j = 0;
+    for (; j + 8 <= n; j += 8) {
+        Place o[8];
+#pragma unroll
+        for (int q = 0; q < 8; q++)
+            o[q] = places[j + q];
+#pragma unroll
+        for (int q = 0; q < 8; q++)
+            at += before(o[q], mine);
+    }
+    for (; j < n; j++)
+        at += before(places[j], mine);
+    return at;
+}
+
 __global__ __launch_bounds__(kBeamThreads) void beam_join_kernel(const BeamParams p, const BeamSplit sp) {
-    __shared__ double bias[SSU_BEAMS_MAX];  // score - log of the sum over the largest logit
-    __shared__ float peak[SSU_BEAMS_MAX];   // that logit
-    __shared__ uint8_t kind[SSU_BEAMS_MAX]; // 0: no candidates, 1: its logits', 2: ended
-    __shared__ Continuation sample[kMostSample];
-    __shared__ Continuation chosen[kMostChosen];
-    __shared__ Continuation floor;
+    constexpr int kSamples = (kMostSample + kBeamThreads - 1) / kBeamThreads;
+    __shared__ double bias[SSU_BEAMS_MAX];   // score - log of the sum over the largest logit
+    __shared__ float peak[SSU_BEAMS_MAX];    // that logit
+    __shared__ uint8_t kind[SSU_BEAMS_MAX];  // 0: no candidates, 1: its logits', 2: ended
+    __shared__ alignas(16) Place sample[kMostSample];
+    __shared__ alignas(16) Place chosen[kMostChosen];
+    __shared__ int32_t tokens[kMostChosen];
+    __shared__ Place floor;
     __shared__ int bad, count;
-    const int lane = threadIdx.x % kWaveLanes, wave = threadIdx.x / kWaveLanes;
+    const int lane = threadIdx.x % kWaveLanes;
     const int64_t request = blockIdx.x;
     const int64_t row0 = request * p.beams;
-    const Continuation none = {-__builtin_inf(), 0, INT32_MAX};
+    const int lists = p.beams * sp.segments;
+    // a sample of every list's first ones, some 64 of them where the lists are few
+    const int each = max((p.keep + lists - 1) / lists, min(p.keep, kWaveLanes / lists)), samples = lists * each;
+    const uint64_t *keys = sp.keys + row0 * sp.segments * p.keep;
+    // they are on their way while the beams' sums are joined; of beams that are not read they are anything
+    uint64_t head[kSamples];
+#pragma unroll
+    for (int u = 0; u < kSamples; u++) {
+        const int i = u * kBeamThreads + threadIdx.x;
+        head[u] = i < samples ? keys[i / each * p.keep + i % each] : 0;
+    }
     if (threadIdx.x == 0) {
         bad = 0;
         count = 0;
-        floor = none;
+        floor = {0, 0};
     }
     __syncthreads();
-    for (int i = wave; i < p.beams; i += kBeamWaves) {
-        const float score = beam_score(p, request, i);
-        const bool ended = beam_ended(p, request, i), reads = beam_reads(score, ended);
-        if (!reads) {
-            if (lane == 0) {
-                if (!(score < __builtin_inff()))
-                    bad = 1;
-                kind[i] = ended && score > -__builtin_inff() ? 2 : 0;
-                bias[i] = score;
-            }
-            continue;
-        }
-        Share s = {kLowest, 0.0f};
-        if (lane < sp.segments)
-            s = sp.shares[(row0 + i) * sp.segments + lane];
+    // as many lanes for each beam as a power of two holds its shares
+    int width = 1;
+    while (width < sp.segments)
+        width *= 2;
+    for (int i0 = 0; i0 < p.beams; i0 += kBeamThreads / width) {
+        const int i = i0 + static_cast<int>(threadIdx.x) / width, j = lane % width;
+        const bool live = i < p.beams;
+        // all three are asked for at once; a share of a beam that is not read is anything
+        Share s = sp.shares[(row0 + min(i, p.beams - 1)) * sp.segments + min(j, sp.segments - 1)];
+        const float score = beam_score(p, request, min(i, p.beams - 1));
+        const bool ended = beam_ended(p, request, min(i, p.beams - 1)), reads = beam_reads(score, ended);
+        if (!reads || j >= sp.segments)
+            s = {kLowest, 0.0f};
         float m = s.m;
-#pragma unroll
-        for (int d = 1; d < kWaveLanes; d *= 2)
+        for (int d = 1; d < width; d *= 2)
             m = fmaxf(m, __shfl_xor(m, d));
         double sum = static_cast<double>(s.s) * __builtin_amdgcn_exp2f((s.m - m) * kLog2e);
-#pragma unroll
-        for (int d = 1; d < kWaveLanes; d *= 2)
+        for (int d = 1; d < width; d *= 2)
             sum += __shfl_xor(sum, d);
-        if (lane == 0) {
-            if (sum != sum)
+        if (live && j == 0) {
+            if (!(score < __builtin_inff()) || sum != sum)
                 bad = 1;
-            kind[i] = sum > 0.0 ? 1 : 0;
-            bias[i] = sum > 0.0 ? static_cast<double>(score) - log(sum) : 0.0;
+            kind[i] = reads ? (sum > 0.0 ? 1 : 0) : ended && score > -__builtin_inff() ? 2 : 0;
+            bias[i] = reads && sum > 0.0 ? static_cast<double>(score) - log(sum) : score;
             peak[i] = m;
         }
     }
@@ -310,55 +371,58 @@ __global__ __launch_bounds__(kBeamThreads) void beam_join_kernel(const BeamParam
         }
         return;
     }
-    // place `at` of list `list` (a share of a row)
-    auto continuation = [&](int list, int at) {
-        const int beam = list / sp.segments, segment = list % sp.segments;
-        Continuation r = none;
-        if (kind[beam] == 1) {
-            const uint64_t key = sp.keys[(row0 * sp.segments + list) * p.keep + at];
-            if (key != 0)
-                r = {bias[beam] + (static_cast<double>(key_value(key)) - peak[beam]), key, beam};
-        } else if (kind[beam] == 2 && segment == 0 && at == 0) {
-            r = {bias[beam], 1, beam};
+    // place `at` of list `list` (a share of a row), which holds `key`
+    auto continuation = [&](int list, int at, uint64_t key) {
+        const int beam = list / sp.segments, segment = list - beam * sp.segments;
+        if (kind[beam] == 1 && key != 0) {
+            const double c = bias[beam] + (static_cast<double>(key_value(key)) - peak[beam]);
+            return Place{score_word(c), rest_word(beam, static_cast<uint32_t>(key >> 32), segment * p.keep + at)};
         }
-        return r;
+        if (kind[beam] == 2 && segment == 0 && at == 0)
+            return Place{score_word(bias[beam]), rest_word(beam, 0, 0)};
+        return Place{0, 0};
     };
-    // the `keep`-th of a sample, of every list's first ones: no continuation behind it is chosen
-    const int lists = p.beams * sp.segments;
-    const int each = min(p.keep, (p.keep + lists - 1) / lists);
-    for (int i = threadIdx.x; i < lists * each; i += kBeamThreads)
-        sample[i] = continuation(i / each, i % each);
-    __syncthreads();
-    for (int i = threadIdx.x; i < lists * each; i += kBeamThreads) {
-        const Continuation mine = sample[i];
-        if (mine.key == 0)
-            continue;
-        int at = 0;
-        for (int j = 0; j < lists * each; j++)
-            at += before(sample[j], mine);
-        if (at == p.keep - 1)
-            floor = mine;
+    // the `keep`-th of the sample: no continuation behind it is chosen
+    Place mine[kSamples];
+#pragma unroll
+    for (int u = 0; u < kSamples; u++) {
+        const int i = u * kBeamThreads + threadIdx.x;
+        if (i < samples) {
+            mine[u] = continuation(i / each, i % each, head[u]);
+            sample[i] = mine[u];
+        }
     }
     __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kSamples; u++) {
+        const int i = u * kBeamThreads + threadIdx.x;
+        if (i < samples && mine[u].score != 0 && number_before(sample, samples, mine[u]) == p.keep - 1)
+            floor = mine[u];
+    }
+    __syncthreads();
+    const Place last = floor;
     for (int i = threadIdx.x; i < lists * p.keep; i += kBeamThreads) {
         const int list = i / p.keep;
-        if (floor.key != 0 && before(floor, sample[list * each]))
-            continue;  // its first one stands behind the floor
-        const Continuation mine = continuation(list, i % p.keep);
-        if (mine.key != 0 && (floor.key == 0 || !before(floor, mine)))
-            chosen[atomicAdd(&count, 1)] = mine;
+        const Place first = sample[list * each];
+        if (first.score == 0 || before(last, first))
+            continue;  // nothing of it, or its first one stands behind the last that is chosen
+        const uint64_t key = keys[i];
+        const Place c = continuation(list, i - list * p.keep, key);
+        if (c.score != 0 && !before(last, c)) {
+            const int to = atomicAdd(&count, 1);
+            chosen[to] = c;
+            tokens[to] = kind[rest_beam(c.rest)] == 2 ? p.end_token : key_index(key);
+        }
     }
     __syncthreads();
     const int n = count;
     for (int i = threadIdx.x; i < n; i += kBeamThreads) {
-        const Continuation mine = chosen[i];
-        int at = 0;
-        for (int j = 0; j < n; j++)
-            at += before(chosen[j], mine);
+        const Place c = chosen[i];
+        const int at = number_before(chosen, n, c);
         if (at < p.keep) {
-            out_scores[at] = static_cast<float>(mine.c);
-            out_parents[at] = mine.beam;
-            out_tokens[at] = kind[mine.beam] == 2 ? p.end_token : key_index(mine.key);
+            out_scores[at] = static_cast<float>(word_score(c.score));
+            out_parents[at] = rest_beam(c.rest);
+            out_tokens[at] = tokens[i];
         }
     }
     for (int i = n + static_cast<int>(threadIdx.x); i < p.keep; i += kBeamThreads) {
@@ -368,11 +432,13 @@ __global__ __launch_bounds__(kBeamThreads) void beam_join_kernel(const BeamParam
     }
 }
 
-// Shares of a row and accesses per share: each has one for every wave.
-void split(int64_t rows, int64_t vocab, int32_t *segments, int32_t *per) {
+// Shares of a row and accesses per share.
+constexpr int64_t kGroups = 4096, kFewGroups = 512, kLeastTiles = 32;
+void split(int64_t rows, int64_t beams, int64_t vocab, int32_t *segments, int32_t *per) {
     const int64_t tiles = (vocab + kTile - 1) / kTile;
-    int64_t s = rows < kSplitBelow ? (kSplitTo + rows - 1) / rows : 1;
-    s = std::min<int64_t>({s, kMostSegments, std::max<int64_t>(1, tiles / kBeamWaves)});
+    int64_t s = std::min((kGroups + rows - 1) / rows, tiles / kLeastTiles);
+    s = std::max(s, std::min((kFewGroups + rows - 1) / rows, tiles / kBeamWaves));
+    s = std::max<int64_t>(1, std::min<int64_t>({s, kMostSegments, kMostLists / beams}));
     *per = static_cast<int32_t>(std::max<int64_t>(1, (tiles + s - 1) / s));
     *segments = static_cast<int32_t>(std::max<int64_t>(1, (tiles + *per - 1) / *per));
 }
@@ -386,16 +452,16 @@ const void *scan_fn(bool mask) {
 
 }  // namespace
 
-int64_t beam_workspace(int64_t rows, int64_t vocab, int64_t keep) {
+int64_t beam_workspace(int64_t rows, int64_t beams, int64_t vocab, int64_t keep) {
     int32_t s, per;
-    split(rows, vocab, &s, &per);
+    split(rows, beams, vocab, &s, &per);
     return share_bytes(rows * s) + rows * s * keep * 8;
 }
 
 int launch_beam_select(const BeamParams &p, int dtype, void *stream) {
     BeamSplit sp = {};
     const int64_t rows = p.batch * p.beams;
-    split(rows, p.vocab, &sp.segments, &sp.tiles);
+    split(rows, p.beams, p.vocab, &sp.segments, &sp.tiles);
     sp.shares = reinterpret_cast<Share *>(p.workspace);
     sp.keys = reinterpret_cast<uint64_t *>(p.workspace + share_bytes(rows * sp.segments));
     const void *fn = dtype == SSU_F32   ? scan_fn<float>(p.mask != nullptr)
