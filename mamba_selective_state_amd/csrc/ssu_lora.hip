@@ -115,20 +115,34 @@ __device__ __forceinline__ int draw_number(int *counter, int id, int lane) {
     return id >= 0 ? atomicAdd(&counter[id], 1) : 0;
 }
 
-// By one workgroup of THREADS; `hist`: `adapters` counters in LDS. The order of an adapter's rows may differ from call to call;
-// a row's result does not depend on it.
-template <int THREADS>
+// By one workgroup of THREADS, PER rows for each thread at a time; `hist`: `adapters` counters in LDS. The order of an adapter's
+// rows may differ from call to call; a row's result does not depend on it.
+template <int THREADS, int PER>
 __device__ void make_plan(const LoraParams &p, const LoraPlan &plan, int *hist) {
     constexpr int kWaves = THREADS / kWaveLanes;
     __shared__ int sums[3][kWaves];
     const int t = threadIdx.x, lane = t % kWaveLanes, wave = t / kWaveLanes;
+    int id[PER], number[PER];
+    auto load_ids = [&](int64_t base) {
+#pragma unroll
+        for (int u = 0; u < PER; u++) {
+            const int64_t row = base + u * THREADS + t;
+            id[u] = row < p.rows ? adapter_of(p, static_cast<int>(row)) : -1;
+        }
+    };
+    load_ids(0);
     for (int i = t; i < p.adapters; i += THREADS)
         hist[i] = 0;
     __syncthreads();
-    const int rounds = (p.rows + THREADS - 1) / THREADS;
-    for (int i = 0; i < rounds; i++) {
-        const int row = i * THREADS + t;
-        draw_number(hist, row < p.rows ? adapter_of(p, row) : -1, lane);
+    constexpr int64_t kBatch = static_cast<int64_t>(THREADS) * PER;
+    for (int64_t base = 0;;) {
+#pragma unroll
+        for (int u = 0; u < PER; u++)
+            number[u] = draw_number(hist, id[u], lane);
+        base += kBatch;
+        if (base >= p.rows)
+            break;
+        load_ids(base);
     }
     __syncthreads();
     // a run of adapters for each thread: rows, up tiles and down tiles before it
@@ -172,19 +186,28 @@ __device__ void make_plan(const LoraParams &p, const LoraPlan &plan, int *hist) 
         at[0] += n;
     }
     __syncthreads();
-    for (int i = 0; i < rounds; i++) {
-        const int row = i * THREADS + t;
-        const int id = row < p.rows ? adapter_of(p, row) : -1;
-        const int to = draw_number(hist, id, lane);
-        if (id >= 0)
-            plan.perm[to] = row;
+    if (p.rows <= kBatch) {  // the first rows' numbers are still known
+#pragma unroll
+        for (int u = 0; u < PER; u++)
+            if (id[u] >= 0)
+                plan.perm[hist[id[u]] + number[u]] = u * THREADS + t;
+        return;
+    }
+    for (int64_t base = 0; base < p.rows; base += kBatch) {
+        load_ids(base);
+#pragma unroll
+        for (int u = 0; u < PER; u++) {
+            const int to = draw_number(hist, id[u], lane);
+            if (id[u] >= 0)
+                plan.perm[to] = static_cast<int32_t>(base + u * THREADS + t);
+        }
     }
 }
 
 constexpr int kPlanThreads = 1024;
 __global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const LoraParams p, const LoraPlan plan) {
     extern __shared__ int dynamic[];
-    make_plan<kPlanThreads>(p, plan, dynamic);
+    make_plan<kPlanThreads, 8>(p, plan, dynamic);
 }
 
 // ---------------------------------------------------------------- down
@@ -192,62 +215,86 @@ __global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const LoraParam
 constexpr int kDownThreads = 512;
 constexpr int kDownWaves = kDownThreads / kWaveLanes;
 
+// A step is 64 values of k: lane group g's 16 are 16 g .. 16 g + 15, in two operands, of both sides. Four lanes read 128 bytes of
+// a row in a row.
+template <typename T>
+struct Step {
+    Frag<T> f[2];
+};
+template <typename T>
+__device__ __forceinline__ Step<T> load_step(const T *p) {
+    return {{load_frag(p), load_frag(p + 8)}};
+}
+template <typename T>
+__device__ __forceinline__ Step<T> load_step(const T *p, int n) {
+    return {{load_frag(p, n), load_frag(p + 8, n - 8)}};
+}
+
 // Rows of x as operands of type T.
 template <typename T, typename SRC>
 struct XRow {
     const SRC *row;
     __device__ __forceinline__ XRow(const LoraParams &p, int64_t r) : row(static_cast<const SRC *>(p.x) + r * p.x_s) {}
-    __device__ __forceinline__ Frag<T> load(int at, int n) const { return load_frag<T>(row + at, n); }
-    __device__ __forceinline__ Frag<T> load(int at) const { return load_frag<T>(row + at); }
+    __device__ __forceinline__ Step<T> load(int at) const { return load_step<T>(row + at); }
+    __device__ __forceinline__ Step<T> load(int at, int n) const { return load_step<T>(row + at, n); }
 };
-// Codes: exact in bf16, which has their four bits and, but for its ends, their scales' range.
+// Codes: exact in bf16, which has their four bits and, but for its ends, their scales' range. A lane's 16
+// lie in one block of 32.
 template <>
 struct XRow<__bf16, Mx8> {
     const uint8_t *codes, *scales;
     __device__ __forceinline__ XRow(const LoraParams &p, int64_t r)
         : codes(static_cast<const uint8_t *>(p.x) + r * p.x_s), scales(p.x_scale + r * p.xs_s) {}
-    __device__ __forceinline__ Frag<__bf16> load(int at) const {
-        typedef u32x2 Any2 __attribute__((aligned(1)));
-        const u32x2 c = *reinterpret_cast<const Any2 *>(codes + at);
+    __device__ __forceinline__ Step<__bf16> load(int at) const {
+        typedef u32x4 Any4 __attribute__((aligned(1)));
+        const u32x4 c = *reinterpret_cast<const Any4 *>(codes + at);
         const uint32_t s = scales[at / 32];
         const float scale = mx8_scale(s);
-        Frag<__bf16> f;
+        Step<__bf16> r;
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < 4; i++) {
             const float2 lo = e4m3_pair<false>(c[i], scale), hi = e4m3_pair<true>(c[i], scale);
             const float v[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
             for (int j = 0; j < 4; j++)
-                f.v[4 * i + j] = narrow<__bf16>(s == 255 ? __builtin_nanf("") : v[j]);
+                r.f[i / 2].v[4 * (i % 2) + j] = narrow<__bf16>(s == 255 ? __builtin_nanf("") : v[j]);
         }
-        return f;
+        return r;
     }
-    __device__ __forceinline__ Frag<__bf16> load(int at, int n) const { return n > 0 ? load(at) : zero_frag<__bf16>(); }
+    __device__ __forceinline__ Step<__bf16> load(int at, int n) const {
+        return n > 0 ? load(at) : Step<__bf16>{{zero_frag<__bf16>(), zero_frag<__bf16>()}};
+    }
 };
 template <>
 struct XRow<__bf16, Mx4> {
     const uint8_t *codes, *scales;
     __device__ __forceinline__ XRow(const LoraParams &p, int64_t r)
         : codes(static_cast<const uint8_t *>(p.x) + r * p.x_s), scales(p.x_scale + r * p.xs_s) {}
-    __device__ __forceinline__ Frag<__bf16> load(int at) const {
-        typedef uint32_t Any1 __attribute__((aligned(1)));
-        const uint32_t c = *reinterpret_cast<const Any1 *>(codes + at / 2);
+    __device__ __forceinline__ Step<__bf16> load(int at) const {
+        typedef u32x2 Any2 __attribute__((aligned(1)));
+        const u32x2 c = *reinterpret_cast<const Any2 *>(codes + at / 2);
         const uint32_t s = scales[at / 32];
         const float scale = mx8_scale(s);
-        const float2 v[4] = {e2m1_pair<0>(c, scale), e2m1_pair<1>(c, scale), e2m1_pair<2>(c, scale), e2m1_pair<3>(c, scale)};
-        Frag<__bf16> f;
+        Step<__bf16> r;
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            f.v[2 * j] = narrow<__bf16>(s == 255 ? __builtin_nanf("") : v[j].x);
-            f.v[2 * j + 1] = narrow<__bf16>(s == 255 ? __builtin_nanf("") : v[j].y);
+        for (int i = 0; i < 2; i++) {
+            const float2 v[4] = {e2m1_pair<0>(c[i], scale), e2m1_pair<1>(c[i], scale), e2m1_pair<2>(c[i], scale), e2m1_pair<3>(c[i], scale)};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                r.f[i].v[2 * j] = narrow<__bf16>(s == 255 ? __builtin_nanf("") : v[j].x);
+                r.f[i].v[2 * j + 1] = narrow<__bf16>(s == 255 ? __builtin_nanf("") : v[j].y);
+            }
         }
-        return f;
+        return r;
     }
-    __device__ __forceinline__ Frag<__bf16> load(int at, int n) const { return n > 0 ? load(at) : zero_frag<__bf16>(); }
+    __device__ __forceinline__ Step<__bf16> load(int at, int n) const {
+        return n > 0 ? load(at) : Step<__bf16>{{zero_frag<__bf16>(), zero_frag<__bf16>()}};
+    }
 };
 
-// h of up to 16 XF rows of one adapter over values [begin, end) of k. `row_of`(i): the i-th row. The waves take
-// turns at steps of 32 and join their sums in LDS, in a fixed order.
+// h of up to 16 XF rows of one adapter over values [begin, end) of k. `row_of`(i): the i-th row. Each wave has a run of
+// k for itself (in step they would all ask for the same 512 bytes of rows a power of two apart, which the same few channels
+// hold), and their sums are joined in LDS, in a fixed order.
 template <typename T, typename SRC, int RF, int XF, typename F>
 __device__ __forceinline__ void down_tile(const LoraParams &p, int adapter, int count, int begin, int end, float *h, f32x4 *sums, F &&row_of) {
     constexpr int kGroup = 4;  // fragments joined at a time
@@ -261,7 +308,7 @@ __device__ __forceinline__ void down_tile(const LoraParams &p, int adapter, int 
     const XRow<T, SRC> x1(p, XF > 1 ? row_of(min(16 + r, count - 1)) : 0);
     f32x4 acc[XF][RF] = {};
     auto step = [&](auto load_x, auto load_a) {
-        Frag<T> x[XF], w[RF];
+        Step<T> x[XF], w[RF];
         x[0] = load_x(x0);
         if constexpr (XF > 1)
             x[1] = load_x(x1);
@@ -269,18 +316,22 @@ __device__ __forceinline__ void down_tile(const LoraParams &p, int adapter, int 
         for (int f = 0; f < RF; f++)
             w[f] = load_a(a[f]);
 #pragma unroll
-        for (int i = 0; i < XF; i++)
+        for (int j = 0; j < 2; j++)
 #pragma unroll
-            for (int f = 0; f < RF; f++)
-                acc[i][f] = mma(w[f], x[i], acc[i][f]);
+            for (int i = 0; i < XF; i++)
+#pragma unroll
+                for (int f = 0; f < RF; f++)
+                    acc[i][f] = mma(w[f].f[j], x[i].f[j], acc[i][f]);
     };
-    int at = begin + wave * 32;
+    const int per = ((end - begin + kDownWaves - 1) / kDownWaves + 63) / 64 * 64;
+    int at = begin + wave * per;
+    end = min(end, at + per);
 #pragma unroll 2
-    for (; at + 32 <= end; at += kDownWaves * 32)
-        step([&](const XRow<T, SRC> &x) { return x.load(at + 8 * g); }, [&](const T *w) { return load_frag(w + at + 8 * g); });
+    for (; at + 64 <= end; at += 64)
+        step([&](const XRow<T, SRC> &x) { return x.load(at + 16 * g); }, [&](const T *w) { return load_step(w + at + 16 * g); });
     if (at < end) {
-        const int n = end - at - 8 * g;
-        step([&](const XRow<T, SRC> &x) { return x.load(at + 8 * g, n); }, [&](const T *w) { return load_frag(w + at + 8 * g, n); });
+        const int n = end - at - 16 * g;
+        step([&](const XRow<T, SRC> &x) { return x.load(at + 16 * g, n); }, [&](const T *w) { return load_step(w + at + 16 * g, n); });
     }
     constexpr int kFrags = XF * RF;
 #pragma unroll
@@ -305,7 +356,8 @@ __device__ __forceinline__ void down_tile(const LoraParams &p, int adapter, int 
 }
 
 // SELF: a workgroup for each (adapter or leading row, slice of k) looks its rows up, the first workgroup makes the plan.
-template <typename T, typename SRC, int RF, bool SELF>
+// XF: operands of 16 rows at a time.
+template <typename T, typename SRC, int RF, int XF, bool SELF>
 __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(const LoraParams p, const LoraPlan plan) {
     extern __shared__ int dynamic[];
     __shared__ f32x4 sums[kDownWaves * 4 * 64];
@@ -314,7 +366,7 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(const LoraParam
     int id = static_cast<int>(blockIdx.x);
     if constexpr (SELF) {
         if (id == 0) {
-            make_plan<kDownThreads>(p, plan, dynamic);
+            make_plan<kDownThreads, kSelfRows / kDownThreads>(p, plan, dynamic);
             return;
         }
         id--;
@@ -350,14 +402,14 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(const LoraParam
         if (__syncthreads_or(earlier))
             return;
         const int n = found;
-        for (int i = 0; i < n; i += 16)
-            down_tile<T, SRC, RF, 1>(p, adapter, min(16, n - i), begin, end, h, sums, [&](int j) { return mine[i + j]; });
+        for (int i = 0; i < n; i += 16 * XF)
+            down_tile<T, SRC, RF, XF>(p, adapter, min(16 * XF, n - i), begin, end, h, sums, [&](int j) { return mine[i + j]; });
     } else {
         const int tile = id / p.slices;
         if (tile >= plan.counts[1])
             return;
         const Tile t = plan.down[tile];
-        down_tile<T, SRC, RF, kDownRows / 16>(p, t.adapter, t.count, begin, end, h, sums, [&](int j) { return plan.perm[t.first + j]; });
+        down_tile<T, SRC, RF, XF>(p, t.adapter, t.count, begin, end, h, sums, [&](int j) { return plan.perm[t.first + j]; });
     }
 }
 
@@ -367,7 +419,7 @@ constexpr int kUpThreads = 256;
 constexpr int kUpWaves = kUpThreads / kWaveLanes;
 constexpr int kUpCols = 64;  // of a wave
 
-// Eight f32 as one operand, or as two whose sum they are to twice its digits.
+// A value as two summands of T.
 template <typename T>
 __device__ __forceinline__ void split_value(float v, T *hi, T *lo) {
     *hi = narrow<T>(v);
@@ -375,121 +427,196 @@ __device__ __forceinline__ void split_value(float v, T *hi, T *lo) {
     *lo = narrow<T>(fabsf(w) < __builtin_inff() ? v - w : 0.0f);
 }
 
+// Tile and block of columns of item `i`: each XCD has a run of items, in groups of eight blocks of columns whose weights stay
+// in its L2 while it goes through the tiles.
+__device__ __forceinline__ void item_at(int64_t i, int64_t tiles, int blocks, int64_t *tile, int *block) {
+    const int64_t group = i / (8 * tiles), in = i - group * 8 * tiles;
+    const int width = min(8, blocks - static_cast<int>(group) * 8);
+    *tile = in / width;
+    *block = static_cast<int>(group * 8 + in % width);
+}
+
+// A tile of rows times four waves' columns. Every wave fetches its columns' weights row by row and takes them to
+// registers through LDS; h of the tile is joined over the slices of k, scaled, split and left in LDS; then the waves go through the
+// rows, 16 at a time.
+//
+// Here h's rows go first and the weights second: lane l has results of rows 4 (l / 16) .. + 3, and fragment f's column l % 16 is
+// output 4 (l % 16) + f of the wave's, so that 16 lanes in a row have 64 outputs in a row of one row of y.
 template <typename T, int R>
 __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(const LoraParams p, const LoraPlan plan) {
+    constexpr int N = 4;                     // outputs of a lane and row
     constexpr int KB = R < 32 ? 1 : R / 32;  // operands of 32 along the rank
     constexpr bool kSplit = sizeof(T) == 2;
-    constexpr bool kBoth = kSplit && R == 16;  // hi and lo fill one operand
+    constexpr bool kBoth = kSplit && R == 16;                    // hi and lo fill one operand
+    constexpr int kHRow = R * 4 + 16;                            // bytes of a row of h in LDS: no two of 16 rows start in the same bank
+    constexpr int kBRow = R * static_cast<int>(sizeof(T)) + 16;  // and of the weights
+    constexpr int kPieces = R / 8;                               // of eight values, of a row; as many for each lane
+    constexpr int kHRows = kUpThreads / (R / 4);                 // rows of h at a time
+    constexpr bool kScaled = std::is_same_v<T, _Float16>;
+    typedef T Y __attribute__((ext_vector_type(N)));
+    typedef T AnyY __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    typedef int64_t L2 __attribute__((ext_vector_type(2)));
+    __shared__ alignas(16) uint8_t staged[std::max(kUpRows * kHRow, kUpWaves * kUpCols * kBRow)];
+    __shared__ alignas(16) int64_t y_rows[kUpRows];  // where the rows are in y
+    __shared__ int32_t rows[kUpRows];
+    __shared__ alignas(16) float units[kScaled ? kUpRows : 4];
     const int lane = threadIdx.x % kWaveLanes, wave = threadIdx.x / kWaveLanes;
     const int r = lane % 16, g = lane / 16;
+    uint8_t *b_rows = staged + wave * kUpCols * kBRow, *h_rows = staged;
     const int blocks = (p.n + kUpWaves * kUpCols - 1) / (kUpWaves * kUpCols);
-    const int64_t items = static_cast<int64_t>(plan.counts[0]) * blocks;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const Tile t = plan.up[item / blocks];
-        const int n0 = static_cast<int>(item % blocks) * (kUpWaves * kUpCols) + wave * kUpCols;
-        if (n0 >= p.n)
-            continue;
-        // fragment f's row i is output n0 + 32 (f / 2) + 8 (i / 4) + 4 (f % 2) + i % 4: a lane's results of
-        // two fragments are eight neighbours
-        Frag<T> w[4][KB];
+    const int64_t tiles = plan.counts[0], items = tiles * blocks;
+    const int64_t run = (items + kXcds - 1) / kXcds, first = blockIdx.x % kXcds * run, last = min(items, first + run);
+    for (int64_t item = first + blockIdx.x / kXcds; item < last; item += gridDim.x / kXcds) {
+        int64_t tile;
+        int block;
+        item_at(item, tiles, blocks, &tile, &block);
+        const Tile t = plan.up[tile];
+        const int col0 = (block * kUpWaves + wave) * kUpCols;
+        const int left = p.n - col0 - N * r;  // of the lane's outputs
+        const T *b = static_cast<const T *>(p.b) + t.adapter * p.b_l;
+        Frag<T> piece[kPieces];
+        if (p.rank == R) {
 #pragma unroll
-        for (int f = 0; f < 4; f++) {
-            const int at = min(n0 + 32 * (f / 2) + 8 * (r / 4) + 4 * (f % 2) + r % 4, p.n - 1);
-            const T *row = static_cast<const T *>(p.b) + t.adapter * p.b_l + at * p.b_n;
+            for (int u = 0; u < kPieces; u++) {
+                const int q = u * kWaveLanes + lane;
+                piece[u] = load_frag(b + min(col0 + q / kPieces, p.n - 1) * p.b_n + q % kPieces * 8);
+            }
+        } else {
 #pragma unroll
-            for (int kb = 0; kb < KB; kb++) {
-                const int k0 = kBoth ? 8 * (g % 2) : 32 * kb + 8 * g;
-                w[f][kb] = load_frag(row + k0, p.rank - k0);
+            for (int u = 0; u < kPieces; u++) {
+                const int q = u * kWaveLanes + lane, c = q % kPieces * 8;
+                piece[u] = load_frag(b + min(col0 + q / kPieces, p.n - 1) * p.b_n + c, p.rank - c);
             }
         }
-        const float scale = p.scale ? p.scale[t.adapter * p.scale_s] : 1.0f;
-        for (int c = 0; c < t.count; c += 16) {
-            const int row = plan.perm[t.first + min(c + r, t.count - 1)];
-            T *y = static_cast<T *>(p.y) + row * p.y_s + n0 + 8 * g;
-            float v[2][8] = {};
+        __syncthreads();  // the last item's h and rows have been read
+        if (threadIdx.x < kUpRows) {
+            const int row = plan.perm[t.first + min(static_cast<int>(threadIdx.x), t.count - 1)];
+            rows[threadIdx.x] = row;
+            y_rows[threadIdx.x] = row * p.y_s;
+        }
 #pragma unroll
-            for (int s = 0; s < 2; s++) {
-                const int left = p.n - n0 - 32 * s - 8 * g;
-                if (left >= 8) {
-                    load8(y + 32 * s, v[s]);
-                } else {
+        for (int u = 0; u < kPieces; u++) {
+            const int q = u * kWaveLanes + lane;
+            *reinterpret_cast<Frag<T> *>(b_rows + q / kPieces * kBRow + q % kPieces * 8 * static_cast<int>(sizeof(T))) = piece[u];
+        }
+        wave_lds_fence();
+        Frag<T> w[N][KB];
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        if (i < left)
-                            v[s][i] = widen(y[32 * s + i]);
-                }
-            }
-            float hv[KB][8];
+        for (int f = 0; f < N; f++)
 #pragma unroll
             for (int kb = 0; kb < KB; kb++) {
                 const int k0 = kBoth ? 8 * (g % 2) : 32 * kb + 8 * g;
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    hv[kb][i] = 0.0f;
-                if (k0 < p.rank) {
-                    const float *h = plan.h + static_cast<int64_t>(row) * R + k0;
-                    for (int s = 0; s < p.slices; s++) {
-                        float part[8];
-                        load8(h + static_cast<int64_t>(s) * p.rows * R, part);
-#pragma unroll
-                        for (int i = 0; i < 8; i++)
-                            hv[kb][i] += part[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; i++)  // past the rank: what padding rows gave
-                        hv[kb][i] = k0 + i < p.rank ? hv[kb][i] * scale : 0.0f;
-                }
+                if (k0 < R)
+                    w[f][kb] = *reinterpret_cast<const Frag<T> *>(b_rows + (N * r + f) * kBRow + k0 * static_cast<int>(sizeof(T)));
+                else
+                    w[f][kb] = zero_frag<T>();
             }
-            // f16 has no room for any h: the row's largest is taken to [0.5, 1)
-            float unit = 1.0f;
-            if constexpr (std::is_same_v<T, _Float16>) {
-                float m = 0.0f;
+        __syncthreads();
+        // h, 16 bytes of a row for each lane, whole lines by lanes in a row
+        const float scale = p.scale ? p.scale[t.adapter * p.scale_s] : 1.0f;
+        const int part = threadIdx.x % (R / 4) * 4;
+#pragma unroll 2
+        for (int row = threadIdx.x / (R / 4); row < (t.count + kHRows - 1) / kHRows * kHRows; row += kHRows) {
+            const float *src = plan.h + static_cast<int64_t>(rows[row]) * R + part;
+            f32x4 v = *reinterpret_cast<const f32x4 *>(src);
+            for (int s = 1; s < p.slices; s++)
+                v += *reinterpret_cast<const f32x4 *>(src + s * static_cast<int64_t>(p.rows) * R);
 #pragma unroll
-                for (int kb = 0; kb < KB; kb++)
+            for (int j = 0; j < 4; j++)  // past the rank: what padding rows gave
+                v[j] = part + j < p.rank ? v[j] * scale : 0.0f;
+            float inv = 1.0f;
+            if constexpr (kScaled) {
+                // f16 has no room for any h: the row's largest is taken to [0.5, 1)
+                float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        m = fmaxf(m, fabsf(hv[kb][i]));
-                m = fmaxf(m, __shfl_xor(m, 16));
-                m = fmaxf(m, __shfl_xor(m, 32));
+                for (int d = 1; d < R / 4; d *= 2)
+                    m = fmaxf(m, __shfl_xor(m, d));
                 const int e = m > 0.0f && m < __builtin_inff() ? min(max(__builtin_amdgcn_frexp_expf(m), -100), 126) : 0;
-                unit = ldexpf(1.0f, e);
-                const float inv = ldexpf(1.0f, -e);
-#pragma unroll
-                for (int kb = 0; kb < KB; kb++)
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        hv[kb][i] *= inv;
+                inv = ldexpf(1.0f, -e);
+                units[row] = ldexpf(1.0f, e);
             }
-            f32x4 acc[4] = {};
+            uint8_t *dst = h_rows + row * kHRow;
+            if constexpr (kSplit) {
+                typedef T V4 __attribute__((ext_vector_type(4)));
+                V4 hi, lo;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    T a, b;
+                    split_value(v[j] * inv, &a, &b);
+                    hi[j] = a;
+                    lo[j] = b;
+                }
+                *reinterpret_cast<V4 *>(dst + part * 2) = hi;
+                *reinterpret_cast<V4 *>(dst + (R + part) * 2) = lo;
+            } else {
+                *reinterpret_cast<f32x4 *>(dst + part * 4) = v;
+            }
+        }
+        __syncthreads();
+        T *y = static_cast<T *>(p.y) + col0 + N * r;
+        const bool whole = col0 + kUpCols <= p.n;
+#pragma unroll 1
+        for (int c = 0; c < t.count; c += 16) {
+            const bool every = whole && c + 16 <= t.count;  // the chunk's outputs all exist
+            const L2 *at = reinterpret_cast<const L2 *>(y_rows + c + 4 * g);
+            T *to[4] = {y + at[0].x, y + at[0].y, y + at[1].x, y + at[1].y};
+            Y v[4];  // as it is until it is used
+            if (every) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    v[i] = *reinterpret_cast<const AnyY *>(to[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int f = 0; f < N; f++)
+                        v[i][f] = f < left ? to[i][f] : static_cast<T>(0.0f);
+            }
+            const uint8_t *h = h_rows + (c + r) * kHRow;
+            f32x4 acc[N] = {};
 #pragma unroll
             for (int kb = 0; kb < KB; kb++) {
-                Frag<T> hi, lo;
+                if constexpr (kBoth) {
+                    const Frag<T> b = load_frag(reinterpret_cast<const T *>(h + 16 * g));
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    if constexpr (kSplit) {
-                        T a, b;
-                        split_value(hv[kb][i], &a, &b);
-                        hi.v[i] = kBoth && g >= 2 ? b : a;
-                        lo.v[i] = b;
-                    } else {
-                        hi.v[i] = hv[kb][i];
-                    }
-                }
+                    for (int f = 0; f < N; f++)
+                        acc[f] = mma(b, w[f][kb], acc[f]);
+                } else if constexpr (kSplit) {
+                    const Frag<T> hi = load_frag(reinterpret_cast<const T *>(h + 64 * kb + 16 * g));
+                    const Frag<T> lo = load_frag(reinterpret_cast<const T *>(h + 2 * R + 64 * kb + 16 * g));
 #pragma unroll
-                for (int f = 0; f < 4; f++) {
-                    acc[f] = mma(w[f][kb], hi, acc[f]);
-                    if constexpr (kSplit && !kBoth)
-                        acc[f] = mma(w[f][kb], lo, acc[f]);
+                    for (int f = 0; f < N; f++)
+                        acc[f] = mma(hi, w[f][kb], acc[f]);
+#pragma unroll
+                    for (int f = 0; f < N; f++)
+                        acc[f] = mma(lo, w[f][kb], acc[f]);
+                } else {
+                    const Frag<T> b = R >= 32 || g < 2 ? load_frag(reinterpret_cast<const T *>(h + 128 * kb + 32 * g)) : zero_frag<T>();
+#pragma unroll
+                    for (int f = 0; f < N; f++)
+                        acc[f] = mma(b, w[f][kb], acc[f]);
                 }
             }
-            if (c + r >= t.count)
-                continue;
+            f32x4 unit = {1.0f, 1.0f, 1.0f, 1.0f};
+            if constexpr (kScaled)
+                unit = *reinterpret_cast<const f32x4 *>(units + c + 4 * g);
 #pragma unroll
-            for (int s = 0; s < 2; s++) {
+            for (int i = 0; i < 4; i++)
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    v[s][i] += acc[2 * s + i / 4][i % 4] * unit;
-                store8(y + 32 * s, p.n - n0 - 32 * s - 8 * g, v[s]);
+                for (int f = 0; f < N; f++)
+                    v[i][f] = narrow<T>(widen(v[i][f]) + acc[f][i] * unit[i]);
+            if (every) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    *reinterpret_cast<AnyY *>(to[i]) = v[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (c + 4 * g + i < t.count)
+#pragma unroll
+                        for (int f = 0; f < N; f++)
+                            if (f < left)
+                                to[i][f] = v[i][f];
             }
         }
     }
@@ -501,32 +628,33 @@ int padded_rank(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank 
 int64_t most_tiles(int64_t rows, int64_t adapters, int64_t tile) { return rows / tile + std::min(rows, adapters); }
 int64_t whole(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
+constexpr int64_t kUpGroups = 8192;  // a multiple of the XCDs
 // Slices of k: enough workgroups for the chip, none with less than kLeastSlice values.
-constexpr int64_t kLeastSlice = 1024, kDownGroups = 256;
+constexpr int64_t kLeastSlice = 1024, kDownGroups = 256, kMostSlices = 4;
 void slices_of(int64_t rows, int64_t adapters, int64_t k, int32_t *slices, int32_t *slice) {
     const int64_t tiles = rows <= kSelfRows ? std::min(rows, adapters) : most_tiles(rows, adapters, kDownRows);
-    const int64_t s = std::max<int64_t>(1, std::min(kDownGroups / tiles, k / kLeastSlice));
+    const int64_t s = std::max<int64_t>(1, std::min<int64_t>({kDownGroups / tiles, k / kLeastSlice, kMostSlices}));
     const int64_t per = std::max<int64_t>(32, ((k + s - 1) / s + 31) / 32 * 32);
     *slice = static_cast<int32_t>(per);
     *slices = static_cast<int32_t>(std::max<int64_t>(1, (k + per - 1) / per));
 }
 
-template <typename T, typename SRC, bool SELF>
+template <typename T, typename SRC, int XF, bool SELF>
 const void *down_rank(int rank) {
-    return rank == 16   ? reinterpret_cast<const void *>(&lora_down_kernel<T, SRC, 1, SELF>)
-           : rank == 32 ? reinterpret_cast<const void *>(&lora_down_kernel<T, SRC, 2, SELF>)
-           : rank == 64 ? reinterpret_cast<const void *>(&lora_down_kernel<T, SRC, 4, SELF>)
-                        : reinterpret_cast<const void *>(&lora_down_kernel<T, SRC, 8, SELF>);
+    return rank == 16   ? reinterpret_cast<const void *>(&lora_down_kernel<T, SRC, 1, XF, SELF>)
+           : rank == 32 ? reinterpret_cast<const void *>(&lora_down_kernel<T, SRC, 2, XF, SELF>)
+           : rank == 64 ? reinterpret_cast<const void *>(&lora_down_kernel<T, SRC, 4, XF, SELF>)
+                        : reinterpret_cast<const void *>(&lora_down_kernel<T, SRC, 8, XF, SELF>);
 }
-template <bool SELF>
+template <int XF, bool SELF>
 const void *down_fn(int dtype, int format, int rank) {
     if (format == SSU_FORMAT_MXFP8)
-        return down_rank<__bf16, Mx8, SELF>(rank);
+        return down_rank<__bf16, Mx8, XF, SELF>(rank);
     if (format == SSU_FORMAT_MXFP4)
-        return down_rank<__bf16, Mx4, SELF>(rank);
-    return dtype == SSU_F32   ? down_rank<float, float, SELF>(rank)
-           : dtype == SSU_F16 ? down_rank<_Float16, _Float16, SELF>(rank)
-                              : down_rank<__bf16, __bf16, SELF>(rank);
+        return down_rank<__bf16, Mx4, XF, SELF>(rank);
+    return dtype == SSU_F32   ? down_rank<float, float, XF, SELF>(rank)
+           : dtype == SSU_F16 ? down_rank<_Float16, _Float16, XF, SELF>(rank)
+                              : down_rank<__bf16, __bf16, XF, SELF>(rank);
 }
 template <typename T>
 const void *up_rank(int rank) {
@@ -566,19 +694,22 @@ int launch_add_lora(const LoraParams &params, int dtype, int format, void *strea
     const unsigned counters = static_cast<unsigned>(p.adapters) * 4;
     void *args[] = {&p, &plan};
     if (p.rows <= kSelfRows) {
-        const int64_t groups = 1 + std::min<int64_t>(p.rows, p.adapters) * p.slices;
-        if (int hip = launch_groups(down_fn<true>(dtype, format, rank), groups, kDownThreads, args, stream, counters))
+        const int64_t each = std::min<int64_t>(p.rows, p.adapters), groups = 1 + each * p.slices;
+        // more than 16 rows for each adapter, if they are spread evenly: 32 at a time
+        const void *down = p.rows > 16 * each ? down_fn<2, true>(dtype, format, rank) : down_fn<1, true>(dtype, format, rank);
+        if (int hip = launch_groups(down, groups, kDownThreads, args, stream, counters))
             return hip;
     } else {
         if (int hip = launch_groups(reinterpret_cast<const void *>(&lora_plan_kernel), 1, kPlanThreads, args, stream, counters))
             return hip;
         const int64_t groups = most_tiles(p.rows, p.adapters, kDownRows) * p.slices;
-        if (int hip = launch_groups(down_fn<false>(dtype, format, rank), groups, kDownThreads, args, stream))
+        if (int hip = launch_groups(down_fn<kDownRows / 16, false>(dtype, format, rank), groups, kDownThreads, args, stream))
             return hip;
     }
     // workgroups take turns at the items: how many there are is known on the device
     const int64_t blocks = (p.n + kUpWaves * kUpCols - 1) / (kUpWaves * kUpCols);
-    const int64_t groups = std::min<int64_t>(most_tiles(p.rows, p.adapters, kUpRows) * blocks, 256 * 8);
+    const int64_t most = (most_tiles(p.rows, p.adapters, kUpRows) * blocks + kXcds - 1) / kXcds * kXcds;
+    const int64_t groups = std::min<int64_t>(most, kUpGroups);
     const void *up = dtype == SSU_F32 ? up_rank<float>(rank) : dtype == SSU_F16 ? up_rank<_Float16>(rank) : up_rank<__bf16>(rank);
     return launch_groups(up, groups, kUpThreads, args, stream);
 }
