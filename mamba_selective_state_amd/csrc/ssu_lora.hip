@@ -75,6 +75,29 @@ __device__ __forceinline__ Frag<T> load_frag(const T *p, int n) {
     return f;
 }
 
+// A vector's elements moved down by `s` places (not negative), zeros behind them.
+template <typename V>
+__device__ __forceinline__ V moved_down(V v, int s) {
+    if constexpr (sizeof(V) == 8) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        return __builtin_bit_cast(V, s < 4 ? b >> (16 * s) : 0);
+    } else if constexpr (sizeof(v[0]) == 2) {
+        typedef uint64_t U2 __attribute__((ext_vector_type(2)));
+        const U2 b = __builtin_bit_cast(U2, v);
+        const uint64_t over = b.y << 1 << (63 - 16 * min(s, 3));  // what comes from the upper half, for s < 4
+        const U2 r = {s < 4 ? b.x >> (16 * s) | over : s < 8 ? b.y >> (16 * (s - 4)) : 0, s < 4 ? b.y >> (16 * s) : 0};
+        return __builtin_bit_cast(V, r);
+    } else {
+        constexpr int kN = sizeof(V) / 4;
+#pragma unroll
+        for (int step = 1; step < 2 * kN; step *= 2)
+#pragma unroll
+            for (int i = 0; i < kN; i++)
+                v[i] = !(s & step) ? v[i] : i + step < kN ? v[i + step < kN ? i + step : 0] : 0.0f;
+        return s < 2 * kN ? v : V{};
+    }
+}
+
 // ---------------------------------------------------------------- the plan
 
 constexpr int kDownRows = 32;  // rows of a down tile
@@ -413,6 +436,220 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(const LoraParam
     }
 }
 
+// ---------------------------------------------------------------- down, many rows
+//
+// Tiles of the plan, through LDS: a stage is 256 bytes (128 or, in f32, 64 values of k) of 32 rows of x and of all rank rows, which
+// LDS-DMA brings in whole lines, two stages ahead. With operands straight from memory, 64 bytes of 16 rows for each access, 8192 x 4096
+// bf16 of rank 64 took 50 us.
+//
+// Chunk c (16 bytes) of row r is at place c ^ r of its row, so that the 16 rows of an operand are read from different banks.
+
+constexpr int kStageBytes = 256;  // of a row of T
+
+// x's part of a stage: bytes of a row, and how an operand is read from them.
+template <typename T, typename SRC>
+struct XStage {
+    static constexpr int kRow = kStageBytes;
+    // `at`: the row's image; chunks' places are swapped by `swap`
+    static __device__ __forceinline__ Frag<T> read(const uint8_t *at, int swap, int step, int g, uint32_t) {
+        Frag<T> f;
+        if constexpr (sizeof(T) == 2) {
+            f = *reinterpret_cast<const Frag<T> *>(at + ((4 * step + g) ^ swap) * 16);
+        } else {
+            *reinterpret_cast<f32x4 *>(&f.v) = *reinterpret_cast<const f32x4 *>(at + ((8 * step + 2 * g) ^ swap) * 16);
+            *(reinterpret_cast<f32x4 *>(&f.v) + 1) = *reinterpret_cast<const f32x4 *>(at + ((8 * step + 2 * g + 1) ^ swap) * 16);
+        }
+        return f;
+    }
+};
+template <>
+struct XStage<__bf16, Mx8> {
+    static constexpr int kRow = kStageBytes / 2;
+    static __device__ __forceinline__ Frag<__bf16> read(const uint8_t *at, int swap, int step, int g, uint32_t scales) {
+        const u32x2 c = *reinterpret_cast<const u32x2 *>(at + ((2 * step + g / 2) ^ (swap / 2 % 8)) * 16 + g % 2 * 8);
+        const uint32_t s = (scales >> (8 * step)) & 0xFF;
+        const float scale = mx8_scale(s);
+        Frag<__bf16> f;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const float2 lo = e4m3_pair<false>(c[i], scale), hi = e4m3_pair<true>(c[i], scale);
+            const float v[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                f.v[4 * i + j] = narrow<__bf16>(s == 255 ? __builtin_nanf("") : v[j]);
+        }
+        return f;
+    }
+};
+template <>
+struct XStage<__bf16, Mx4> {
+    static constexpr int kRow = kStageBytes / 4;
+    static __device__ __forceinline__ Frag<__bf16> read(const uint8_t *at, int swap, int step, int g, uint32_t scales) {
+        const uint32_t c = *reinterpret_cast<const uint32_t *>(at + (step ^ (swap / 4 % 4)) * 16 + g * 4);
+        const uint32_t s = (scales >> (8 * step)) & 0xFF;
+        const float scale = mx8_scale(s);
+        const float2 v[4] = {e2m1_pair<0>(c, scale), e2m1_pair<1>(c, scale), e2m1_pair<2>(c, scale), e2m1_pair<3>(c, scale)};
+        Frag<__bf16> f;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            f.v[2 * j] = narrow<__bf16>(s == 255 ? __builtin_nanf("") : v[j].x);
+            f.v[2 * j + 1] = narrow<__bf16>(s == 255 ? __builtin_nanf("") : v[j].y);
+        }
+        return f;
+    }
+};
+
+template <typename T, typename SRC, int RF>
+__global__ __launch_bounds__(kDownThreads) void lora_down_staged_kernel(const LoraParams p, const LoraPlan plan) {
+    constexpr bool kCodes = std::is_same_v<SRC, Mx8> || std::is_same_v<SRC, Mx4>;
+    using Stage = XStage<T, SRC>;
+    constexpr int kDepth = kStageBytes / static_cast<int>(sizeof(T)), kSteps = kDepth / 32;
+    constexpr int kXRow = Stage::kRow, kXBytes = kDownRows * kXRow, kABytes = RF * 16 * kStageBytes, kBytes = kXBytes + kABytes;
+    // KiB of a stage, and for codes the rows' scale words; of a wave, and how many waves have one more
+    constexpr int kWhole = kBytes / 1024, kFills = kWhole + kCodes, kEach = kFills / kDownWaves, kMore = kFills % kDownWaves;
+    constexpr int kScaleBytes = kCodes ? 256 : 0;
+    constexpr int kRing = RF == 8 ? 2 : 3;
+    constexpr int kPairs = kDownRows / 16 * RF;  // of an operand of x and one of A
+    constexpr int kMine = kPairs > kDownWaves ? kPairs / kDownWaves : 1;
+    constexpr int kSubs = kPairs >= kDownWaves ? 1 : kDownWaves / kPairs < kSteps ? kDownWaves / kPairs : kSteps;  // waves of a pair: turns at the steps
+    // arrays of their own: the compiler tells fills of one from reads of another
+    __shared__ alignas(16) uint8_t s0[kBytes + kScaleBytes], s1[kBytes + kScaleBytes], s2[kRing > 2 ? kBytes + kScaleBytes : 16];
+    __shared__ f32x4 sums[kSubs > 1 ? kDownWaves * 64 : 1];
+    const int tile = static_cast<int>(blockIdx.x) / p.slices, slice = static_cast<int>(blockIdx.x) % p.slices;
+    if (tile >= plan.counts[1])
+        return;
+    const Tile t = plan.down[tile];
+    const int lane = threadIdx.x % kWaveLanes, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
+    const int r = lane % 16, g = lane / 16;
+    const int begin = slice * p.slice, end = min(p.k, begin + p.slice), stages = (end - begin) / kDepth;
+    constexpr int64_t kUnit = static_cast<int64_t>(sizeof(T));
+    const uint8_t *a = static_cast<const uint8_t *>(p.a) + t.adapter * p.a_l * kUnit;
+    // what this wave fills: KiB number wave + 8 i of a stage, x's first
+    const uint8_t *src[kEach + 1];
+    int advance[kEach + 1];
+#pragma unroll
+    for (int i = 0; i <= kEach; i++) {
+        const int fill = wave + i * kDownWaves;
+        if (fill < kXBytes / 1024) {
+            constexpr int kLanes = kXRow / 16;
+            const int row = fill * (1024 / kXRow) + lane / kLanes, slot = lane % kLanes;
+            const int swap = kXRow == 256 ? row % 16 : kXRow == 128 ? row % 16 / 2 : row % 16 / 4;
+            const int64_t stride = kCodes ? p.x_s : p.x_s * kUnit;
+            src[i] = static_cast<const uint8_t *>(p.x) + plan.perm[t.first + min(row, t.count - 1)] * stride +
+                     begin / kDepth * kXRow + (slot ^ swap) * 16;
+            advance[i] = kXRow;
+        } else if (kCodes && fill >= kWhole) {
+            src[i] = p.x_scale + plan.perm[t.first + min(lane % kDownRows, t.count - 1)] * p.xs_s + begin / 32;
+            advance[i] = kSteps;
+        } else {
+            const int row = (fill - kXBytes / 1024) * 4 + lane / 16, slot = lane % 16;
+            src[i] = a + min(row, p.rank - 1) * p.a_r * kUnit + begin * kUnit + (slot ^ (row % 16)) * 16;
+            advance[i] = kStageBytes;
+        }
+    }
+    // the waits count fetches in the order in which they are written down here
+    auto in_order = [] {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto fill = [&](int stage, uint8_t *image) {
+        in_order();
+#pragma unroll
+        for (int i = 0; i <= kEach; i++) {
+            if (i == kEach && wave >= kMore)
+                break;
+            const int fill = wave + i * kDownWaves;
+            const auto *from = (const __attribute__((address_space(1))) void *)(src[i] + static_cast<int64_t>(stage) * advance[i]);
+            auto *to = (__attribute__((address_space(3))) void *)(image + fill * 1024);
+            if (kCodes && i == kFills / kDownWaves - (kFills % kDownWaves == 0) && fill == kWhole)
+                __builtin_amdgcn_global_load_lds(from, to, 4, 0, 0);
+            else
+                __builtin_amdgcn_global_load_lds(from, to, 16, 0, 0);
+        }
+        in_order();
+    };
+    // Barrier behind which the next stage's fills, all but `left` of this wave's, have arrived, and the last
+    // stage's image has been read. Spelled out: a barrier with the compiler's own waits would wait for all fills.
+    auto meet = [&](auto left) {
+        in_order();
+        __builtin_amdgcn_s_waitcnt(0x0070 | decltype(left)::value);  // vmcnt(left) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        in_order();
+    };
+    const int pair0 = kPairs >= kDownWaves ? wave * kMine : wave % kPairs, sub = kPairs >= kDownWaves ? 0 : wave / kPairs;
+    const int xf = pair0 / RF;  // pairs of a wave share x's operand
+    const int x_row = plan.perm[t.first + min(16 * xf + r, t.count - 1)];
+    f32x4 acc[kMine] = {};
+    auto image = [&](int i) { return i == 0 ? s0 : i == 1 ? s1 : s2; };
+    for_passes<0, kRing - 1>([&](auto i) {
+        if (decltype(i)::value < stages)
+            fill(decltype(i)::value, image(decltype(i)::value));
+    });
+    for (int first = 0; first < stages; first += kRing)
+        for_passes<0, kRing>([&](auto i) {
+            constexpr int n = decltype(i)::value;
+            const int stage = first + n;
+            if (stage >= stages)
+                return;
+            // the next stage's fills may still be on their way
+            if (kRing == 2 || stage + 1 >= stages)
+                meet(std::integral_constant<int, 0>());
+            else if (wave < kMore)
+                meet(std::integral_constant<int, kEach + 1>());
+            else
+                meet(std::integral_constant<int, kEach>());
+            if (stage + kRing - 1 < stages)
+                fill(stage + kRing - 1, image((n + kRing - 1) % kRing));
+            const uint8_t *x_image = image(n) + (16 * xf + r) * kXRow, *a_image = image(n) + kXBytes;
+            const uint32_t scales = kCodes ? *reinterpret_cast<const uint32_t *>(image(n) + kBytes + (16 * xf + r) * 4) : 0;
+#pragma unroll
+            for (int step = 0; step < kSteps; step++) {
+                if (kSubs > 1 && step % kSubs != sub)
+                    continue;
+                const Frag<T> x = Stage::read(x_image, r, step, g, scales);
+#pragma unroll
+                for (int m = 0; m < kMine; m++) {
+                    const Frag<T> w = XStage<T, T>::read(a_image + ((pair0 + m) % RF * 16 + r) * kStageBytes, r, step, g, 0);
+                    acc[m] = mma(w, x, acc[m]);
+                }
+            }
+        });
+    // what is left of k, straight from memory
+    for (int at = begin + stages * kDepth + 32 * sub; at < end && sub < kSubs; at += 32 * kSubs) {
+        const int n = end - at - 8 * g;
+        Frag<T> x;
+        if constexpr (kCodes) {
+            x = zero_frag<T>();
+            if (n > 0) {  // a lane's eight of the sixteen that the other kernel takes
+                const Step<T> both = XRow<T, SRC>(p, x_row).load(at + g / 2 * 16);
+                x.v = g % 2 ? both.f[1].v : both.f[0].v;
+            }
+        } else {
+            x = load_frag(static_cast<const T *>(p.x) + x_row * p.x_s + at + 8 * g, n);
+        }
+#pragma unroll
+        for (int m = 0; m < kMine; m++) {
+            const T *row = reinterpret_cast<const T *>(a) + min((pair0 + m) % RF * 16 + r, p.rank - 1) * p.a_r;
+            acc[m] = mma(load_frag(row + at + 8 * g, n), x, acc[m]);
+        }
+    }
+    if constexpr (kSubs > 1) {
+        sums[wave * 64 + lane] = acc[0];
+        __syncthreads();
+        if (sub != 0)
+            return;
+#pragma unroll
+        for (int i = 1; i < kSubs; i++)
+            acc[0] += sums[(wave + i * kPairs) * 64 + lane];
+    }
+    if (sub == 0 && 16 * xf + r < t.count) {
+        float *h = plan.h + (static_cast<int64_t>(slice) * p.rows + x_row) * (RF * 16) + 4 * g;
+#pragma unroll
+        for (int m = 0; m < kMine; m++)
+            *reinterpret_cast<f32x4 *>(h + (pair0 + m) % RF * 16) = acc[m];
+    }
+}
+
 // ---------------------------------------------------------------- up
 
 constexpr int kUpThreads = 256;
@@ -427,15 +664,6 @@ __device__ __forceinline__ void split_value(float v, T *hi, T *lo) {
     *lo = narrow<T>(fabsf(w) < __builtin_inff() ? v - w : 0.0f);
 }
 
-// Tile and block of columns of item `i`: each XCD has a run of items, in groups of eight blocks of columns whose weights stay
-// in its L2 while it goes through the tiles.
-__device__ __forceinline__ void item_at(int64_t i, int64_t tiles, int blocks, int64_t *tile, int *block) {
-    const int64_t group = i / (8 * tiles), in = i - group * 8 * tiles;
-    const int width = min(8, blocks - static_cast<int>(group) * 8);
-    *tile = in / width;
-    *block = static_cast<int>(group * 8 + in % width);
-}
-
 // A tile of rows times four waves' columns. Every wave fetches its columns' weights row by row and takes them to
 // registers through LDS; h of the tile is joined over the slices of k, scaled, split and left in LDS; then the waves go through the
 // rows, 16 at a time.
@@ -443,7 +671,7 @@ __device__ __forceinline__ void item_at(int64_t i, int64_t tiles, int blocks, in
 // Here h's rows go first and the weights second: lane l has results of rows 4 (l / 16) .. + 3, and fragment f's column l % 16 is
 // output 4 (l % 16) + f of the wave's, so that 16 lanes in a row have 64 outputs in a row of one row of y.
 template <typename T, int R>
-__global__ __launch_bounds__(kUpThreads) void lora_up_kernel(const LoraParams p, const LoraPlan plan) {
+__global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void lora_up_kernel(const LoraParams p, const LoraPlan plan) {
     constexpr int N = 4;                     // outputs of a lane and row
     constexpr int KB = R < 32 ? 1 : R / 32;  // operands of 32 along the rank
     constexpr bool kSplit = sizeof(T) == 2;
@@ -452,6 +680,9 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(const LoraParams p,
     constexpr int kBRow = R * static_cast<int>(sizeof(T)) + 16;  // and of the weights
     constexpr int kPieces = R / 8;                               // of eight values, of a row; as many for each lane
     constexpr int kHRows = kUpThreads / (R / 4);                 // rows of h at a time
+    // a chunk of y ahead, where the registers leave room for it and four waves: 8192 x 18560 bf16 of rank 64 take 132 us without
+    // it and 145 with it and three waves, 2048 x 18560 of rank 16 48 and 42
+    constexpr bool kAhead = R <= 32;
     constexpr bool kScaled = std::is_same_v<T, _Float16>;
     typedef T Y __attribute__((ext_vector_type(N)));
     typedef T AnyY __attribute__((ext_vector_type(N), aligned(sizeof(T))));
@@ -463,16 +694,16 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(const LoraParams p,
     const int lane = threadIdx.x % kWaveLanes, wave = threadIdx.x / kWaveLanes;
     const int r = lane % 16, g = lane / 16;
     uint8_t *b_rows = staged + wave * kUpCols * kBRow, *h_rows = staged;
-    const int blocks = (p.n + kUpWaves * kUpCols - 1) / (kUpWaves * kUpCols);
-    const int64_t tiles = plan.counts[0], items = tiles * blocks;
-    const int64_t run = (items + kXcds - 1) / kXcds, first = blockIdx.x % kXcds * run, last = min(items, first + run);
-    for (int64_t item = first + blockIdx.x / kXcds; item < last; item += gridDim.x / kXcds) {
-        int64_t tile;
-        int block;
-        item_at(item, tiles, blocks, &tile, &block);
-        const Tile t = plan.up[tile];
-        const int col0 = (block * kUpWaves + wave) * kUpCols;
+    const uint32_t blocks = (p.n + kUpWaves * kUpCols - 1) / (kUpWaves * kUpCols);
+    const uint32_t items = static_cast<uint32_t>(plan.counts[0]) * blocks;
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const Tile t = plan.up[item / blocks];
+        const int col0 = (static_cast<int>(item % blocks) * kUpWaves + wave) * kUpCols;
         const int left = p.n - col0 - N * r;  // of the lane's outputs
+        const bool whole = col0 + kUpCols <= p.n;  // the wave's outputs all exist
+        // what is needed first is asked for at once: the tile's rows, weights, then the rows' first h and y
+        const int row_lo = plan.perm[t.first + min(lane, t.count - 1)];
+        const int part = threadIdx.x % (R / 4) * 4, h_first = threadIdx.x / (R / 4);
         const T *b = static_cast<const T *>(p.b) + t.adapter * p.b_l;
         Frag<T> piece[kPieces];
         if (p.rank == R) {
@@ -484,8 +715,36 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(const LoraParams p,
         } else {
 #pragma unroll
             for (int u = 0; u < kPieces; u++) {
-                const int q = u * kWaveLanes + lane, c = q % kPieces * 8;
-                piece[u] = load_frag(b + min(col0 + q / kPieces, p.n - 1) * p.b_n + c, p.rank - c);
+                // a row's last eight values hold its end; what lies past it becomes 0
+                const int q = u * kWaveLanes + lane, c = q % kPieces * 8, from = max(0, min(c, p.rank - 8));
+                const T *row = b + min(col0 + q / kPieces, p.n - 1) * p.b_n;
+                if (p.rank >= 8) {
+                    piece[u].v = moved_down(load_frag(row + from).v, c - from);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const T value = row[min(i, p.rank - 1)];
+                        piece[u].v[i] = c + i < p.rank ? value : static_cast<T>(0.0f);
+                    }
+                }
+            }
+        }
+        auto h_at = [&](int row) {
+            const float *src = plan.h + static_cast<int64_t>(row) * R + part;
+            f32x4 v = *reinterpret_cast<const f32x4 *>(src);
+            for (int s = 1; s < p.slices; s++)
+                v += *reinterpret_cast<const f32x4 *>(src + s * static_cast<int64_t>(p.rows) * R);
+            return v;
+        };
+        const f32x4 h0 = h_at(__shfl(row_lo, h_first));
+        T *y = static_cast<T *>(p.y) + col0 + N * r;
+        Y v[4];  // a chunk's outputs, as they are until they are used
+        T *to[4];
+        if (kAhead && whole) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                to[i] = y + __shfl(row_lo, 4 * g + i) * p.y_s;
+                v[i] = *reinterpret_cast<const AnyY *>(to[i]);
             }
         }
         __syncthreads();  // the last item's h and rows have been read
@@ -514,13 +773,8 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(const LoraParams p,
         __syncthreads();
         // h, 16 bytes of a row for each lane, whole lines by lanes in a row
         const float scale = p.scale ? p.scale[t.adapter * p.scale_s] : 1.0f;
-        const int part = threadIdx.x % (R / 4) * 4;
-#pragma unroll 2
-        for (int row = threadIdx.x / (R / 4); row < (t.count + kHRows - 1) / kHRows * kHRows; row += kHRows) {
-            const float *src = plan.h + static_cast<int64_t>(rows[row]) * R + part;
-            f32x4 v = *reinterpret_cast<const f32x4 *>(src);
-            for (int s = 1; s < p.slices; s++)
-                v += *reinterpret_cast<const f32x4 *>(src + s * static_cast<int64_t>(p.rows) * R);
+        for (int row = h_first; row < (t.count + kHRows - 1) / kHRows * kHRows; row += kHRows) {
+            f32x4 v = row == h_first ? h0 : h_at(rows[row]);
 #pragma unroll
             for (int j = 0; j < 4; j++)  // past the rank: what padding rows gave
                 v[j] = part + j < p.rank ? v[j] * scale : 0.0f;
@@ -553,25 +807,8 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(const LoraParams p,
             }
         }
         __syncthreads();
-        T *y = static_cast<T *>(p.y) + col0 + N * r;
-        const bool whole = col0 + kUpCols <= p.n;
-#pragma unroll 1
-        for (int c = 0; c < t.count; c += 16) {
-            const bool every = whole && c + 16 <= t.count;  // the chunk's outputs all exist
-            const L2 *at = reinterpret_cast<const L2 *>(y_rows + c + 4 * g);
-            T *to[4] = {y + at[0].x, y + at[0].y, y + at[1].x, y + at[1].y};
-            Y v[4];  // as it is until it is used
-            if (every) {
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    v[i] = *reinterpret_cast<const AnyY *>(to[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int f = 0; f < N; f++)
-                        v[i][f] = f < left ? to[i][f] : static_cast<T>(0.0f);
-            }
+        // v += delta, for the chunk from row c on
+        auto add = [&](int c) {
             const uint8_t *h = h_rows + (c + r) * kHRow;
             f32x4 acc[N] = {};
 #pragma unroll
@@ -605,11 +842,71 @@ __global__ __launch_bounds__(kUpThreads) void lora_up_kernel(const LoraParams p,
 #pragma unroll
                 for (int f = 0; f < N; f++)
                     v[i][f] = narrow<T>(widen(v[i][f]) + acc[f][i] * unit[i]);
-            if (every) {
+        };
+        auto places = [&](int c, T *(&to)[4]) {
+            const L2 *at = reinterpret_cast<const L2 *>(y_rows + c + 4 * g);
+            to[0] = y + at[0].x, to[1] = y + at[0].y, to[2] = y + at[1].x, to[3] = y + at[1].y;
+        };
+        auto load = [&](int c) {
+            places(c, to);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                v[i] = *reinterpret_cast<const AnyY *>(to[i]);
+        };
+        int c = 0;
+        if (whole) {
+#pragma unroll 1
+            for (; c + 16 <= t.count; c += 16) {
+                if constexpr (kAhead) {
+                    // the next chunk is on its way while one is worked on; no store is waited for
+                    T *next_to[4];
+                    Y next[4];
+                    if (c + 16 < t.count) {
+                        places(c + 16, next_to);
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            next[i] = *reinterpret_cast<const AnyY *>(next_to[i]);
+                    }
+                    add(c);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        *reinterpret_cast<AnyY *>(to[i]) = v[i];
+                        to[i] = next_to[i];
+                        v[i] = next[i];
+                    }
+                } else {
+                    load(c);
+                    add(c);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        *reinterpret_cast<AnyY *>(to[i]) = v[i];
+                }
+            }
+            if (c < t.count) {
+                if constexpr (!kAhead)
+                    load(c);
+                add(c);
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    *reinterpret_cast<AnyY *>(to[i]) = v[i];
-            } else {
+                    if (c + 4 * g + i < t.count)
+                        *reinterpret_cast<AnyY *>(to[i]) = v[i];
+            }
+        } else {
+            const int past = max(0, N - left);  // how far the lane's outputs reach past the row's end
+#pragma unroll 1
+            for (; c < t.count; c += 16) {
+                places(c, to);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (p.n >= N) {
+                        v[i] = moved_down(static_cast<Y>(*reinterpret_cast<const AnyY *>(to[i] - past)), past);
+                    } else {
+#pragma unroll
+                        for (int f = 0; f < N; f++)
+                            v[i][f] = to[i][min(f, left - 1)];
+                    }
+                }
+                add(c);
 #pragma unroll
                 for (int i = 0; i < 4; i++)
                     if (c + 4 * g + i < t.count)
@@ -628,13 +925,13 @@ int padded_rank(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank 
 int64_t most_tiles(int64_t rows, int64_t adapters, int64_t tile) { return rows / tile + std::min(rows, adapters); }
 int64_t whole(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
-constexpr int64_t kUpGroups = 8192;  // a multiple of the XCDs
+constexpr int64_t kUpGroups = 8192;
 // Slices of k: enough workgroups for the chip, none with less than kLeastSlice values.
-constexpr int64_t kLeastSlice = 1024, kDownGroups = 256, kMostSlices = 4;
+constexpr int64_t kLeastSlice = 1024, kDownGroups = 512, kMostSlices = 4;
 void slices_of(int64_t rows, int64_t adapters, int64_t k, int32_t *slices, int32_t *slice) {
     const int64_t tiles = rows <= kSelfRows ? std::min(rows, adapters) : most_tiles(rows, adapters, kDownRows);
-    const int64_t s = std::max<int64_t>(1, std::min<int64_t>({kDownGroups / tiles, k / kLeastSlice, kMostSlices}));
-    const int64_t per = std::max<int64_t>(32, ((k + s - 1) / s + 31) / 32 * 32);
+    const int64_t s = std::max<int64_t>(1, std::min<int64_t>({(kDownGroups + tiles - 1) / tiles, k / kLeastSlice, kMostSlices}));
+    const int64_t per = std::max<int64_t>(128, ((k + s - 1) / s + 127) / 128 * 128);  // whole stages
     *slice = static_cast<int32_t>(per);
     *slices = static_cast<int32_t>(std::max<int64_t>(1, (k + per - 1) / per));
 }
@@ -655,6 +952,30 @@ const void *down_fn(int dtype, int format, int rank) {
     return dtype == SSU_F32   ? down_rank<float, float, XF, SELF>(rank)
            : dtype == SSU_F16 ? down_rank<_Float16, _Float16, XF, SELF>(rank)
                               : down_rank<__bf16, __bf16, XF, SELF>(rank);
+}
+template <typename T, typename SRC>
+const void *staged_rank(int rank) {
+    return rank == 16   ? reinterpret_cast<const void *>(&lora_down_staged_kernel<T, SRC, 1>)
+           : rank == 32 ? reinterpret_cast<const void *>(&lora_down_staged_kernel<T, SRC, 2>)
+           : rank == 64 ? reinterpret_cast<const void *>(&lora_down_staged_kernel<T, SRC, 4>)
+                        : reinterpret_cast<const void *>(&lora_down_staged_kernel<T, SRC, 8>);
+}
+const void *staged_fn(int dtype, int format, int rank) {
+    if (format == SSU_FORMAT_MXFP8)
+        return staged_rank<__bf16, Mx8>(rank);
+    if (format == SSU_FORMAT_MXFP4)
+        return staged_rank<__bf16, Mx4>(rank);
+    return dtype == SSU_F32   ? staged_rank<float, float>(rank)
+           : dtype == SSU_F16 ? staged_rank<_Float16, _Float16>(rank)
+                              : staged_rank<__bf16, __bf16>(rank);
+}
+// Whether LDS-DMA can fetch x and a, 16 bytes from places that are multiples of them, and words of scales.
+bool staged_fits(const LoraParams &p, int dtype, int format) {
+    const int64_t unit = dtype == SSU_F32 ? 4 : 2, x_unit = format == SSU_FORMAT_SAME ? unit : 1;
+    auto whole16 = [](const void *at) { return reinterpret_cast<uintptr_t>(at) % 16 == 0; };
+    if (format != SSU_FORMAT_SAME && (reinterpret_cast<uintptr_t>(p.x_scale) % 4 != 0 || p.xs_s % 4 != 0))
+        return false;
+    return whole16(p.x) && whole16(p.a) && p.x_s * x_unit % 16 == 0 && p.a_l * unit % 16 == 0 && p.a_r * unit % 16 == 0;
 }
 template <typename T>
 const void *up_rank(int rank) {
@@ -703,12 +1024,15 @@ int launch_add_lora(const LoraParams &params, int dtype, int format, void *strea
         if (int hip = launch_groups(reinterpret_cast<const void *>(&lora_plan_kernel), 1, kPlanThreads, args, stream, counters))
             return hip;
         const int64_t groups = most_tiles(p.rows, p.adapters, kDownRows) * p.slices;
-        if (int hip = launch_groups(down_fn<kDownRows / 16, false>(dtype, format, rank), groups, kDownThreads, args, stream))
+        const void *down = staged_fits(p, dtype, format) ? staged_fn(dtype, format, rank) : down_fn<kDownRows / 16, false>(dtype, format, rank);
+        if (int hip = launch_groups(down, groups, kDownThreads, args, stream))
             return hip;
     }
     // workgroups take turns at the items: how many there are is known on the device
     const int64_t blocks = (p.n + kUpWaves * kUpCols - 1) / (kUpWaves * kUpCols);
-    const int64_t most = (most_tiles(p.rows, p.adapters, kUpRows) * blocks + kXcds - 1) / kXcds * kXcds;
+    const int64_t most = most_tiles(p.rows, p.adapters, kUpRows) * blocks;
+    if (most > UINT32_MAX / 2)
+        return kTooManyWorkItems;
     const int64_t groups = std::min<int64_t>(most, kUpGroups);
     const void *up = dtype == SSU_F32 ? up_rank<float>(rank) : dtype == SSU_F16 ? up_rank<_Float16>(rank) : up_rank<__bf16>(rank);
     return launch_groups(up, groups, kUpThreads, args, stream);
