@@ -74,10 +74,11 @@ struct LoraParams {
     void *y;
     int64_t x_s, xs_s, a_l, a_r, b_l, b_n, ids_s, scale_s, y_s;
     int32_t rows, k, n, rank, adapters, ids_i64;
-    int32_t slices, slice;  // of k; set by the launch
+    int32_t slices, slice;  // of k; set by the launch, like the rows of a tile of the second product
+    int32_t up_rows, parts;
     uint8_t *workspace;
 };
-int64_t lora_workspace(int64_t rows, int64_t adapters, int64_t k, int64_t rank);
+int64_t lora_workspace(int64_t rows, int64_t adapters, int64_t k, int64_t n, int64_t rank);
 int launch_add_lora(const LoraParams &p, int dtype, int format, void *stream);
 
 // Beam search: choice of continuations. Strides in elements.

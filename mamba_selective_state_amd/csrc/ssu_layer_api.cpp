@@ -407,10 +407,10 @@ ssu_status_t ssu_token_logprobs(const ssu_logprob_args_t *a, void *workspace, in
 }
 
 int64_t ssu_add_lora_workspace_bytes(const ssu_lora_args_t *a) {
-    if (!a || a->a.ndim != 3 || a->y.ndim != 2 || a->y.size[0] <= 0 || a->y.size[0] > kMostSize || a->a.size[0] <= 0 || a->a.size[1] <= 0 ||
+    if (!a || a->a.ndim != 3 || a->y.ndim != 2 || a->y.size[0] <= 0 || a->y.size[0] > kMostSize || a->y.size[1] < 0 || a->a.size[0] <= 0 || a->a.size[1] <= 0 ||
         a->a.size[1] > SSU_LORA_RANK_MAX || a->a.size[2] < 0 || a->a.size[2] > kMostSize)
         return 0;
-    return ssu::lora_workspace(a->y.size[0], a->a.size[0], a->a.size[2], a->a.size[1]);
+    return ssu::lora_workspace(a->y.size[0], a->a.size[0], a->a.size[2], a->y.size[1], a->a.size[1]);
 }
 
 ssu_status_t ssu_add_lora(const ssu_lora_args_t *a, void *workspace, int64_t workspace_bytes, void *stream) {
