@@ -18,6 +18,7 @@ constexpr int kBeamThreads = 256;
 constexpr int kBeamWaves = kBeamThreads / kWaveLanes;
 constexpr int kTile = kVec * kWaveLanes;  // logits per wave and access
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr int in_flight(int element) { return 16 / element; }  // accesses of a wave: 8 KiB
 
 // Largest logit and the sum over it of a share of a row.
 struct Share {
@@ -48,7 +49,7 @@ __device__ __forceinline__ bool beam_reads(float score, bool ended) {
 // one, and its others only where the second best reaches T too. Of 16 kept about one lane in three workgroups does.
 template <typename T, bool MASK>
 __global__ __launch_bounds__(kBeamThreads, 4) void beam_scan_kernel(const BeamParams p, const BeamSplit sp) {
-    constexpr int kInFlight = 16 / sizeof(T);  // accesses of a wave: 8 KiB
+    constexpr int kInFlight = in_flight(sizeof(T));
     constexpr int kRoom = 512;  // logits that reach T; where there are more, by equal ones, each wave finds its first ones
     __shared__ Share wave_shares[kBeamWaves];
     __shared__ uint32_t heads[kWaveLanes];
@@ -141,9 +142,20 @@ __global__ __launch_bounds__(kBeamThreads, 4) void beam_scan_kernel(const BeamPa
         if (round)
             fetch_round();
     }
-    for (; t < end; t += kBeamWaves) {
-        fetch_part(t, &raw[0], &bits[0]);
-        take(t, raw[0], bits[0], std::false_type());
+    // less than a round of whole accesses, in flight together too
+    for (; t < whole_end; t += kInFlight * kBeamWaves) {
+#pragma unroll
+        for (int u = 0; u < kInFlight; u++)
+            if (t + u * kBeamWaves < whole_end)
+                fetch(t + u * kBeamWaves, &raw[u], &bits[u]);
+#pragma unroll
+        for (int u = 0; u < kInFlight; u++)
+            if (t + u * kBeamWaves < whole_end)
+                take(t + u * kBeamWaves, raw[u], bits[u], std::bool_constant<!MASK>());
+    }
+    if (whole < end && (whole - first) % kBeamWaves == wave) {  // the row's last, not whole
+        fetch_part(whole, &raw[0], &bits[0]);
+        take(whole, raw[0], bits[0], std::false_type());
     }
 
     // T, and the workgroup's sum
@@ -304,7 +316,7 @@ __device__ __forceinline__ int number_before(const Place *places, int n, const P
 }
 
 __global__ __launch_bounds__(kBeamThreads) void beam_join_kernel(const BeamParams p, const BeamSplit sp) {
-    constexpr int kSamples = (kMostSample + kBeamThreads - 1) / kBeamThreads;
+    constexpr int kSamples = (kMostSample + kBeamThreads - 1) / kBeamThreads, kSampleLanes = (kMostSample + kWaveLanes - 1) / kWaveLanes;
     __shared__ double bias[SSU_BEAMS_MAX];   // score - log of the sum over the largest logit
     __shared__ float peak[SSU_BEAMS_MAX];    // that logit
     __shared__ uint8_t kind[SSU_BEAMS_MAX];  // 0: no candidates, 1: its logits', 2: ended
@@ -382,39 +394,68 @@ __global__ __launch_bounds__(kBeamThreads) void beam_join_kernel(const BeamParam
             return Place{score_word(bias[beam]), rest_word(beam, 0, 0)};
         return Place{0, 0};
     };
-    // the `keep`-th of the sample: no continuation behind it is chosen
-    Place mine[kSamples];
+    // A bound below the sample's `keep`-th: no score below it is chosen. Found bit by bit over the scores' leading 24 bits, by each
+    // wave for itself.
+    uint32_t lead[kSampleLanes];
 #pragma unroll
     for (int u = 0; u < kSamples; u++) {
         const int i = u * kBeamThreads + threadIdx.x;
-        if (i < samples) {
-            mine[u] = continuation(i / each, i % each, head[u]);
-            sample[i] = mine[u];
-        }
+        if (i < samples)
+            sample[i] = continuation(i / each, i % each, head[u]);
     }
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kSamples; u++) {
-        const int i = u * kBeamThreads + threadIdx.x;
-        if (i < samples && mine[u].score != 0 && number_before(sample, samples, mine[u]) == p.keep - 1)
-            floor = mine[u];
-    }
-    __syncthreads();
-    const Place last = floor;
-    for (int i = threadIdx.x; i < lists * p.keep; i += kBeamThreads) {
-        const int list = i / p.keep;
-        const Place first = sample[list * each];
-        if (first.score == 0 || before(last, first))
-            continue;  // nothing of it, or its first one stands behind the last that is chosen
-        const uint64_t key = keys[i];
-        const Place c = continuation(list, i - list * p.keep, key);
-        if (c.score != 0 && !before(last, c)) {
-            const int to = atomicAdd(&count, 1);
-            chosen[to] = c;
-            tokens[to] = kind[rest_beam(c.rest)] == 2 ? p.end_token : key_index(key);
+    for (int u = 0; u < kSampleLanes; u++)
+        lead[u] = u * kWaveLanes + lane < samples ? static_cast<uint32_t>(sample[u * kWaveLanes + lane].score >> 32) : 0;
+    uint32_t bound = 0;
+    auto search = [&](auto lanes) {
+#pragma unroll
+        for (int bit = 31; bit >= 8; bit--) {
+            const uint32_t t = bound | (1u << bit);
+            int above = 0;
+#pragma unroll
+            for (int u = 0; u < decltype(lanes)::value; u++)
+                above += __popcll(__ballot(lead[u] >= t));
+            bound = above >= p.keep ? t : bound;
         }
+    };
+    if (samples <= kWaveLanes)
+        search(std::integral_constant<int, 1>());
+    else if (samples <= 3 * kWaveLanes)
+        search(std::integral_constant<int, 3>());
+    else
+        search(std::integral_constant<int, kSampleLanes>());
+    // what reaches it (or, of equal scores, stands before `last`), of all lists whose first one does
+    auto choose = [&](const Place &last) {
+        for (int i = threadIdx.x; i < lists * p.keep; i += kBeamThreads) {
+            const int list = i / p.keep;
+            const Place first = sample[list * each];
+            if (first.score == 0 || first.score >> 32 < bound || before(last, first))
+                continue;
+            const uint64_t key = keys[i];
+            const Place c = continuation(list, i - list * p.keep, key);
+            if (c.score != 0 && c.score >> 32 >= bound && !before(last, c)) {
+                const int to = atomicAdd(&count, 1);
+                if (to < kMostChosen) {
+                    chosen[to] = c;
+                    tokens[to] = kind[rest_beam(c.rest)] == 2 ? p.end_token : key_index(key);
+                }
+            }
+        }
+        __syncthreads();
+    };
+    choose(Place{0, 0});
+    if (count > kMostChosen) {
+        // too many scores are equal, or nearly so: the sample's `keep`-th itself is the bound
+        for (int i = threadIdx.x; i < samples; i += kBeamThreads)
+            if (sample[i].score != 0 && number_before(sample, samples, sample[i]) == p.keep - 1)
+                floor = sample[i];
+        __syncthreads();
+        if (threadIdx.x == 0)
+            count = 0;
+        __syncthreads();
+        choose(floor);
     }
-    __syncthreads();
     const int n = count;
     for (int i = threadIdx.x; i < n; i += kBeamThreads) {
         const Place c = chosen[i];
@@ -432,15 +473,21 @@ __global__ __launch_bounds__(kBeamThreads) void beam_join_kernel(const BeamParam
     }
 }
 
-// Shares of a row and accesses per share.
-constexpr int64_t kGroups = 4096, kFewGroups = 512, kLeastTiles = 32;
-void split(int64_t rows, int64_t beams, int64_t vocab, int32_t *segments, int32_t *per) {
-    const int64_t tiles = (vocab + kTile - 1) / kTile;
-    int64_t s = std::min((kGroups + rows - 1) / rows, tiles / kLeastTiles);
-    s = std::max(s, std::min((kFewGroups + rows - 1) / rows, tiles / kBeamWaves));
-    s = std::max<int64_t>(1, std::min<int64_t>({s, kMostSegments, kMostLists / beams}));
-    *per = static_cast<int32_t>(std::max<int64_t>(1, (tiles + s - 1) / s));
-    *segments = static_cast<int32_t>(std::max<int64_t>(1, (tiles + *per - 1) / *per));
+// Shares of a row and accesses per share: as many workgroups as the chip holds at once, of whole rounds of accesses; few rows
+// go to shares of one access for each wave.
+constexpr int64_t kGroups = 4096, kFewGroups = 512;
+void split(int64_t rows, int64_t beams, int64_t vocab, int dtype, int32_t *segments, int32_t *per) {
+    const int64_t tiles = (vocab + kTile - 1) / kTile, round = in_flight(dtype == SSU_F32 ? 4 : 2) * kBeamWaves;
+    const int64_t most = std::min<int64_t>(kMostSegments, kMostLists / beams);
+    auto whole = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    int64_t s = std::max<int64_t>(1, std::min({whole(kGroups, rows), whole(tiles, round), most}));
+    int64_t each = std::max<int64_t>(1, whole(whole(tiles, s), round) * round);
+    if (rows * whole(tiles, each) < kFewGroups) {
+        s = std::max<int64_t>(1, std::min({whole(kFewGroups, rows), tiles / kBeamWaves, most}));
+        each = std::max<int64_t>(1, whole(tiles, s));
+    }
+    *per = static_cast<int32_t>(each);
+    *segments = static_cast<int32_t>(std::max<int64_t>(1, whole(tiles, each)));
 }
 
 int64_t share_bytes(int64_t shares) { return (shares * static_cast<int64_t>(sizeof(Share)) + 255) / 256 * 256; }
@@ -452,16 +499,16 @@ const void *scan_fn(bool mask) {
 
 }  // namespace
 
-int64_t beam_workspace(int64_t rows, int64_t beams, int64_t vocab, int64_t keep) {
+int64_t beam_workspace(int64_t rows, int64_t beams, int64_t vocab, int64_t keep, int dtype) {
     int32_t s, per;
-    split(rows, beams, vocab, &s, &per);
+    split(rows, beams, vocab, dtype, &s, &per);
     return share_bytes(rows * s) + rows * s * keep * 8;
 }
 
 int launch_beam_select(const BeamParams &p, int dtype, void *stream) {
     BeamSplit sp = {};
     const int64_t rows = p.batch * p.beams;
-    split(rows, p.beams, p.vocab, &sp.segments, &sp.tiles);
+    split(rows, p.beams, p.vocab, dtype, &sp.segments, &sp.tiles);
     sp.shares = reinterpret_cast<Share *>(p.workspace);
     sp.keys = reinterpret_cast<uint64_t *>(p.workspace + share_bytes(rows * sp.segments));
     const void *fn = dtype == SSU_F32   ? scan_fn<float>(p.mask != nullptr)

@@ -94,7 +94,7 @@ struct BeamParams {
     int32_t beams, vocab, keep, end_token;
     uint8_t *workspace;
 };
-int64_t beam_workspace(int64_t rows, int64_t beams, int64_t vocab, int64_t keep);
+int64_t beam_workspace(int64_t rows, int64_t beams, int64_t vocab, int64_t keep, int dtype);
 int launch_beam_select(const BeamParams &p, int dtype, void *stream);
 
 // Beam search: states after the choice. Strides of slots, parents and out in elements, of a

@@ -493,7 +493,7 @@ int64_t ssu_beam_select_workspace_bytes(const ssu_beam_args_t *a) {
         a->scores.ndim != 2 || a->scores.size[1] < 1 || a->scores.size[1] > SSU_BEAMS_MAX || a->out_tokens.ndim != 2 ||
         a->out_tokens.size[1] <= 0 || a->out_tokens.size[1] > SSU_TOP_MAX)
         return 0;
-    return ssu::beam_workspace(a->logits.size[0], a->scores.size[1], a->logits.size[1], a->out_tokens.size[1]);
+    return ssu::beam_workspace(a->logits.size[0], a->scores.size[1], a->logits.size[1], a->out_tokens.size[1], a->logits.dtype);
 }
 
 ssu_status_t ssu_beam_select(const ssu_beam_args_t *a, void *workspace, int64_t workspace_bytes, void *stream) {

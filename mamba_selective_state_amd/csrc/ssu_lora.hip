@@ -102,7 +102,7 @@ __device__ __forceinline__ V moved_down(V v, int s) {
 
 constexpr int kDownRows = 32;  // rows of a down tile
 constexpr int kUpRows = 128;   // rows of an up tile at most
-constexpr int kSelfRows = 2048;
+constexpr int kSelfRows = 256;
 
 struct Tile {
     int32_t adapter, first, count, unused;  // rows perm[first .. first + count)
@@ -393,13 +393,13 @@ template <typename T, typename SRC, int RF, int XF, bool SELF>
 __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(const LoraParams p, const LoraPlan plan) {
     extern __shared__ int dynamic[];
     __shared__ f32x4 sums[kDownWaves * 4 * 64];
-    constexpr int kScan = kSelfRows / kDownThreads;
+    constexpr int kScan = (kSelfRows + kDownThreads - 1) / kDownThreads;
     __shared__ int mine[SELF ? kSelfRows : 1];
     __shared__ int counts[SELF ? kScan * kDownWaves : 1];
     int id = static_cast<int>(blockIdx.x);
     if constexpr (SELF) {
         if (id == 0) {
-            make_plan<kDownThreads, kSelfRows / kDownThreads>(p, plan, dynamic);
+            make_plan<kDownThreads, kScan>(p, plan, dynamic);
             return;
         }
         id--;
@@ -1060,8 +1060,8 @@ int launch_add_lora(const LoraParams &params, int dtype, int format, void *strea
     const unsigned counters = static_cast<unsigned>(p.adapters) * 4;
     void *args[] = {&p, &plan};
     if (p.rows <= kSelfRows) {
-        // An adapter's rows go to several workgroups if even shares are more than one pass of 32: what has none costs its scan
-        // (2048 rows of 64 adapters, MXFP8: 12.3 us, in four parts 18; 777 of 13: 9 us, in parts 5.5).
+        // An adapter's rows go to several workgroups if even shares are more than one pass of 32. A workgroup that has none costs its
+        // scan: 2048 rows of 64 adapters took 12.3 us in one part each, in four 18; 777 of 13 9 us, in four parts 5.5.
         const int64_t each = std::min<int64_t>(p.rows, p.adapters);
         p.parts = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(kMostParts, p.rows / (each * 24))));
         const int64_t groups = 1 + each * p.slices * p.parts;

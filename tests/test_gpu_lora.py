@@ -75,7 +75,7 @@ def test_outputs(n, dt):
     check(run(c, scale=False), c, scale=False)
 
 
-@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 33, 127, 128, 129, 511, 513, 2047, 2048, 2049, 5000])
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 33, 127, 128, 129, 255, 256, 257, 511, 513, 2047, 2048, 2049, 5000])
 @pytest.mark.parametrize("adapters", [1, 3, 50])
 @pytest.mark.parametrize("order", ["mixed", "runs"])
 def test_rows_and_adapters(rows, adapters, order):
@@ -89,7 +89,7 @@ def test_many_adapters(rows):
     check(run(c), c)
 
 
-@pytest.mark.parametrize("rows,rank", [(60, 16), (60, 128), (2500, 16), (2500, 64), (2500, 128)])
+@pytest.mark.parametrize("rows,rank", [(60, 16), (60, 128), (250, 20), (250, 64), (2500, 16), (2500, 64), (2500, 128)])
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 def test_large_inner_and_ranks(rows, rank, dt):
     c = inputs(rows, 2100, 130, rank, 5, dt, seed=rank, order="runs")
@@ -104,6 +104,42 @@ def test_codes(fmt, rows, k, rank):
     codes, scales = ssu.mx_quantize(x.cuda(), fmt)
     v = R.decode(codes, scales, fmt)
     check(run(c, x=(codes, scales)), c, x=v)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rank", [16, 32, 64, 128])
+@pytest.mark.parametrize("k", [128, 512, 648, 4096, 4104])
+def test_many_rows_in_whole_lines(dt, rank, k):
+    """Rows that LDS-DMA can fetch: whole stages, an end that is none, several slices of k."""
+    c = inputs(300, k, 136, rank, 3, dt, seed=k + rank)
+    check(run(c), c)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("rank", [16, 32, 64, 128])
+@pytest.mark.parametrize("k", [128, 640, 4096, 4192])
+def test_many_rows_of_codes(fmt, rank, k):
+    c = inputs(300, k, 70, rank, 3, "bf16", seed=k + rank)
+    x = torch.randn(300, k, generator=torch.Generator().manual_seed(k)) * 3
+    x[7, 40] = math.inf  # a block of NaNs, in a row that no adapter takes
+    c["adapter"][7] = -1
+    codes, scales = ssu.mx_quantize(x.cuda(), fmt)
+    v = R.decode(codes, scales, fmt)
+    check(run(c, x=(codes, scales)), c, x=v)
+
+
+@pytest.mark.parametrize("rows", [200, 1500])
+def test_few_of_many_adapters(rows):
+    """Most rows of one adapter, most adapters without a row, and rows before the matrix that LDS-DMA cannot fetch whole."""
+    c = inputs(rows, 256, 300, 16, 64, "bf16", seed=rows, none=0.05)
+    c["adapter"][c["adapter"] >= 0] = 37
+    c["adapter"][::50] = 3
+    check(run(c), c)
+    wide = torch.zeros(rows, 259, dtype=torch.bfloat16)
+    wide[:, 1:257] = c["x"]
+    d = {k: v.cuda() for k, v in c.items()}
+    y = ssu.add_lora(d["y"], wide.cuda()[:, 1:257], d["a"], d["b"], d["adapter"], d["scale"])
+    check(y.cpu(), c)
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
