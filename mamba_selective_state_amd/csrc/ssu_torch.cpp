@@ -391,6 +391,8 @@ PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
         ssu_beam_args_t args = {};
         describe_rows(logits, dev, "logits", &args.logits);
         describe(scores, dev, &args.scores);
+        if (logits.dim() > 2 && (logits.dim() != 3 || scores.dim() != 2 || logits.size(0) != scores.size(0) || logits.size(1) != scores.size(1)))
+            raise(PyExc_ValueError, "logits must be [batch, beams, vocab] or [batch * beams, vocab], scores [batch, beams]");
         if (finished) {
             if (finished->scalar_type() == at::kBool)  // a byte each, 0 or 1
                 describe(finished->view(at::kByte), dev, &args.finished);

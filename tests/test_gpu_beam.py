@@ -166,6 +166,35 @@ def test_equal_scores(vocab, dt):
     assert r.parents.tolist() == [[0] * 32] * 2 and r.tokens.tolist() == [list(range(32))] * 2
 
 
+@pytest.mark.parametrize("beams", [3, 64])
+def test_all_equal(beams):
+    """More equal scores than the second kernel has room for: 64 beams of many shares each."""
+    d = torch.zeros(beams, 40000, dtype=torch.bfloat16, device="cuda")
+    say("all equal", beams)
+    r = ssu.beam_select(d, torch.zeros(1, beams, device="cuda"), 32)
+    assert r.parents.tolist() == [[0] * 32] and r.tokens.tolist() == [list(range(32))]
+    assert torch.allclose(r.scores.cpu(), torch.full((1, 32), -math.log(40000)), atol=1e-5)
+    # Beams in pairs of equal scores, one token each that stands out: it scores 5 - i // 2 - L, L = log(39999 + e^5), and beam 0's
+    # and 1's other tokens score -L. So the first ten (fewer where there are fewer beams) are known, and all that follow
+    # score -L, whichever of equal ones they are.
+    at = torch.randint(0, 40000, (beams,), generator=torch.Generator().manual_seed(beams))
+    d[torch.arange(beams), at] = 5
+    scores = -(torch.arange(beams) // 2).float()[None]
+    n, first = min(32, beams), min(10, beams)
+    r = ssu.beam_select(d, scores.cuda(), n)
+    assert r.parents[0, :first].tolist() == list(range(first))
+    assert torch.equal(r.tokens[0, :first].cpu().long(), at[:first])
+    want = torch.tensor([max(5 - i // 2, 0) for i in range(n)]) - math.log(39999 + math.exp(5))
+    assert torch.allclose(r.scores[0].cpu(), want, atol=1e-5)
+
+
+def test_shapes_that_do_not_agree():
+    x = torch.zeros(3, 4, 50, device="cuda")
+    for logits, scores in ((x, (4, 3)), (x, (12, 1)), (x.view(1, 3, 4, 50), (3, 4)), (x.view(12, 50), (3, 5))):
+        with pytest.raises(ValueError):
+            ssu.beam_select(logits, torch.zeros(scores, device="cuda"), 2)
+
+
 def test_extreme_logits():
     c = inputs(2, 2, 1500, "f32")
     c["logits"][0] = -3e38
