@@ -2,9 +2,14 @@
 //   h = x A_i^T (down: k to rank),   y += (scale_i h) B_i^T (up: rank to n),   i the row's adapter.
 //
 // Rows of one adapter are worked on together, so that each adapter's weights are read once for up to a tile of rows.
-// Which rows these are is found on the device: lora_plan makes lists of tiles (an adapter and a run of `perm`).
+// Which rows these are is found on the device: make_plan makes lists of tiles (an adapter and a run of `perm`).
 // Up to kSelfRows rows, the down kernel's workgroups look their rows up for themselves, and one more workgroup makes the
-// plan for the up kernel in the meantime: two launches. More rows: plan, down, up.
+// plan for the up kernel in the meantime: two launches. More rows: plan, down, up. 256 rows of 48 adapters (8192 -> 4096, rank
+// 16) take 7.2 + 6.0 us in two launches; at 512 rows of 4 adapters among 64 the two launches took 22 + 5.5 us, since a workgroup takes an
+// adapter's rows one pass after another, and three take 4.6 + 5 + 5.5.
+//
+// Bytes bound it, y's above all (read and written): 8192 rows, 4096 -> 18560, rank 64, bf16 8 + 35 + 138 us (608 MB of y at
+// 4.4 TB/s), 2048 rows of MXFP8, rank 16, 64 adapters 6 + 8 + 41 (152 MB of y, 46 MB of weights).
 //
 // Rows of other adapters never meet a weight, not even times zero: what one adapter's weights hold (NaN, infinity) stays with
 // its rows. h is f32 in the workspace; the up kernel splits 16-bit types' h into two summands of that type, hi + lo,
@@ -472,8 +477,8 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(const LoraParam
 // ---------------------------------------------------------------- down, many rows
 //
 // Tiles of the plan, through LDS: a stage is 256 bytes (128 or, in f32, 64 values of k) of 32 rows of x and of all rank rows, which
-// LDS-DMA brings in whole lines, two stages ahead. With operands straight from memory, 64 bytes of 16 rows for each access, 8192 x 4096
-// bf16 of rank 64 took 50 us.
+// LDS-DMA brings in whole lines, two stages ahead. 8192 x 4096 bf16 of rank 64 take 35 us (67 MB of x, and A once for each 32 rows, 134 MB
+// from the L2s); with operands straight from memory, 64 bytes of 16 rows for each access, 50.
 //
 // Chunk c (16 bytes) of row r is at place c ^ r of its row, so that the 16 rows of an operand are read from different banks.
 
@@ -702,7 +707,8 @@ __device__ __forceinline__ void split_value(float v, T *hi, T *lo) {
 // rows, 16 at a time.
 //
 // Here h's rows go first and the weights second: lane l has results of rows 4 (l / 16) .. + 3, and fragment f's column l % 16 is
-// output 4 (l % 16) + f of the wave's, so that 16 lanes in a row have 64 outputs in a row of one row of y.
+// output 4 (l % 16) + f of the wave's, so that 16 lanes in a row have 64 outputs in a row of one row of y. With rows in the lanes, 16
+// lines for every 16 lanes, 8192 x 18560 bf16 of rank 64 took 200 us instead of 138.
 template <typename T, int R>
 __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void lora_up_kernel(const LoraParams p, const LoraPlan plan) {
     constexpr int N = 4;                     // outputs of a lane and row
@@ -959,7 +965,8 @@ int64_t most_tiles(int64_t rows, int64_t adapters, int64_t tile) { return rows /
 int64_t whole(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 constexpr int64_t kUpGroups = 8192;
-// Slices of k: enough workgroups for the chip, none with less than kLeastSlice values.
+// Slices of k: enough workgroups for the chip, none with less than kLeastSlice values. Every item of the second product adds the
+// slices up: 256 rows of 64 adapters, 8192 -> 4096, take 7.3 + 5.8 us with four slices and 7.0 + 6.8 with eight.
 constexpr int64_t kMostParts = 8;
 constexpr int64_t kLeastSlice = 512, kSelfGroups = 256, kDownGroups = 512, kMostSlices = 4;
 void slices_of(int64_t rows, int64_t adapters, int64_t k, int32_t *slices, int32_t *slice) {
@@ -1020,7 +1027,8 @@ const void *up_rank(int rank) {
                         : reinterpret_cast<const void *>(&lora_up_kernel<T, 128>);
 }
 
-// Rows of an up tile: shorter ones where there would be too few items for the chip.
+// Rows of an up tile: shorter ones where there would be too few items for the chip (622 rows of 11 adapters, 2049 outputs: 8.4 us, with
+// 128 rows 12).
 constexpr int64_t kFewItems = 1024;
 int up_rows_of(int64_t rows, int64_t n) {
     const int64_t blocks = (n + kUpWaves * kUpCols - 1) / (kUpWaves * kUpCols);

@@ -3,7 +3,8 @@
 // The first successor of a beam goes on in its slot; only further ones are copied, into the slots of beams without a
 // successor. As many are left as are needed, and nothing reads them, so the copies have no order: every workgroup
 // finds them for itself from the request's row of parents (a ballot for each beam) and copies its piece of the slot for each. The
-// bytes of the copied slots bound it, read and written once.
+// bytes of the copied slots bound it, read and written once: 24 slots of 2.1 MB in each of eight layers (829 MB) take 144 us, 5.7 TB/s,
+// some of it from the last-level cache; a copy of 1 GiB reaches 5.2. A piece is what the workgroup's lanes have in flight together, 16 KiB.
 #include <algorithm>
 
 #include "ssu_layer_device.h"

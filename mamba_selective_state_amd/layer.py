@@ -274,7 +274,8 @@ def add_lora(y, x, lora_a, lora_b, adapter, scale=None):
 
     x [..., k] is what the projection took: floats of y's dtype, or (y in bfloat16) a pair (codes, scales) from
     add_rms_norm or mx_quantize. lora_a [adapters, rank, k] and lora_b [adapters, n, rank] have y's dtype (float32,
-    float16 or bfloat16); rank is at most 128, smaller ones are padded with zeros by the caller or kept in groups of their own.
+    float16 or bfloat16); rank is at most 128; adapters of smaller ranks have zeros
+    in their last rows of lora_a or columns of lora_b.
     adapter: int32 or int64, one per row, in any order; a row whose number is none of [0, adapters), such as -1, keeps
     its values. scale: float32 [adapters]. Sums are kept in float32, and y is rounded once more."""
     x_scale, fmt = None, FORMAT_SAME
