@@ -8,8 +8,8 @@
 // 16) take 7.2 + 6.0 us in two launches; at 512 rows of 4 adapters among 64 the two launches took 22 + 5.5 us, since a workgroup takes an
 // adapter's rows one pass after another, and three take 4.6 + 5 + 5.5.
 //
-// Bytes bound it, y's above all (read and written): 8192 rows, 4096 -> 18560, rank 64, bf16 8 + 35 + 138 us (608 MB of y at
-// 4.4 TB/s), 2048 rows of MXFP8, rank 16, 64 adapters 6 + 8 + 41 (152 MB of y, 46 MB of weights).
+// Bytes bound it, y's above all (read and written): 8192 rows, 4096 -> 18560, rank 64, bf16 8 + 21 + 144 us (608 MB of y at
+// 4.2 TB/s), 2048 rows of MXFP8, rank 16, 64 adapters 6 + 7 + 39 (152 MB of y, 46 MB of weights).
 //
 // Rows of other adapters never meet a weight, not even times zero: what one adapter's weights hold (NaN, infinity) stays with
 // its rows. h is f32 in the workspace; the up kernel splits 16-bit types' h into two summands of that type, hi + lo,
@@ -477,8 +477,8 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(const LoraParam
 // ---------------------------------------------------------------- down, many rows
 //
 // Tiles of the plan, through LDS: a stage is 256 bytes (128 or, in f32, 64 values of k) of 32 rows of x and of all rank rows, which
-// LDS-DMA brings in whole lines, two stages ahead. 8192 x 4096 bf16 of rank 64 take 35 us (67 MB of x, and A once for each 32 rows, 134 MB
-// from the L2s); with operands straight from memory, 64 bytes of 16 rows for each access, 50.
+// LDS-DMA brings in whole lines, two stages ahead. 8192 x 4096 bf16 of rank 64 take 21 us (67 MB of x, part of it from the last-level cache, and A once for each 32 rows, 134 MB
+// from the L2s), 35 with x from HBM; with operands straight from memory, 64 bytes of 16 rows for each access, 50.
 //
 // Chunk c (16 bytes) of row r is at place c ^ r of its row, so that the 16 rows of an operand are read from different banks.
 
@@ -709,7 +709,11 @@ __device__ __forceinline__ void split_value(float v, T *hi, T *lo) {
 // Here h's rows go first and the weights second: lane l has results of rows 4 (l / 16) .. + 3, and fragment f's column l % 16 is
 // output 4 (l % 16) + f of the wave's, so that 16 lanes in a row have 64 outputs in a row of one row of y. With rows in the lanes, 16
 // lines for every 16 lanes, 8192 x 18560 bf16 of rank 64 took 200 us instead of 138.
-template <typename T, int R>
+//
+// PAST: y goes past the caches both ways, which keep x and the weights: 8192 x 18560 of rank 64 with the first product 184
+// us, so 174 (with the writes alone 184). Rows that share lines (an odd number of outputs) need the caches: 777 x 2049
+// f16 18.6 us, past them 20.0.
+template <typename T, int R, bool PAST>
 __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void lora_up_kernel(const LoraParams p, const LoraPlan plan) {
     constexpr int N = 4;                     // outputs of a lane and row
     constexpr int KB = R < 32 ? 1 : R / 32;  // operands of 32 along the rank
@@ -778,12 +782,23 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
         const f32x4 h0 = h_at(__shfl(row_lo, h_first));
         T *y = static_cast<T *>(p.y) + col0 + N * r;
         Y v[4];  // a chunk's outputs, as they are until they are used
+        auto read_y = [](const T *at) -> Y {
+            const AnyY *y = reinterpret_cast<const AnyY *>(at);
+            return PAST ? __builtin_nontemporal_load(y) : *y;
+        };
+        auto write_y = [](T *at, const Y &value) {
+            AnyY *y = reinterpret_cast<AnyY *>(at);
+            if constexpr (PAST)
+                __builtin_nontemporal_store(static_cast<AnyY>(value), y);
+            else
+                *y = value;
+        };
         T *to[4];
         if (kAhead && whole) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 to[i] = y + __shfl(row_lo, 4 * g + i) * p.y_s;
-                v[i] = *reinterpret_cast<const AnyY *>(to[i]);
+                v[i] = read_y(to[i]);
             }
         }
         __syncthreads();  // the last item's h and rows have been read
@@ -890,7 +905,7 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
             places(c, to);
 #pragma unroll
             for (int i = 0; i < 4; i++)
-                v[i] = *reinterpret_cast<const AnyY *>(to[i]);
+                v[i] = read_y(to[i]);
         };
         int c = 0;
         if (whole) {
@@ -904,12 +919,12 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
                         places(c + 16, next_to);
 #pragma unroll
                         for (int i = 0; i < 4; i++)
-                            next[i] = *reinterpret_cast<const AnyY *>(next_to[i]);
+                            next[i] = read_y(next_to[i]);
                     }
                     add(c);
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        *reinterpret_cast<AnyY *>(to[i]) = v[i];
+                        write_y(to[i], v[i]);
                         to[i] = next_to[i];
                         v[i] = next[i];
                     }
@@ -918,7 +933,7 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
                     add(c);
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        *reinterpret_cast<AnyY *>(to[i]) = v[i];
+                        write_y(to[i], v[i]);
                 }
             }
             if (c < t.count) {
@@ -928,7 +943,7 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
 #pragma unroll
                 for (int i = 0; i < 4; i++)
                     if (c + 4 * g + i < t.count)
-                        *reinterpret_cast<AnyY *>(to[i]) = v[i];
+                        write_y(to[i], v[i]);
             }
         } else {
             const int past = max(0, N - left);  // how far the lane's outputs reach past the row's end
@@ -1019,12 +1034,20 @@ bool staged_fits(const LoraParams &p, int dtype, int format) {
         return false;
     return whole16(p.x) && whole16(p.a) && p.x_s * x_unit % 16 == 0 && p.a_l * unit % 16 == 0 && p.a_r * unit % 16 == 0;
 }
-template <typename T>
+template <typename T, bool PAST>
 const void *up_rank(int rank) {
-    return rank == 16   ? reinterpret_cast<const void *>(&lora_up_kernel<T, 16>)
-           : rank == 32 ? reinterpret_cast<const void *>(&lora_up_kernel<T, 32>)
-           : rank == 64 ? reinterpret_cast<const void *>(&lora_up_kernel<T, 64>)
-                        : reinterpret_cast<const void *>(&lora_up_kernel<T, 128>);
+    return rank == 16   ? reinterpret_cast<const void *>(&lora_up_kernel<T, 16, PAST>)
+           : rank == 32 ? reinterpret_cast<const void *>(&lora_up_kernel<T, 32, PAST>)
+           : rank == 64 ? reinterpret_cast<const void *>(&lora_up_kernel<T, 64, PAST>)
+                        : reinterpret_cast<const void *>(&lora_up_kernel<T, 128, PAST>);
+}
+template <bool PAST>
+const void *up_fn(int dtype, int rank) {
+    return dtype == SSU_F32 ? up_rank<float, PAST>(rank) : dtype == SSU_F16 ? up_rank<_Float16, PAST>(rank) : up_rank<__bf16, PAST>(rank);
+}
+// Whether y's rows begin at whole lines.
+bool whole_lines(const LoraParams &p, int dtype) {
+    return reinterpret_cast<uintptr_t>(p.y) % 128 == 0 && p.y_s * (dtype == SSU_F32 ? 4 : 2) % 128 == 0;
 }
 
 // Rows of an up tile: shorter ones where there would be too few items for the chip (622 rows of 11 adapters, 2049 outputs: 8.4 us, with
@@ -1091,7 +1114,7 @@ int launch_add_lora(const LoraParams &params, int dtype, int format, void *strea
     if (most > UINT32_MAX / 2)
         return kTooManyWorkItems;
     const int64_t groups = std::min<int64_t>(most, kUpGroups);
-    const void *up = dtype == SSU_F32 ? up_rank<float>(rank) : dtype == SSU_F16 ? up_rank<_Float16>(rank) : up_rank<__bf16>(rank);
+    const void *up = whole_lines(p, dtype) ? up_fn<true>(dtype, rank) : up_fn<false>(dtype, rank);
     return launch_groups(up, groups, kUpThreads, args, stream);
 }
 
