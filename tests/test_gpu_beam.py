@@ -95,6 +95,11 @@ def test_beams_and_keep(batch, beams, keep):
     check(run(c, keep), c, keep)
 
 
+def test_large_batch():
+    c = inputs(1500, 4, 33, "f16", seed=8, ended=True)
+    check(run(c, 8, end_token=3), c, 8, 3)
+
+
 @pytest.mark.parametrize("mask", [None, "one", "rows"])
 @pytest.mark.parametrize("vocab", [5, 100, 3001])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])

@@ -83,6 +83,12 @@ def test_rows_and_adapters(rows, adapters, order):
     check(run(c), c)
 
 
+@pytest.mark.parametrize("rows,adapters,order", [(8191, 3, "mixed"), (8193, 1, "runs"), (20000, 40, "mixed"), (20000, 4096, "mixed"), (30001, 9, "runs")])
+def test_more_rows_than_the_lists_take_at_once(rows, adapters, order):
+    c = inputs(rows, 64, 40, 4, adapters, "bf16", seed=rows + adapters, order=order)
+    check(run(c), c)
+
+
 @pytest.mark.parametrize("rows", [1, 4, 700, 3000])
 def test_many_adapters(rows):
     c = inputs(rows, 64, 24, 4, 4096, "f16", seed=rows)

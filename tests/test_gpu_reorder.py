@@ -86,6 +86,11 @@ def test_numbers_out_of_range():
     check(pools, slots, parents, index=torch.int64)
 
 
+def test_large_batch():
+    say("3000 requests")
+    check(*inputs(3000, 3, [((5, 3), torch.bfloat16)], seed=12, low=-1))
+
+
 def test_many_pools():
     """More than one launch takes."""
     pools, slots, parents = inputs(2, 4, [((i + 1,), torch.uint8) for i in range(150)], seed=4)
