@@ -979,11 +979,11 @@ int padded_rank(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank 
 int64_t most_tiles(int64_t rows, int64_t adapters, int64_t tile) { return rows / tile + std::min(rows, adapters); }
 int64_t whole(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
-constexpr int64_t kUpGroups = 8192;
+constexpr int64_t kUpGroups = 8192;  // some times what the chip holds at once
 // Slices of k: enough workgroups for the chip, none with less than kLeastSlice values. Every item of the second product adds the
 // slices up: 256 rows of 64 adapters, 8192 -> 4096, take 7.3 + 5.8 us with four slices and 7.0 + 6.8 with eight.
-constexpr int64_t kMostParts = 8;
 constexpr int64_t kLeastSlice = 512, kSelfGroups = 256, kDownGroups = 512, kMostSlices = 4;
+constexpr int64_t kMostParts = 8;
 void slices_of(int64_t rows, int64_t adapters, int64_t k, int32_t *slices, int32_t *slice) {
     const int64_t tiles = rows <= kSelfRows ? std::min(rows, adapters) : most_tiles(rows, adapters, kDownRows);
     const int64_t groups = rows <= kSelfRows ? kSelfGroups : kDownGroups;
@@ -1087,6 +1087,11 @@ int launch_add_lora(const LoraParams &params, int dtype, int format, void *strea
     LoraPlan plan = {reinterpret_cast<int32_t *>(p.workspace), reinterpret_cast<Tile *>(p.workspace + o.up),
                      reinterpret_cast<Tile *>(p.workspace + o.down), reinterpret_cast<int32_t *>(p.workspace + o.perm),
                      reinterpret_cast<float *>(p.workspace + o.h)};
+    // refused before anything is enqueued
+    const int64_t blocks = (p.n + kUpWaves * kUpCols - 1) / (kUpWaves * kUpCols);
+    const int64_t most = most_tiles(p.rows, p.adapters, p.up_rows) * blocks;
+    if (most > UINT32_MAX / 2 || most_tiles(p.rows, p.adapters, kDownRows) * p.slices > UINT32_MAX / kDownThreads)
+        return kTooManyWorkItems;
     const int rank = padded_rank(p.rank);
     const unsigned counters = static_cast<unsigned>(p.adapters) * 4;
     void *args[] = {&p, &plan};
@@ -1109,10 +1114,6 @@ int launch_add_lora(const LoraParams &params, int dtype, int format, void *strea
             return hip;
     }
     // workgroups take turns at the items: how many there are is known on the device
-    const int64_t blocks = (p.n + kUpWaves * kUpCols - 1) / (kUpWaves * kUpCols);
-    const int64_t most = most_tiles(p.rows, p.adapters, p.up_rows) * blocks;
-    if (most > UINT32_MAX / 2)
-        return kTooManyWorkItems;
     const int64_t groups = std::min<int64_t>(most, kUpGroups);
     const void *up = whole_lines(p, dtype) ? up_fn<true>(dtype, rank) : up_fn<false>(dtype, rank);
     return launch_groups(up, groups, kUpThreads, args, stream);

@@ -134,6 +134,20 @@ def test_many_rows_of_codes(fmt, rank, k):
     check(run(c, x=(codes, scales)), c, x=v)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("rows", [40, 300])
+def test_codes_off_any_alignment(fmt, rows):
+    c = inputs(rows, 608, 70, 16, 3, "bf16", seed=rows)
+    x = torch.randn(rows, 608, generator=torch.Generator().manual_seed(2))
+    codes, scales = ssu.mx_quantize(x.cuda(), fmt)
+    v = R.decode(codes, scales, fmt)
+    wide = torch.full((rows, codes.shape[1] + 13), 0x7F, dtype=torch.uint8, device="cuda")
+    wide[:, 3:3 + codes.shape[1]] = codes
+    wide_scales = torch.full((rows, 27), 255, dtype=torch.uint8, device="cuda")
+    wide_scales[:, 5:24] = scales
+    check(run(c, x=(wide[:, 3:3 + codes.shape[1]], wide_scales[:, 5:24])), c, x=v)
+
+
 @pytest.mark.parametrize("rows", [200, 1500])
 def test_few_of_many_adapters(rows):
     """Most rows of one adapter, most adapters without a row, and rows before the matrix that LDS-DMA cannot fetch whole."""

@@ -158,6 +158,13 @@ def test_lora_empty_calls_and_workspace():
             assert need(ctypes.byref(lora_args(rows=rows, rank=rank))) >= rows * (4 + 4 * padded)
 
 
+def test_lora_too_large_for_one_launch():
+    """2^30 rows of 2^31 outputs: more tiles than one launch has numbers for."""
+    a = lora_args(rows=2 ** 30, n=2 ** 31 - 70000)
+    need = S._lib.ssu_add_lora_workspace_bytes(ctypes.byref(a))
+    assert refused(S._lib.ssu_add_lora, a, "more rows or outputs than one launch takes", (ctypes.c_void_p(FAKE), need, None)) == S.ERR_NOT_IMPLEMENTED
+
+
 # ---------------------------------------------------------------- beam_select
 
 def beam_args(batch=2, beams=3, vocab=50, keep=4, dt=S.BF16):
