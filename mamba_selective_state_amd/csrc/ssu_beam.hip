@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kBeamThreads, 4) void beam_scan_kernel(const BeamPa
         }
     };
     Share w = {kLowest, 0.0f};  // m: of the wave
-    float m1 = kLowest, m2 = kLowest;
+    float m1 = -__builtin_inff(), m2 = -__builtin_inff();  // nothing yet: below the lowest finite logit, which counts like any other
     int best_at = first + wave;
     auto take = [&](int t, const Raw &raw, uint32_t bits, auto all) {
         float x[kVec];
@@ -202,11 +202,11 @@ __global__ __launch_bounds__(kBeamThreads, 4) void beam_scan_kernel(const BeamPa
                 to++;
             }
     };
-    if (m1 >= bound && m1 > kLowest) {
+    if (m1 >= bound) {
         fetch_part(best_at, &raw[0], &bits[0]);
         append(best_at, raw[0], bits[0]);
     }
-    const bool more = m2 >= bound && m2 > kLowest;
+    const bool more = m2 >= bound;
     if (__ballot(more)) {
         t = first + wave;
         for (; t + (kInFlight - 1) * kBeamWaves < whole_end; t += kInFlight * kBeamWaves)
