@@ -574,7 +574,7 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_staged_kernel(const Lo
             const int swap = kXRow == 256 ? row % 16 : kXRow == 128 ? row % 16 / 2 : row % 16 / 4;
             const int64_t stride = kCodes ? p.x_s : p.x_s * kUnit;
             src[i] = static_cast<const uint8_t *>(p.x) + plan.perm[t.first + min(row, t.count - 1)] * stride +
-                     begin / kDepth * kXRow + (slot ^ swap) * 16;
+                     static_cast<int64_t>(begin / kDepth) * kXRow + (slot ^ swap) * 16;
             advance[i] = kXRow;
         } else if (kCodes && fill >= kWhole) {
             src[i] = p.x_scale + plan.perm[t.first + min(lane % kDownRows, t.count - 1)] * p.xs_s + begin / 32;
