@@ -581,8 +581,9 @@ SSU_API ssu_status_t ssu_token_logprobs(const ssu_logprob_args_t *args, void *wo
  *   y        [rows, n], a's dtype, last stride 1: read and written; overlaps nothing else
  *   x_format SSU_FORMAT_SAME, or the codes' SSU_FORMAT_MXFP8 / SSU_FORMAT_MXFP4 (k a multiple of 32)
  * rank is at most SSU_LORA_RANK_MAX, adapters at most SSU_LORA_ADAPTERS_MAX. Both products are summed in f32; x a^T reaches
- * the second one as f32, or as two summands of the 16-bit type (16 bits of it in bf16, 22 in f16, or what is above
- * 2^-24 of the row's largest); y is rounded once.
+ * the second one as f32, or as two summands of the 16-bit type (16 bits of it in bf16, but 8 for weights of 2^64 or more
+ * at ranks up to 16; 22 in f16, or what is above 2^-24 of the row's largest); y is rounded once. Infinite weights
+ * give what they give in f32.
  * `workspace`: as for ssu_mx_linear. Two or three kernels. */
 #define SSU_LORA_RANK_MAX 128
 #define SSU_LORA_ADAPTERS_MAX 4096

@@ -694,10 +694,12 @@ constexpr int kUpThreads = 256;
 constexpr int kUpWaves = kUpThreads / kWaveLanes;
 constexpr int kUpCols = 64;  // of a wave
 
-// A value as two summands of T.
+// A value as two summands of T, the first of the value's sign: in f16 what is too small for one is the smallest less itself.
 template <typename T>
 __device__ __forceinline__ void split_value(float v, T *hi, T *lo) {
     *hi = narrow<T>(v);
+    if constexpr (std::is_same_v<T, _Float16>)
+        *hi = *hi == static_cast<T>(0.0f) && v != 0.0f ? static_cast<T>(copysignf(0x1p-24f, v)) : *hi;
     const float w = widen(*hi);
     *lo = narrow<T>(fabsf(w) < __builtin_inff() ? v - w : 0.0f);
 }
@@ -727,13 +729,19 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
     // it and 145 with it and three waves, 2048 x 18560 of rank 16 48 and 42
     constexpr bool kAhead = R <= 32;
     constexpr bool kScaled = std::is_same_v<T, _Float16>;
+    // lo times an infinite weight is NaN where lo is 0, and an infinity of lo's sign otherwise; hi has h's sign. Products beyond f32's range
+    // are the same. So where a sum is NaN, it is that of hi alone. A look at every sum took 2048 x 18560 of rank 16 from 53.4 to 57
+    // us; there, where hi and lo have weights of their own, lo's are 0 for infinite ones (in bf16 from 2^64 on: 8 bits of h are left for them),
+    // and bf16 rows of an h of 2^64 or more are taken by 2^-100 through the products: 54.1 us.
+    constexpr bool kLook = kSplit && !kBoth, kLess = kBoth && !kScaled;
+    constexpr float kLarge = kScaled ? __builtin_inff() : 0x1p64f;
     typedef T Y __attribute__((ext_vector_type(N)));
     typedef T AnyY __attribute__((ext_vector_type(N), aligned(sizeof(T))));
     typedef int64_t L2 __attribute__((ext_vector_type(2)));
     __shared__ alignas(16) uint8_t staged[std::max(kUpRows * kHRow, kUpWaves * kUpCols * kBRow)];
     __shared__ alignas(16) int64_t y_rows[kUpRows];  // where the rows are in y
     __shared__ int32_t rows[kUpRows];
-    __shared__ alignas(16) float units[kScaled ? kUpRows : 4];
+    __shared__ alignas(16) float units[kScaled || kLess ? kUpRows : 4];  // what the rows' sums are multiplied by
     const int lane = threadIdx.x % kWaveLanes, wave = threadIdx.x / kWaveLanes;
     const int r = lane % 16, g = lane / 16;
     uint8_t *b_rows = staged + wave * kUpCols * kBRow, *h_rows = staged;
@@ -812,6 +820,19 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
             const int q = u * kWaveLanes + lane;
             *reinterpret_cast<Frag<T> *>(b_rows + q / kPieces * kBRow + q % kPieces * 8 * static_cast<int>(sizeof(T))) = piece[u];
         }
+        bool past = false;  // whether a weight of the wave's is large
+        if constexpr (kBoth) {
+            typedef uint16_t U2 __attribute__((ext_vector_type(2)));
+            U2 most = {0, 0};
+#pragma unroll
+            for (int u = 0; u < kPieces; u++) {
+                const u32x4 bits = __builtin_bit_cast(u32x4, piece[u].v);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    most = __builtin_elementwise_max(most, __builtin_bit_cast(U2, bits[i] & 0x7FFF7FFFu));
+            }
+            past = __ballot(max(most.x, most.y) >= __builtin_bit_cast(uint16_t, static_cast<T>(kLarge))) != 0;
+        }
         wave_lds_fence();
         Frag<T> w[N][KB];
 #pragma unroll
@@ -824,6 +845,13 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
                 else
                     w[f][kb] = zero_frag<T>();
             }
+        if (kBoth && past) {
+#pragma unroll
+            for (int f = 0; f < N; f++)
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    w[f][0].v[i] = g < 2 || fabsf(widen(w[f][0].v[i])) < kLarge ? w[f][0].v[i] : static_cast<T>(0.0f);
+        }
         __syncthreads();
         // h, 16 bytes of a row for each lane, whole lines by lanes in a row
         const float scale = p.scale ? p.scale[t.adapter * p.scale_s] : 1.0f;
@@ -842,6 +870,17 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
                 const int e = m > 0.0f && m < __builtin_inff() ? min(max(__builtin_amdgcn_frexp_expf(m), -100), 126) : 0;
                 inv = ldexpf(1.0f, -e);
                 units[row] = ldexpf(1.0f, e);
+            }
+            if constexpr (kLess) {
+                float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))), unit = 1.0f;
+                if (__ballot(m >= kLarge)) {
+#pragma unroll
+                    for (int d = 1; d < R / 4; d *= 2)
+                        m = fmaxf(m, __shfl_xor(m, d));
+                    inv = m >= kLarge ? 0x1p-100f : 1.0f;
+                    unit = m >= kLarge ? 0x1p100f : 1.0f;
+                }
+                units[row] = unit;
             }
             uint8_t *dst = h_rows + row * kHRow;
             if constexpr (kSplit) {
@@ -888,8 +927,29 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
                         acc[f] = mma(b, w[f][kb], acc[f]);
                 }
             }
+            if constexpr (kLook) {
+                bool nan = false;
+#pragma unroll
+                for (int f = 0; f < N; f++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        nan = nan || acc[f][i] != acc[f][i];
+                if (__ballot(nan)) {
+#pragma unroll
+                    for (int f = 0; f < N; f++) {
+                        __builtin_amdgcn_sched_barrier(0);  // one at a time: few registers
+                        f32x4 alone = {};
+#pragma unroll
+                        for (int kb = 0; kb < KB; kb++)
+                            alone = mma(load_frag(reinterpret_cast<const T *>(h + 64 * kb + 16 * g)), w[f][kb], alone);
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            acc[f][i] = acc[f][i] != acc[f][i] ? alone[i] : acc[f][i];
+                    }
+                }
+            }
             f32x4 unit = {1.0f, 1.0f, 1.0f, 1.0f};
-            if constexpr (kScaled)
+            if constexpr (kScaled || kLess)
                 unit = *reinterpret_cast<const f32x4 *>(units + c + 4 * g);
 #pragma unroll
             for (int i = 0; i < 4; i++)
