@@ -862,12 +862,15 @@ __global__ __launch_bounds__(kUpThreads, sizeof(T) == 2 && R <= 64 ? 4 : 2) void
                 v[j] = part + j < p.rank ? v[j] * scale : 0.0f;
             float inv = 1.0f;
             if constexpr (kScaled) {
-                // f16 has no room for any h: the row's largest is taken to [0.5, 1)
-                float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+                // f16 has no room for any h: the row's largest finite one is taken to [0.5, 1)
+                float m = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    m = fmaxf(m, fabsf(v[j]) < __builtin_inff() ? fabsf(v[j]) : 0.0f);
 #pragma unroll
                 for (int d = 1; d < R / 4; d *= 2)
                     m = fmaxf(m, __shfl_xor(m, d));
-                const int e = m > 0.0f && m < __builtin_inff() ? min(max(__builtin_amdgcn_frexp_expf(m), -100), 126) : 0;
+                const int e = m > 0.0f ? min(max(__builtin_amdgcn_frexp_expf(m), -100), 126) : 0;
                 inv = ldexpf(1.0f, -e);
                 units[row] = ldexpf(1.0f, e);
             }

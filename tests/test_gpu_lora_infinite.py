@@ -93,3 +93,15 @@ def test_products_beyond_float32(rank, large, weight):
     h = c["x"].double() @ c["a"][0].double().t()
     assert (h[:, [1, 3]].abs() > 0.01 * large).all()
     assert torch.isinf(compare(c)[:, [11, 65]]).all()
+
+
+def test_infinite_h_beside_large_ones_in_f16():
+    """Beyond f16's own range, in a row that has an infinite one."""
+    for rank in (8, 20):
+        c = inputs(40, 64, 50, rank, 1, "f16", none=0.0)
+        c["x"] = (c["x"].float() * 2000).half()
+        c["a"] = (c["a"].float() * 300).half()
+        c["b"] = (c["b"].float() * 2.0 ** -16).half()
+        c["a"][0, 3, 5] = math.inf
+        assert (c["x"][:, 5] != 0).all()
+        assert torch.equal(torch.isinf(compare(c)), (c["b"][0, :, 3] != 0).expand(40, 50))
