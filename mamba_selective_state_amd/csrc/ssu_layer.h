@@ -109,12 +109,13 @@ struct ReorderParams {
     const void *slots, *parents;
     void *out;
     int64_t slots_b, slots_s, parents_b, parents_s, out_b;
-    int64_t batch, piece;  // bytes of a slot that a workgroup copies; set by the launch
+    int64_t batch, piece;  // bytes of a slot that a workgroup copies; set by plan_reorder
     int32_t beams, count;
     int32_t slots_i64, parents_i64, out_i64;
-    int32_t first_piece[kReorderPools + 1];  // set by the launch
+    int32_t first_piece[kReorderPools + 1];  // set by plan_reorder
     ReorderPool pool[kReorderPools];
 };
+int plan_reorder(ReorderParams &p);  // 0, or kTooManyWorkItems
 int launch_reorder(const ReorderParams &p, void *stream);
 
 }  // namespace ssu

@@ -616,19 +616,24 @@ ssu_status_t ssu_reorder_states(const ssu_tensor_t *pools, int32_t count, const 
         *to = {static_cast<uint8_t *>(const_cast<void *>(t.data)), t.stride[0] * b, elements * b, t.size[0]};
         return SSU_OK;
     };
-    for (int32_t i = 0; i < count; i++)  // all are looked at before anything is enqueued
+    for (int32_t i = 0; i < count; i++)
         if (ssu_status_t st = describe(i, &p.pool[0]))
             return st;
     if (batch == 0)
         return done(0);
-    for (int32_t at = 0; at == 0 || at < count; at += ssu::kReorderPools) {
-        p.count = count - at < ssu::kReorderPools ? count - at : ssu::kReorderPools;
-        for (int32_t i = 0; i < p.count; i++)
-            if (ssu_status_t st = describe(at + i, &p.pool[i]))
-                return st;
-        if (const int hip = ssu::launch_reorder(p, stream))
-            return done(hip);
-    }
+    // the launches, kReorderPools pools each: all are looked at before the first one is enqueued
+    for (const bool go : {false, true})
+        for (int32_t at = 0; at == 0 || at < count; at += ssu::kReorderPools) {
+            p.count = count - at < ssu::kReorderPools ? count - at : ssu::kReorderPools;
+            for (int32_t i = 0; i < p.count; i++)
+                if (ssu_status_t st = describe(at + i, &p.pool[i]))
+                    return st;
+            int hip = ssu::plan_reorder(p);
+            if (hip == 0 && go)
+                hip = ssu::launch_reorder(p, stream);
+            if (hip != 0)
+                return done(hip);
+        }
     return done(0);
 }
 

@@ -10,8 +10,11 @@
 namespace ssu {
 namespace {
 
+// Whether one launch takes them.
+inline bool groups_fit(int64_t groups, int threads) { return groups <= static_cast<int64_t>(UINT32_MAX) / threads; }
+
 inline int launch_groups(const void *fn, int64_t groups, int threads, void **args, void *stream, unsigned lds_bytes = 0) {
-    if (groups > static_cast<int64_t>(UINT32_MAX) / threads)
+    if (!groups_fit(groups, threads))
         return kTooManyWorkItems;
     return static_cast<int>(hipLaunchKernel(fn, dim3(static_cast<unsigned>(groups)), dim3(static_cast<unsigned>(threads)), args, lds_bytes,
                                             static_cast<hipStream_t>(stream)));

@@ -100,8 +100,7 @@ __global__ __launch_bounds__(kReorderThreads) void reorder_kernel(const ReorderP
 
 }  // namespace
 
-int launch_reorder(const ReorderParams &params, void *stream) {
-    ReorderParams p = params;
+int plan_reorder(ReorderParams &p) {
     p.piece = kReorderRound;
     int64_t pieces = 0;
     for (int i = 0; i < p.count; i++) {
@@ -112,8 +111,13 @@ int launch_reorder(const ReorderParams &params, void *stream) {
     }
     pieces = std::max<int64_t>(pieces, 1);  // the slots are written all the same
     p.first_piece[p.count] = static_cast<int32_t>(pieces);
+    return groups_fit(p.batch * pieces, kReorderThreads) ? 0 : kTooManyWorkItems;
+}
+
+int launch_reorder(const ReorderParams &params, void *stream) {
+    ReorderParams p = params;
     void *args[] = {&p};
-    return launch_groups(reinterpret_cast<const void *>(&reorder_kernel), p.batch * pieces, kReorderThreads, args, stream);
+    return launch_groups(reinterpret_cast<const void *>(&reorder_kernel), p.batch * p.first_piece[p.count], kReorderThreads, args, stream);
 }
 
 }  // namespace ssu
