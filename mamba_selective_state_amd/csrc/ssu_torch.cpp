@@ -386,6 +386,8 @@ PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const c10::DeviceGuard guard(dev);
         if (keep < 0)
             raise(PyExc_ValueError, "keep must not be negative");
+        if (keep > SSU_TOP_MAX)  // before outputs of that size are made
+            raise(PyExc_NotImplementedError, "ssu_beam_select: keep must be at most " + std::to_string(SSU_TOP_MAX));
         if (end_token < INT32_MIN || end_token > INT32_MAX)
             raise(PyExc_ValueError, "end_token must lie in the vocabulary");
         ssu_beam_args_t args = {};
