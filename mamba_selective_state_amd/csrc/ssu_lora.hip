@@ -392,19 +392,22 @@ __device__ __forceinline__ void down_tile(const LoraParams &p, int adapter, int 
     }
 }
 
-// SELF: a workgroup for each (adapter or leading row, slice of k, part of its rows) looks its rows up, the first workgroup makes
-// the plan. XF: operands of 16 rows at a time.
+// SELF: the workgroups look their rows up for themselves, one pass of up to 16 XF rows of an adapter each, and the first one makes the
+// plan. Three waves are enough for eight rows of weights in flight: held to registers for four, 256 rows of 64 adapters, 8192 -> 4096, rank 128, took
+// 87.5 us instead of 79.5.
 template <typename T, typename SRC, int RF, int XF, bool SELF>
-__global__ __launch_bounds__(kDownThreads) void lora_down_kernel(const LoraParams p, const LoraPlan plan) {
+__global__ __launch_bounds__(kDownThreads) __attribute__((amdgpu_waves_per_eu(RF == 8 ? 2 : 1, RF == 8 ? 3 : 8))) void lora_down_kernel(const LoraParams p, const LoraPlan plan) {
     extern __shared__ int dynamic[];
     __shared__ f32x4 sums[kDownWaves * 4 * 64];
-    constexpr int kScan = (kSelfRows + kDownThreads - 1) / kDownThreads;
-    __shared__ int mine[SELF ? kSelfRows : 1];
-    __shared__ int counts[SELF ? kScan * kDownWaves : 1];
+    constexpr int kSelfWaves = SELF ? kSelfRows / kWaveLanes : 1;
+    static_assert(kSelfRows <= kDownThreads && kSelfRows % kWaveLanes == 0, "a row for each thread");
+    __shared__ alignas(16) int rows[SELF ? kSelfRows : 1];
+    __shared__ int counts[SELF ? kDownWaves : 1];
+    __shared__ int found, found_skip;
     int id = static_cast<int>(blockIdx.x);
     if constexpr (SELF) {
         if (id == 0) {
-            make_plan<kDownThreads, kScan>(p, plan, dynamic);
+            make_plan<kDownThreads, 1>(p, plan, dynamic);
             return;
         }
         id--;
@@ -413,58 +416,82 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(const LoraParam
     const int begin = slice * p.slice, end = min(p.k, begin + p.slice);
     float *h = plan.h + static_cast<int64_t>(slice) * p.rows * (RF * 16);
     if constexpr (SELF) {
-        const int lane = threadIdx.x % kWaveLanes, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
-        int adapter = id / p.slices / p.parts, from = 0;
-        const int part = id / p.slices % p.parts;
-        if (p.rows < p.adapters) {  // the row's adapter, if no row before it has it
-            from = adapter;
-            adapter = adapter_of(p, from);
+        constexpr int kPass = 16 * XF;
+        const int t = threadIdx.x, lane = t % kWaveLanes, wave = __builtin_amdgcn_readfirstlane(t / kWaveLanes);
+        const int group = id / p.slices, heads = min(p.rows, p.adapters) * p.parts;
+        // thread t has row t
+        const int id_here = t < p.rows ? adapter_of(p, t) : -1;
+        // The pass: from the `skip`-th of the adapter's rows on.
+        int adapter = group / p.parts, skip = group % p.parts * kPass, from = -1;
+        if (group >= heads) {
+            // the passes that are left, in the adapters' order
+            for (int i = t; i < p.adapters; i += kDownThreads)
+                dynamic[i] = 0;
+            if (t == 0)
+                found = -1;
+            __syncthreads();
+            draw_number(dynamic, id_here, lane);
+            __syncthreads();
+            auto passes = [&](int i) { return max(0, (dynamic[i] + kPass - 1) / kPass - p.parts); };
+            const int per = (p.adapters + kDownThreads - 1) / kDownThreads;
+            const int first = min(t * per, p.adapters), last = min(first + per, p.adapters);
+            int own = 0;
+            for (int i = first; i < last; i++)
+                own += passes(i);
+            int at = own;
+#pragma unroll
+            for (int d = 1; d < kWaveLanes; d *= 2) {
+                const int o = __shfl_up(at, d);
+                at += lane >= d ? o : 0;
+            }
+            if (lane == kWaveLanes - 1)
+                counts[wave] = at;
+            at -= own;
+            __syncthreads();
+            for (int w = 0; w < wave; w++)
+                at += counts[w];
+            int left = group - heads - at;
+            if (left >= 0 && left < own) {
+                int i = first;
+                for (; left >= passes(i); i++)
+                    left -= passes(i);
+                found = i;
+                found_skip = (p.parts + left) * kPass;
+            }
+            __syncthreads();
+            adapter = __builtin_amdgcn_readfirstlane(found), skip = __builtin_amdgcn_readfirstlane(found_skip);
+            if (adapter < 0)
+                return;
+        } else if (p.rows < p.adapters) {
+            from = group;
+            adapter = __builtin_amdgcn_readfirstlane(adapter_of(p, from));
             if (adapter < 0)
                 return;
         }
-        int64_t ids[kScan];
-        if (p.ids_i64) {
-#pragma unroll
-            for (int u = 0; u < kScan; u++)
-                ids[u] = static_cast<const int64_t *>(p.ids)[min(u * kDownThreads + static_cast<int>(threadIdx.x), p.rows - 1) * p.ids_s];
-        } else {
-#pragma unroll
-            for (int u = 0; u < kScan; u++)
-                ids[u] = static_cast<const int32_t *>(p.ids)[min(u * kDownThreads + static_cast<int>(threadIdx.x), p.rows - 1) * p.ids_s];
-        }
-        // the rows in their own order, the same for every part
-        bool earlier = false;
-        uint64_t which[kScan];
-#pragma unroll
-        for (int u = 0; u < kScan; u++) {
-            const int row = u * kDownThreads + threadIdx.x;
-            const bool is = row < p.rows && ids[u] == adapter;
-            earlier = earlier || (is && row < from);
-            which[u] = __ballot(is);
-            if (lane == 0)
-                counts[u * kDownWaves + wave] = __popcll(which[u]);
-        }
-        if (__syncthreads_or(earlier))
-            return;
-        // rows before each of the waves' accesses, in the lanes
-        static_assert(kScan * kDownWaves <= kWaveLanes, "one for each lane");
-        const int own = lane < kScan * kDownWaves ? counts[lane] : 0;
-        int upto = own;
-#pragma unroll
-        for (int d = 1; d < kScan * kDownWaves; d *= 2) {
-            const int o = __shfl_up(upto, d);
-            upto += lane >= d ? o : 0;
-        }
-        const int n = __builtin_amdgcn_readlane(upto, kScan * kDownWaves - 1);
-#pragma unroll
-        for (int u = 0; u < kScan; u++) {
-            const int first = __builtin_amdgcn_readlane(upto - own, u * kDownWaves + wave);
-            if ((which[u] >> lane) & 1)
-                mine[first + __popcll(which[u] & ((1ull << lane) - 1))] = u * kDownThreads + threadIdx.x;
-        }
+        // the adapter's rows in their own order, the same for every pass
+        const uint64_t which = __ballot(id_here == adapter);
+        if (lane == 0)
+            counts[wave] = __popcll(which);
         __syncthreads();
-        for (int i = part * 16 * XF; i < n; i += p.parts * 16 * XF)
-            down_tile<T, SRC, RF, XF>(p, adapter, min(16 * XF, n - i), begin, end, h, sums, [&](int j) { return mine[i + j]; });
+        int at = __popcll(which & ((1ull << lane) - 1)), n = 0;
+#pragma unroll
+        for (int w = 0; w < kSelfWaves; w++) {
+            at += w < wave ? counts[w] : 0;
+            n += counts[w];
+        }
+        n = __builtin_amdgcn_readfirstlane(n);
+        if (id_here == adapter)
+            rows[at] = t;
+        if (t == from)
+            found_skip = at;
+        __syncthreads();
+        if (from >= 0) {
+            skip = __builtin_amdgcn_readfirstlane(found_skip);
+            if (skip % kPass != 0)
+                return;
+        }
+        if (skip < n)
+            down_tile<T, SRC, RF, XF>(p, adapter, min(kPass, n - skip), begin, end, h, sums, [&](int j) { return rows[skip + j]; });
     } else {
         const int tile = id / p.slices;
         if (tile >= plan.counts[1])
@@ -1159,13 +1186,15 @@ int launch_add_lora(const LoraParams &params, int dtype, int format, void *strea
     const unsigned counters = static_cast<unsigned>(p.adapters) * 4;
     void *args[] = {&p, &plan};
     if (p.rows <= kSelfRows) {
-        // An adapter's rows go to several workgroups if even shares are more than one pass of 32. A workgroup that has none costs its
-        // scan: 2048 rows of 64 adapters took 12.3 us in one part each, in four 18; 777 of 13 9 us, in four parts 5.5.
-        const int64_t each = std::min<int64_t>(p.rows, p.adapters);
-        p.parts = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(kMostParts, p.rows / (each * 24))));
-        const int64_t groups = 1 + each * p.slices * p.parts;
-        // more than 16 rows for each adapter, if they are spread evenly: 32 at a time
-        const void *down = p.rows > 16 * each ? down_fn<2, true>(dtype, format, rank) : down_fn<1, true>(dtype, format, rank);
+        // A workgroup takes one pass: the first of an adapter's, or the one that a row begins where rows are fewer than adapters. Were rows
+        // spread evenly, an adapter would have rows / adapters, 32 at a time if those are more than 16; workgroups for as many passes know theirs
+        // at once. For more, however the rows are spread, further ones look through all of them. (An adapter's workgroup that took pass
+        // after pass needed 68 us for 256 rows of one adapter among 64, 8192 -> 4096, rank 16, and 233 among 512.)
+        const int64_t heads = std::min<int64_t>(p.rows, p.adapters), pass = p.rows > 16 * heads ? 32 : 16;
+        const void *down = pass > 16 ? down_fn<2, true>(dtype, format, rank) : down_fn<1, true>(dtype, format, rank);
+        p.parts = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(kMostParts, p.rows / (heads * 24))));
+        const int64_t more = p.rows < p.adapters ? 0 : std::max<int64_t>(0, (p.rows - 1) / pass - (p.parts - 1));
+        const int64_t groups = 1 + (heads * p.parts + more) * p.slices;
         if (int hip = launch_groups(down, groups, kDownThreads, args, stream, counters))
             return hip;
     } else {

@@ -1,0 +1,84 @@
+"""add_lora where rows are spread unevenly over the adapters, up to 256 of them and a few more: one adapter's prompt among
+many adapters, one with most rows beside others with few, none at all."""
+import statistics
+
+import pytest
+import torch
+
+import mamba_selective_state_amd as ssu
+from test_gpu_lora import check, inputs, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    torch.cuda.init()
+
+
+def spread(rows, adapters, kind, seed):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "one":
+        return torch.full((rows,), adapters // 2, dtype=torch.int32)
+    if kind == "most":  # in any order, some rows without one
+        ids = torch.where(torch.rand(rows, generator=g) < 0.7, adapters - 1, torch.randint(-1, adapters, (rows,), generator=g))
+    elif kind == "pairs":
+        ids = torch.randint(0, 2, (rows,), generator=g) * (adapters - 1)
+    else:  # first
+        ids = torch.where(torch.arange(rows) < rows * 3 // 5, 0, torch.arange(rows) % adapters)
+    return ids.to(torch.int32)
+
+
+@pytest.mark.parametrize("kind", ["one", "most", "pairs", "first"])
+@pytest.mark.parametrize("rows,adapters", [(17, 2), (33, 40), (64, 5), (100, 100), (200, 16), (255, 300), (256, 1), (256, 7), (256, 64), (256, 4096), (257, 64)])
+def test_spreads(rows, adapters, kind):
+    c = inputs(rows, 200, 72, 8, adapters, "bf16", seed=rows + adapters)
+    c["adapter"] = spread(rows, adapters, kind, rows)
+    check(run(c), c)
+
+
+@pytest.mark.parametrize("dt,rank", [("f32", 16), ("f16", 33), ("bf16", 128)])
+def test_types_and_ranks(dt, rank):
+    c = inputs(250, 1100, 40, rank, 70, dt, seed=rank)
+    c["adapter"] = spread(250, 70, "most", 1)
+    check(run(c), c)
+
+
+def test_no_adapter_at_all():
+    for rows, adapters in ((256, 3), (40, 100)):
+        c = inputs(rows, 64, 40, 8, adapters, "bf16")
+        c["adapter"][:] = -1
+        check(run(c), c)
+
+
+def microseconds(f):
+    for _ in range(5):
+        f()
+    found = []
+    for _ in range(15):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(10):
+            f()
+        b.record()
+        b.synchronize()
+        found.append(100 * a.elapsed_time(b))
+    return statistics.median(found)
+
+
+@pytest.mark.parametrize("rank", [16, 128])
+def test_adapters_that_nothing_uses_cost_little(rank):
+    """One request's 256 rows take as long with 512 adapters in the table as with one, but for the search for rows: not three
+    times as long. (A workgroup that took all rows of its adapter needed 17 to 31 times as long.)"""
+    rows, k, n = 256, 8192, 1024
+    x, y = torch.randn(rows, k, device="cuda").bfloat16(), torch.randn(rows, n, device="cuda").bfloat16()
+    took = []
+    for adapters in (1, 64, 512):
+        a = torch.randn(adapters, rank, k, dtype=torch.bfloat16, device="cuda") / 90
+        b = torch.zeros(adapters, n, rank, dtype=torch.bfloat16, device="cuda")
+        ids = torch.full((rows,), adapters // 2, dtype=torch.int32, device="cuda")
+        took.append(microseconds(lambda: ssu.add_lora(y, x, a, b, ids)))
+    print("[gpu] add_lora, rank", rank, took, flush=True)
+    assert max(took) < 3 * took[0]
