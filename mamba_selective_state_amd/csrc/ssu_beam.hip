@@ -7,8 +7,8 @@
 // goes on, then the first `keep` of all lists.
 //
 // The logits' bytes bound it, and close behind them the instructions for them (an exponential takes a quarter of the lanes
-// at a time): 1601 live rows of 131072 bf16 (420 MB) take 86 us, 4.9 TB/s, 256 rows of 65536 (33 MB) 13, of which a third is the
-// end of the workgroups. The join takes 5 to 6 us. Beams at a score of -inf and ended ones are not read.
+// at a time): 1601 live rows of 131072 bf16 (420 MB) take 87 us, 4.8 TB/s, 256 rows of 65536 (33 MB) 14, of which a third is the
+// end of the workgroups. The join takes 5 to 6 us, of 64 beams 21. Beams at a score of -inf and ended ones are not read.
 #include <algorithm>
 
 #include "ssu_logits_device.h"
@@ -479,8 +479,8 @@ __global__ __launch_bounds__(kBeamThreads) void beam_join_kernel(const BeamParam
 }
 
 // Shares of a row and accesses per share: up to twice as many workgroups as the chip holds at once, of whole rounds of accesses; few
-// rows go to shares of one access for each wave. 256 rows of 65536 bf16: 13 us in four shares, 27 whole; 185 of 50021 f32 with a mask
-// 12.6 us in seven shares of a round, 14.2 in three; 2048 of 131072 bf16 94 in two, 100 whole, since every fourth row
+// rows go to shares of one access for each wave. 256 rows of 65536 bf16: 13 us in four shares, 16 in two, 21 whole; 185 of 50021 f32 with a mask
+// 13.3 us in seven shares of a round, 15.4 in three; 2048 of 131072 bf16 86 in two, 97 whole, since every fourth row
 // is not read and leaves its unit idle.
 constexpr int64_t kGroups = 4096, kFewGroups = 512;
 void split(int64_t rows, int64_t beams, int64_t vocab, int dtype, int32_t *segments, int32_t *per) {

@@ -4,12 +4,13 @@
 // Rows of one adapter are worked on together, so that each adapter's weights are read once for up to a tile of rows.
 // Which rows these are is found on the device: make_plan makes lists of tiles (an adapter and a run of `perm`).
 // Up to kSelfRows rows, the down kernel's workgroups look their rows up for themselves, and one more workgroup makes the
-// plan for the up kernel in the meantime: two launches. More rows: plan, down, up. 256 rows of 48 adapters (8192 -> 4096, rank
-// 16) take 7.2 + 6.0 us in two launches; at 512 rows of 4 adapters among 64 the two launches took 22 + 5.5 us, since a workgroup takes an
-// adapter's rows one pass after another, and three take 4.6 + 5 + 5.5.
+// plan for the up kernel in the meantime: two launches. More rows: plan, down, up, and the down kernel's operands go through LDS. 8192 -> 4096:
+// 256 rows of 64 adapters take 12.6 us at rank 16 and 49.5 at 128 in two launches, 257 18.0 and 50.5 in three; with one adapter
+// 13.5 and 32.3 in two, 16.8 and 26.5 in three.
 //
-// Bytes bound it, y's above all (read and written): 8192 rows, 4096 -> 18560, rank 64, bf16 8 + 21 + 144 us (608 MB of y at
-// 4.2 TB/s), 2048 rows of MXFP8, rank 16, 64 adapters 6 + 7 + 39 (152 MB of y, 46 MB of weights).
+// Bytes bound it, y's above all (read and written): 8192 rows, 4096 -> 18560, rank 64, bf16 8 + 22 + 144 us (608 MB of y at
+// 4.2 TB/s), 2048 rows of MXFP8, rank 16, 64 adapters 6 + 7 + 40 (152 MB of y, 46 MB of weights). f32, 2048 rows of rank 128:
+// 5 + 45 + 208 us for 12 GFLOP, which f32 matrix instructions do in 76 at best.
 //
 // Rows of other adapters never meet a weight, not even times zero: what one adapter's weights hold (NaN, infinity) stays with
 // its rows. h is f32 in the workspace; the up kernel splits 16-bit types' h into two summands of that type, hi + lo,
@@ -504,7 +505,7 @@ __global__ __launch_bounds__(kDownThreads) __attribute__((amdgpu_waves_per_eu(RF
 // ---------------------------------------------------------------- down, many rows
 //
 // Tiles of the plan, through LDS: a stage is 256 bytes (128 or, in f32, 64 values of k) of 32 rows of x and of all rank rows, which
-// LDS-DMA brings in whole lines, two stages ahead. 8192 x 4096 bf16 of rank 64 take 21 us (67 MB of x, part of it from the last-level cache, and A once for each 32 rows, 134 MB
+// LDS-DMA brings in whole lines, two stages ahead. 8192 x 4096 bf16 of rank 64 take 22 us (67 MB of x, part of it from the last-level cache, and A once for each 32 rows, 134 MB
 // from the L2s), 35 with x from HBM; with operands straight from memory, 64 bytes of 16 rows for each access, 50.
 //
 // Chunk c (16 bytes) of row r is at place c ^ r of its row, so that the 16 rows of an operand are read from different banks.
@@ -1071,7 +1072,9 @@ int64_t whole(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 constexpr int64_t kUpGroups = 8192;  // some times what the chip holds at once
 // Slices of k: enough workgroups for the chip, none with less than kLeastSlice values. Every item of the second product adds the
-// slices up: 256 rows of 64 adapters, 8192 -> 4096, take 7.3 + 5.8 us with four slices and 7.0 + 6.8 with eight.
+// slices up: 256 rows of 64 adapters, 8192 -> 4096, take 7.3 + 5.8 us with four slices and 7.0 + 6.8 with eight. How many of the adapters have
+// rows is not known here; the rule takes all that can. 512 rows of rank 128 with 512 adapters in the table: 193 us where 300 have rows, 62 where one
+// has; with no more than 64 of them counted 228 and 30. Rank 16: 43 and 27, 45 and 18.
 constexpr int64_t kLeastSlice = 512, kSelfGroups = 256, kDownGroups = 512, kMostSlices = 4;
 constexpr int64_t kMostParts = 8;
 void slices_of(int64_t rows, int64_t adapters, int64_t k, int32_t *slices, int32_t *slice) {
